@@ -62,7 +62,10 @@ typedef struct CUstream_st* dspark_stream_t;
 
 typedef enum {
   DSPARK_F32 = 0,  /* IEEE binary32                     */
-  DSPARK_BF16 = 1  /* bfloat16, passed as uint16 bits    */
+  DSPARK_BF16 = 1, /* bfloat16, passed as uint16 bits    */
+  DSPARK_F16 = 2,  /* IEEE binary16 (paged cache calls)  */
+  DSPARK_E4M3 = 3  /* 8-bit float, 4 exponent and 3 mantissa bits, largest
+                      value 448, no infinities (paged cache only) */
 } dspark_dtype;
 
 typedef enum {
@@ -74,8 +77,9 @@ typedef enum {
   DSPARK_ERR_BOUNDS = -5,      /* device: token, slot or row out of range  */
   DSPARK_ERR_WORKSPACE = -6,   /* workspace null or smaller than required  */
   DSPARK_ERR_ALIGNMENT = -7,   /* a pointer is not 16-byte aligned         */
-  DSPARK_ERR_SCRATCH_LIMIT = -8 /* sizes need more scratch than the fixed
+  DSPARK_ERR_SCRATCH_LIMIT = -8, /* sizes need more scratch than the fixed
                                    array of dspark_markov_sample_static    */
+  DSPARK_ERR_CACHE_FULL = -9   /* device: no free cache block for a request */
 } dspark_status;
 
 /* Statistics of one draft-logits cache row (one request, one draft step),
@@ -315,6 +319,161 @@ dspark_status dspark_noise(const uint64_t* seed, const int64_t* pos,
                            const uint32_t* col, const uint32_t* stream,
                            uint32_t* word, float* u, float* g, int64_t n,
                            dspark_stream_t stream_handle);
+
+/* ------------------------------------------------------------------------
+ * The paged key/value cache of the target model's verification pass.
+ *
+ * Between two drafting steps the target model runs the anchor token and the
+ * K drafts of every request over that request's cached keys and values, and
+ * the rejection sampler decides how many of them stay. The three calls below
+ * are the cache's part of that pass, all lengths on the device, so that a step
+ * follows from the last one's num_accepted without the host:
+ *   dspark_paged_tables     block tables, query offsets, positions, slot map
+ *   dspark_kv_append        the new keys and values into their pages
+ *   dspark_paged_attention  the new tokens' attention over the pages
+ * The pages of the drafter have no counterpart; the layouts are the ones that
+ * paged caches commonly have.
+ *
+ * A cache holds `num_blocks` blocks of `page_size` tokens for each of
+ * `kv_heads` heads, head_dim values to a token. The three strides (elements
+ * between blocks, between heads, between tokens) admit head-major pages,
+ * token-major pages and keys interleaved with values; the head_dim values are
+ * contiguous. A request slot s owns the first held_blocks[s] entries of row s
+ * of the block table; token position p of it lies in block
+ * block_table[s, p / page_size] at offset p % page_size, and its "slot" is
+ * block * page_size + offset.
+ * ------------------------------------------------------------------------ */
+#define DSPARK_MAX_PAGED_BATCH 1024
+
+typedef struct {
+  void* k;                  /* DEVICE memory, as every pointer below          */
+  void* v;
+  const float* k_scale;     /* [kv_heads] or NULL (= 1): a stored value x     */
+  const float* v_scale;     /*   stands for x * scale[head]                   */
+  int64_t k_block_stride, k_head_stride, k_token_stride; /* elements */
+  int64_t v_block_stride, v_head_stride, v_token_stride;
+  dspark_dtype dtype;       /* DSPARK_BF16, DSPARK_F16 or DSPARK_E4M3         */
+  int32_t num_blocks;       /* in [1, 2^30)                                   */
+  int32_t kv_heads;         /* in [1, 1024]                                   */
+  int32_t page_size;        /* 16, 32, 64, 128 or 256 tokens                  */
+  int32_t head_dim;         /* 64 or 128                                      */
+} dspark_paged_kv;          /* the struct itself is HOST memory */
+
+/* ------------------------------------------------------------------------
+ * dspark_paged_tables -- a step's block tables and slot map from the request
+ * lengths.
+ *
+ * For every request b (in order) with slot s = req_state_idx[b] >= 0:
+ *   cached = cached_lens[s] + (num_accepted ? num_accepted[b] + 1 : 0), stored
+ *     back: the tokens that the last step's verification kept (its anchor and
+ *     the accepted drafts); num_accepted[b] = -1 adds nothing;
+ *   seq_lens[b] = cached + new_lens[b];
+ *   need = ceil(seq_lens[b] / page_size) blocks.
+ *   A request that holds more returns the blocks of its last columns (their
+ *   table entries become -1); one that holds fewer takes new ones.
+ *   free_blocks[0 .. pool[0]) is a stack: first all returned blocks are pushed,
+ *   last request first and of each request the last column first, then the
+ *   new ones are popped in the order of the requests and their columns (so a
+ *   step taken back whole leaves the stack as it was).
+ *   query_start[b] = the new tokens of the requests before b;
+ *   token i of request b: positions[query_start[b] + i] = cached + i,
+ *   slot_map[...] = the slot of that position.
+ * query_start[B] = all new tokens; positions and slot_map from there to T are
+ * -1. Padding requests (slot < 0) have seq_lens 0 and no tokens.
+ * A request that cannot be served is treated as padding (its cached_lens,
+ * held blocks and table row stay as they are) and *status set: a slot, length
+ * or held count out of range, a need above M blocks, or new tokens past T (of
+ * the requests with new tokens the first that does not fit and all after it)
+ * give DSPARK_ERR_BOUNDS; new blocks that the stack does not have (the first
+ * that does not fit, and all after it that need any) DSPARK_ERR_CACHE_FULL.
+ *
+ * Arguments
+ *   req_state_idx [B] int32      slots, distinct, < 0 for padding
+ *   new_lens      [B] int32      tokens of this step, >= 0
+ *   cached_lens   [S] int32      tokens in the cache (updated with num_accepted)
+ *   num_accepted  [B] int32, or NULL
+ *   block_table   [S, M] int32   (updated)
+ *   held_blocks   [S] int32      (updated)
+ *   free_blocks   [N] int32      (updated; entries from pool[0] on are unspecified)
+ *   pool          [2] int32      pool[0] free blocks (updated); pool[1] is the
+ *                                call's own, 0 before the first call
+ *   query_start   [B+1] int32, seq_lens [B] int32,
+ *   positions     [T] int64, slot_map [T] int64   (written)
+ *   B in [0, 1024], S >= 1, M in [1, 2^20], N in [1, 2^30), T in [0, 2^30).
+ * ------------------------------------------------------------------------ */
+dspark_status dspark_paged_tables(
+    const int32_t* req_state_idx, const int32_t* new_lens, int32_t* cached_lens,
+    const int32_t* num_accepted, int32_t* block_table, int32_t* held_blocks,
+    int32_t* free_blocks, int32_t* pool, int32_t* query_start, int32_t* seq_lens,
+    int64_t* positions, int64_t* slot_map, int B, int S, int M, int N, int T,
+    int page_size, int32_t* status, dspark_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * dspark_kv_append -- keys and values of new tokens into their pages.
+ *
+ * For every token t with slot_map[t] >= 0 and every head h:
+ *   k_cache[slot / page_size, h, slot % page_size, :] = k[t, h, :]
+ * and the same for v; in an 8-bit cache round(k / k_scale[h]) (IEEE division,
+ * nearest even, clamped to +-448, NaN stays NaN). Tokens with a negative slot
+ * are skipped; a slot past the cache is skipped and gives DSPARK_ERR_BOUNDS.
+ *
+ * Arguments
+ *   k, v          [T, kv_heads, head_dim] dtype, tokens k_stride / v_stride
+ *                 elements apart (the heads of a token are contiguous)
+ *   dtype         DSPARK_BF16 or DSPARK_F16, the cache's unless that is 8-bit
+ *   slot_map      [T] int64; of two tokens with one slot either may win
+ *   T in [0, 2^30).
+ * Alignment: k, v, the caches and all strides (in bytes): 16.
+ * ------------------------------------------------------------------------ */
+dspark_status dspark_kv_append(const void* k, const void* v, dspark_dtype dtype,
+                               int64_t k_stride, int64_t v_stride,
+                               const dspark_paged_kv* cache,
+                               const int64_t* slot_map, int T, int32_t* status,
+                               dspark_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * dspark_paged_attention -- attention of a step's new tokens over the pages.
+ *
+ * Request b owns the query rows t = query_start[b] .. query_start[b+1] - 1;
+ * its n rows are the last n of its seq_lens[b] tokens, so row i has position
+ * P_i = seq_lens[b] - n + i. Query head hq reads the keys and values of head
+ * h = hq / (q_heads / kv_heads). Row i sees the key at position j if
+ *   0 <= j < seq_lens[b],  j <= P_i (causal),  j > P_i - window (window > 0):
+ *   x_j = scale * k_scale[h] * sum_d q[t, hq, d] k[j, h, d]       (fp32)
+ *   lse[t, hq] = log sum_j exp(x_j)
+ *   out[t, hq, :] = v_scale[h] * sum_j exp(x_j - lse) v[j, h, :]
+ * and what it does not see does not reach it, whatever the cache holds there.
+ * A row that sees nothing gives out 0 and lse -inf. Requests without tokens
+ * are skipped; rows of no request are not written. A slot or length out of
+ * range makes the request's rows see nothing, a page outside the cache reads
+ * as zeros; both give DSPARK_ERR_BOUNDS, and offsets that run backwards or past
+ * T leave the request's rows unwritten, with the same code.
+ *
+ * Arguments
+ *   q             [T, q_heads, head_dim] dtype, tokens q_stride elements apart
+ *   out           [T, q_heads, head_dim] dtype, contiguous
+ *   lse           [T, q_heads] fp32, or NULL
+ *   dtype         DSPARK_BF16 or DSPARK_F16, the cache's unless that is 8-bit
+ *   block_table   [S, M] int32
+ *   req_state_idx [B] int32 row of the block table, < 0: sees nothing
+ *   query_start   [B+1] int32, seq_lens [B] int32
+ *   q_heads       a multiple of kv_heads, at most 128 * kv_heads
+ *   causal 0 or 1; window >= 0, 0 = none; scale finite
+ *   B in [0, 1024], S >= 1, M in [1, 2^20], T in [0, 2^24).
+ *   workspace     at least dspark_paged_attention_workspace_bytes() bytes,
+ *                 256-byte aligned, no initial contents required.
+ * Alignment: q, out, the caches and all strides (in bytes): 16.
+ * ------------------------------------------------------------------------ */
+size_t dspark_paged_attention_workspace_bytes(int B, int q_heads, int kv_heads,
+                                              int head_dim);
+
+dspark_status dspark_paged_attention(
+    const void* q, dspark_dtype dtype, int64_t q_stride,
+    const dspark_paged_kv* cache, const int32_t* block_table,
+    const int32_t* req_state_idx, const int32_t* query_start,
+    const int32_t* seq_lens, void* out, float* lse, float scale, int causal,
+    int window, int q_heads, int B, int S, int M, int T, void* workspace,
+    size_t workspace_bytes, int32_t* status, dspark_stream_t stream);
 
 /* Human-readable name of a status code (static storage; never NULL). */
 const char* dspark_status_string(int status);

@@ -14,7 +14,9 @@ __all__ = ["build", "workloads"]
 
 def __getattr__(name):
     if name in ("markov_sample", "rejection_sample", "noise", "markov_workspace_bytes",
-                "verify_workspace_bytes", "status_string", "DsparkError", "lib"):
+                "verify_workspace_bytes", "status_string", "DsparkError", "lib",
+                "paged_tables", "kv_append", "paged_attention",
+                "paged_attention_workspace_bytes"):
         from . import _lib
         return getattr(_lib, name)
     raise AttributeError(name)

@@ -18,6 +18,8 @@ LIB_PATH = os.path.join(_PKG, "_build", "libdspark.so")
 
 DSPARK_F32 = 0
 DSPARK_BF16 = 1
+DSPARK_F16 = 2
+DSPARK_E4M3 = 3
 
 STATUS = {
     0: "DSPARK_OK",
@@ -29,6 +31,7 @@ STATUS = {
     -6: "DSPARK_ERR_WORKSPACE",
     -7: "DSPARK_ERR_ALIGNMENT",
     -8: "DSPARK_ERR_SCRATCH_LIMIT",
+    -9: "DSPARK_ERR_CACHE_FULL",
 }
 
 # Every symbol include/dspark.h and include/dspark_testing.h declare.
@@ -43,9 +46,22 @@ EXPORTS = (
     "dspark_verify_workspace_bytes",
     "dspark_rejection_sample",
     "dspark_noise",
+    "dspark_paged_tables",
+    "dspark_kv_append",
+    "dspark_paged_attention_workspace_bytes",
+    "dspark_paged_attention",
     "dspark_status_string",
     "dspark_version",
 )
+
+
+class PagedKv(ctypes.Structure):
+    """dspark_paged_kv (see include/dspark.h)."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")]
+                + [(f"{c}_{n}_stride", ctypes.c_int64) for c in "kv"
+                   for n in ("block", "head", "token")]
+                + [(n, ctypes.c_int32) for n in ("dtype", "num_blocks", "kv_heads", "page_size",
+                                                 "head_dim")])
 
 
 class DsparkError(RuntimeError):
@@ -99,6 +115,17 @@ def lib(path: str | None = None) -> ctypes.CDLL:
                                               vp, vp, i32, i32, i32, i32, i32, vp, sz, vp, vp]
         L.dspark_noise.restype = i32
         L.dspark_noise.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, vp]
+        kvp = ctypes.POINTER(PagedKv)
+        L.dspark_paged_tables.restype = i32
+        L.dspark_paged_tables.argtypes = [vp] * 12 + [i32] * 6 + [vp, vp]
+        L.dspark_kv_append.restype = i32
+        L.dspark_kv_append.argtypes = [vp, vp, i32, i64, i64, kvp, vp, i32, vp, vp]
+        L.dspark_paged_attention_workspace_bytes.restype = sz
+        L.dspark_paged_attention_workspace_bytes.argtypes = [i32] * 4
+        L.dspark_paged_attention.restype = i32
+        L.dspark_paged_attention.argtypes = [vp, i32, i64, kvp, vp, vp, vp, vp, vp, vp,
+                                             ctypes.c_float, i32, i32, i32, i32, i32, i32, i32,
+                                             vp, sz, vp, vp]
         L.dspark_status_string.restype = ctypes.c_char_p
         L.dspark_status_string.argtypes = [i32]
         L.dspark_version.restype = i32
@@ -428,3 +455,137 @@ def noise(seed, pos, col, stream_word, word=None, u=None, g=None, stream=None):
     code = lib().dspark_noise(_ptr(seed), _ptr(pos), _ptr(col), _ptr(stream_word),
                               _ptr(word), _ptr(u), _ptr(g), n, _stream(stream))
     _check(code, "dspark_noise")
+
+
+_PAGED_DTYPES = {torch.bfloat16: DSPARK_BF16, torch.float16: DSPARK_F16,
+                 torch.float8_e4m3fn: DSPARK_E4M3}
+
+
+def _of(t, name, dtype, shape=None):
+    """Address of a contiguous CUDA tensor of one dtype (and shape)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _maybe(t, name, dtype, shape=None):
+    return None if t is None else _of(t, name, dtype, shape)
+
+
+def _rows(t, name, heads=None):
+    """[T, H, D] rows whose tokens may be further apart than H * D (a view into
+    a fused projection): (address, dtype, elements between tokens)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype is not torch.bfloat16 and t.dtype is not torch.float16:
+        raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [T, heads, head_dim]")
+    T, H, D = t.shape
+    st, sh, sd = t.stride()
+    if (sd != 1 and D > 1) or (sh != D and H > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), _PAGED_DTYPES[t.dtype], H * D if T < 2 else st
+
+
+def _paged_kv(k_cache, v_cache, k_scale, v_scale):
+    """The dspark_paged_kv of caches [num_blocks, kv_heads, page_size, head_dim]
+    of any strides with contiguous head_dim."""
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.dtype not in _PAGED_DTYPES:
+            raise TypeError(f"{name} must be bfloat16, float16 or float8_e4m3fn, got {t.dtype}")
+        if t.dim() != 4 or t.stride(3) != 1:
+            raise ValueError(f"{name} must be [num_blocks, kv_heads, page_size, head_dim] with "
+                             "contiguous head_dim")
+    if k_cache.dtype != v_cache.dtype or k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache must have the same dtype and shape")
+    N, H, P, D = k_cache.shape
+    return PagedKv(k_cache.data_ptr(), v_cache.data_ptr(),
+                   _maybe(k_scale, "k_scale", torch.float32, (H,)),
+                   _maybe(v_scale, "v_scale", torch.float32, (H,)),
+                   *k_cache.stride()[:3], *v_cache.stride()[:3],
+                   _PAGED_DTYPES[k_cache.dtype], N, H, P, D)
+
+
+def paged_tables(req_state_idx, new_lens, cached_lens, block_table, held_blocks, free_blocks,
+                 pool, query_start, seq_lens, positions, slot_map, page_size, num_accepted=None,
+                 status=None, stream=None):
+    """dspark_paged_tables on torch tensors (see include/dspark.h): the step's
+    block tables, query offsets, positions and slot map from the request
+    lengths; updates cached_lens (with num_accepted), block_table,
+    held_blocks, free_blocks and pool."""
+    i32, i64 = torch.int32, torch.int64
+    B, (S, M) = req_state_idx.shape[0], block_table.shape
+    N, T = free_blocks.shape[0], slot_map.shape[0]
+    code = lib().dspark_paged_tables(
+        _of(req_state_idx, "req_state_idx", i32, (B,)), _of(new_lens, "new_lens", i32, (B,)),
+        _of(cached_lens, "cached_lens", i32, (S,)),
+        _maybe(num_accepted, "num_accepted", i32, (B,)),
+        _of(block_table, "block_table", i32), _of(held_blocks, "held_blocks", i32, (S,)),
+        _of(free_blocks, "free_blocks", i32, (N,)), _of(pool, "pool", i32, (2,)),
+        _of(query_start, "query_start", i32, (B + 1,)), _of(seq_lens, "seq_lens", i32, (B,)),
+        _of(positions, "positions", i64, (T,)), _of(slot_map, "slot_map", i64, (T,)),
+        B, S, M, N, T, page_size, _maybe(status, "status", i32), _stream(stream))
+    _check(code, "dspark_paged_tables")
+
+
+def kv_append(k, v, k_cache, v_cache, slot_map, k_scale=None, v_scale=None, status=None,
+              stream=None):
+    """dspark_kv_append on torch tensors (see include/dspark.h): rows k, v
+    [T, kv_heads, head_dim] (views of a fused projection will do) into the
+    caches [num_blocks, kv_heads, page_size, head_dim]."""
+    cache = _paged_kv(k_cache, v_cache, k_scale, v_scale)
+    T = slot_map.shape[0]
+    want = (T, cache.kv_heads, cache.head_dim)
+    kp, dt, ks = _rows(k, "k")
+    vp, vdt, vs = _rows(v, "v")
+    if k.shape != want or v.shape != want or dt != vdt:
+        raise ValueError(f"k and v must be {list(want)} of one dtype")
+    code = lib().dspark_kv_append(kp, vp, dt, ks, vs, cache,
+                                  _of(slot_map, "slot_map", torch.int64, (T,)), T,
+                                  _maybe(status, "status", torch.int32), _stream(stream))
+    _check(code, "dspark_kv_append")
+
+
+def paged_attention_workspace_bytes(B, q_heads, kv_heads, head_dim) -> int:
+    return int(lib().dspark_paged_attention_workspace_bytes(B, q_heads, kv_heads, head_dim))
+
+
+def paged_attention(q, k_cache, v_cache, block_table, req_state_idx, query_start, seq_lens, out,
+                    scale=None, causal=True, window=0, k_scale=None, v_scale=None, lse=None,
+                    workspace_buf=None, status=None, stream=None):
+    """dspark_paged_attention on torch tensors (see include/dspark.h): the
+    attention of rows q [T, q_heads, head_dim] (a view of a fused projection
+    will do) over the caches, into out and, if given, lse [T, q_heads]. scale
+    is 1 / sqrt(head_dim) if not given."""
+    cache = _paged_kv(k_cache, v_cache, k_scale, v_scale)
+    qp, dt, qs = _rows(q, "q")
+    T, Hq, D = q.shape
+    B, (S, M) = req_state_idx.shape[0], block_table.shape
+    if D != cache.head_dim:
+        raise ValueError("q and the caches must have the same head_dim")
+    if workspace_buf is None:
+        need = paged_attention_workspace_bytes(B, Hq, cache.kv_heads, D)
+        if stream is None:
+            workspace_buf = workspace(need, q.device)
+        else:  # memory of the stream that uses it
+            with torch.cuda.stream(stream):
+                workspace_buf = workspace(need, q.device)
+    i32 = torch.int32
+    code = lib().dspark_paged_attention(
+        qp, dt, qs, cache, _of(block_table, "block_table", i32),
+        _of(req_state_idx, "req_state_idx", i32, (B,)),
+        _of(query_start, "query_start", i32, (B + 1,)), _of(seq_lens, "seq_lens", i32, (B,)),
+        _of(out, "out", q.dtype, q.shape), _maybe(lse, "lse", torch.float32, (T, Hq)),
+        D ** -0.5 if scale is None else scale, bool(causal), window, Hq, B, S, M, T,
+        workspace_buf.data_ptr(), workspace_buf.numel() * workspace_buf.element_size(),
+        _maybe(status, "status", i32), _stream(stream))
+    _check(code, "dspark_paged_attention")

@@ -380,6 +380,8 @@ const char* dspark_status_string(int status) {
       return "pointer not 16-byte aligned";
     case DSPARK_ERR_SCRATCH_LIMIT:
       return "sizes need more scratch than the library's fixed array";
+    case DSPARK_ERR_CACHE_FULL:
+      return "no free block in the paged cache";
     default:
       return "unknown status";
   }
