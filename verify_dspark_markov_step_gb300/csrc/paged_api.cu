@@ -22,7 +22,7 @@ int page_shift_of(int page_size) {
 }
 
 bool stride_ok(int64_t elements, int elem_bytes) {
-  return elements >= 0 && elements < int64_t(1) << 38 && elements * elem_bytes % 16 == 0;
+  return elements > 0 && elements < int64_t(1) << 38 && elements * elem_bytes % 16 == 0;
 }
 
 // The checks both cache calls make of the cache's description. `dtype` is the
@@ -38,10 +38,12 @@ dspark_status check_cache(const dspark_paged_kv* c, int dtype) {
     return DSPARK_ERR_UNSUPPORTED;
   const int es = c->dtype == DSPARK_E4M3 ? 1 : 2;
   if (!aligned16(c->k) || !aligned16(c->v)) return DSPARK_ERR_ALIGNMENT;
-  const int64_t strides[] = {c->k_block_stride, c->k_head_stride, c->k_token_stride,
-                             c->v_block_stride, c->v_head_stride, c->v_token_stride};
-  for (const int64_t s : strides)
-    if (!stride_ok(s, es)) return DSPARK_ERR_ALIGNMENT;
+  if (!stride_ok(c->k_token_stride, es) || !stride_ok(c->v_token_stride, es))
+    return DSPARK_ERR_ALIGNMENT;
+  if (c->kv_heads > 1 && (!stride_ok(c->k_head_stride, es) || !stride_ok(c->v_head_stride, es)))
+    return DSPARK_ERR_ALIGNMENT;
+  if (c->num_blocks > 1 && (!stride_ok(c->k_block_stride, es) || !stride_ok(c->v_block_stride, es)))
+    return DSPARK_ERR_ALIGNMENT;
   return DSPARK_OK;
 }
 
@@ -171,7 +173,7 @@ dspark_status dspark_paged_attention(const void* q, dspark_dtype dtype, int64_t 
   p.lse = lse;
   p.scale = scale;
   p.causal = causal;
-  p.window = window;
+  p.window = window > 1 << 28 ? 0 : window;  // longer than any cache
   p.dtype = dtype;
   p.Hq = q_heads;
   p.B = B;

@@ -1,129 +1,1176 @@
-// paged_attention.cu -- attention of a step's new tokens over the paged cache.
+// paged_attention.cu -- attention of a step's new tokens over the paged cache,
+// on the 5th-generation tensor cores: one persistent launch, and a small one
+// that joins the requests whose keys were split over CTAs.
 //
-// The plainest form that is right for every case: one CTA per (token, query
-// head). Each warp takes every fourth key that the row sees, its lanes split
-// the head dimension, and the softmax runs along with one pass over the keys
-// (running maximum and sum in fp32); the four warps' partial results are
-// joined at the end.
+// Mathematics. For a query row, softmax(x) V over its visible keys in one pass
+// over tiles of 128 keys: with a reference r (a running maximum of the scaled
+// scores, in powers of two), p_j = 2^(x_j - r), l = sum p_j and O = sum p_j v_j
+// are kept; when the maximum grows, O and l are multiplied by
+// 2^(r_old - r_new). r is only moved when the maximum has grown by more than
+// 2^8 (p then stays below 2^8, exact in any of the types), so that O, which
+// lives in tensor memory, is hardly ever touched by the softmax. Scores, l and
+// O are fp32; the p_j are rounded to the MMA's 16-bit type (bf16 keeps its
+// range; fp16 gets 2^7 on top, so that a p 2^-31 below the maximum is still
+// nonzero), which costs as much accuracy as the output's own rounding.
+//
+// Rows. The query heads of a key head read the same keys, so a tile's 128 rows
+// are (token, head of the group) pairs: floor(128 / group) tokens. A unit of
+// work is two such row tiles of one request and key head ("pair": each of the
+// two softmax warpgroups owns a row tile, and every key tile is used twice), or
+// a single one ("single": the two warpgroups take key tiles in turn, and their
+// results are joined at the end). Either way the tensor core works on one
+// warpgroup's scores while the other's are being exponentiated.
+//
+// Split. Lengths live on the device and are ragged. Every CTA sums up the key
+// tiles of all units and takes an equal run of them, so a long request is
+// spread over many CTAs and short ones share a CTA, without the host and
+// without atomics. A unit that a run's ends cut is written as partial (O, r, l)
+// per CTA and joined by paged_join_kernel in a fixed order.
+//
+// Warps: 0-3 and 4-7 softmax (thread = row = lane of tensor memory), 8 TMA
+// producer, 9 MMA issuer; with an 8-bit cache 12-15 convert e4m3 tiles to fp16
+// in shared memory (the 8-bit values are exact in fp16; an 8-bit MMA would want
+// the queries and p in 8 bits too) and query rows are brought to fp16 by a
+// power of two per row. Pages: a 128-key tile is 128 / page_size TMA boxes.
+//
+// What a row does not see must not reach it: masked scores are replaced (not
+// added to), value rows past the request's last token are zeroed in shared
+// memory, and in tiles that some row sees only in part a non-finite value of a
+// key that is not seen by all moves that tile's P V off the tensor core (where
+// 0 * NaN would spread) onto a slow exact path.
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
 #include "common.cuh"
 #include "paged.h"
+#include "tc_ptx.cuh"
 
 namespace dspark {
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kRows = 128;   // rows of a tile (UMMA M, lanes of tensor memory)
+constexpr int kKeys = 128;   // keys of a tile
+constexpr int kMaxStages = 10;
+constexpr int kMaxRaw = 8;
+constexpr int kMaxCtas = 160;
+constexpr int kMinTiles = 2;  // key tiles a CTA takes at least
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kGrow = 8.0f;  // the reference moves when the maximum passes it by 2^8
 
-__device__ __forceinline__ float f16_bits_to_float(uint16_t h) {
-  float f;
-  asm("cvt.f32.f16 %0, %1;" : "=f"(f) : "h"(h));
-  return f;
+template <int D, bool kQuant>
+struct Cfg {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kTileBytes = kHalves * kRows * 128;  // 128 x D in 16 bits
+  static constexpr int kRawBytes = kKeys * D;               // 128 x D in 8 bits
+  static constexpr int kStages = kQuant ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 10);
+  static constexpr int kRaw = kQuant ? (D == 128 ? 3 : 6) : 0;
+  static constexpr int kThreads = kQuant ? 512 : 384;
+  // registers a thread after the split (the launch gives 128 or 168 to each)
+  static constexpr int kSoftmaxRegs = kQuant ? 192 : 216;
+  static constexpr int kOtherRegs = kQuant ? 64 : 72;
+  // shared memory, offsets from a 1024-byte aligned base
+  static constexpr int q = 0;
+  static constexpr int kv = q + 2 * kTileBytes;
+  static constexpr int raw = kv + kStages * kTileBytes;
+  static constexpr int misc = raw + kRaw * kRawBytes;
+  static constexpr int row_scale = misc + 2048;             // 8-bit cache: [2][kRows]
+  static constexpr int kBytes = row_scale + (kQuant ? 1024 : 0) + 1024;
+  static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
+};
+
+struct Misc {
+  uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
+  uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];
+  uint64_t s_full[2], p_ready[2], q_ready[2], o_full[2], scanned[2];
+  uint64_t merge, merged, drain;
+  uint32_t tmem;
+  int fail;
+  int bad[2];      // the last tile whose values were found non-finite, per warpgroup
+  int skip_pv[2];  // the last item whose P V the warpgroup did itself
+  int start_b, per;
+  long long start_rem, start_cost, pos, end;
+  unsigned long long warp_sum[17];
+  float2 x[kRows];  // r, l of the second warpgroup in a joined unit
+};
+static_assert(sizeof(Misc) <= 2048, "Misc fits its place");
+
+// One CTA's tail unit that others continue: what the join needs.
+struct JoinDesc {
+  int parts;   // 0: nothing to join
+  int token0;  // first query row (token) of the unit
+  int tokens;  // its tokens
+  int h;
+};
+
+struct Ws {
+  size_t desc, stats, o, total;
+  __host__ __device__ explicit Ws(int D) {
+    desc = 0;
+    stats = desc + kMaxCtas * sizeof(JoinDesc);
+    o = stats + size_t(kMaxCtas) * 2 * 2 * kRows * sizeof(float2);
+    total = o + size_t(kMaxCtas) * 2 * 2 * kRows * D * sizeof(float);
+  }
+};
+
+// ---- tensor memory ---------------------------------------------------------------
+#define DSPARK_R8(r, i) \
+  "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), \
+      "=r"(r[i + 6]), "=r"(r[i + 7])
+#define DSPARK_V8(r, i) \
+  "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), \
+      "r"(r[i + 6]), "r"(r[i + 7])
+// Each lane of the warp reads (writes) 32 consecutive 32-bit columns of its lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : DSPARK_R8(r, 0), DSPARK_R8(r, 8), DSPARK_R8(r, 16), DSPARK_R8(r, 24)
+      : "r"(a)
+      : "memory");
 }
-__device__ __forceinline__ uint16_t float_to_f16_bits(float f) {
-  uint16_t h;
-  asm("cvt.rn.f16.f32 %0, %1;" : "=h"(h) : "f"(f));
-  return h;
+__device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(a),
+      DSPARK_V8(r, 0), DSPARK_V8(r, 8), DSPARK_V8(r, 16), DSPARK_V8(r, 24)
+      : "memory");
 }
-__device__ __forceinline__ float e4m3_to_float(uint8_t b) {
-  uint32_t h;
-  asm("{ .reg .b16 x; cvt.u16.u32 x, %1; cvt.rn.f16x2.e4m3x2 %0, x; }"
-      : "=r"(h)
-      : "r"(static_cast<uint32_t>(b)));
-  return f16_bits_to_float(static_cast<uint16_t>(h & 0xFFFFu));
+__device__ __forceinline__ uint32_t tmem_ld1(uint32_t a) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(a) : "memory");
+  return r;
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ float load_value(const void* p, int dtype, int64_t i) {
-  if (dtype == DSPARK_E4M3) return e4m3_to_float(static_cast<const uint8_t*>(p)[i]);
-  const uint16_t h = static_cast<const uint16_t*>(p)[i];
-  return dtype == DSPARK_F16 ? f16_bits_to_float(h) : bf16_bits_to_float(h);
+// D[tmem] (+)= A * B^T, kind::f16, A from shared (ss) or tensor (ts) memory.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t acc) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t acc) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// Instruction descriptor: fp32 accumulator, both operands bf16 or fp16, A
+// K-major, B K-major or (b_mn) MN-major.
+__device__ constexpr uint32_t idesc_of(bool bf16, bool b_mn, int N) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(kRows >> 4) << 24);
+}
+// Descriptor of the values as the MN-major operand (N = head dimension, K =
+// keys): 128-byte swizzled rows of 64 values; the next 64 values of N one half
+// tile on (leading offset), the next 8 keys 1024 bytes on (stride offset).
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>((kKeys * 128) >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
 }
 
-template <int kDim>
-__global__ void __launch_bounds__(32 * kWarps) paged_attention_kernel(PagedAttentionParams P) {
-  constexpr int kPer = kDim / 32;
-  __shared__ float s_m[kWarps], s_l[kWarps], s_o[kWarps][kDim];
-  const int t = blockIdx.x, hq = blockIdx.y;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // the request of this token: the first whose range holds it
-  int b = -1, q0 = 0, q1 = 0;
-  for (int i = 0; i < P.B; ++i) {
-    const int a = P.query_start[i], e = P.query_start[i + 1];
-    if (a < 0 || e < a || e > P.T) {
-      if (threadIdx.x == 0) report(P.status, DSPARK_ERR_BOUNDS);
-      continue;
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z,
+                                            int w, uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar)),
+      "l"(policy)
+      : "memory");
+}
+
+// ---- small conversions -----------------------------------------------------------
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ void unpack_f16(uint32_t w, float& lo, float& hi) {
+  asm("{ .reg .b16 a, b; mov.b32 {a, b}, %2; cvt.f32.f16 %0, a; cvt.f32.f16 %1, b; }"
+      : "=f"(lo), "=f"(hi)
+      : "r"(w));
+}
+__device__ __forceinline__ void unpack_bf16(uint32_t w, float& lo, float& hi) {
+  lo = __uint_as_float(w << 16);
+  hi = __uint_as_float(w & 0xFFFF0000u);
+}
+// Two e4m3 values (low 16 bits of w, or high) as two fp16, exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
+  uint32_t r;
+  asm("{ .reg .b16 h; cvt.u16.u32 h, %1; cvt.rn.f16x2.e4m3x2 %0, h; }" : "=r"(r) : "r"(w));
+  return r;
+}
+
+// A wait that gives up after kWaitLimitNs or when another warp has.
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t phase, volatile int* fail,
+                                        int32_t* status) {
+  if (mbar_try_wait(bar, phase)) return true;
+  const unsigned long long t0 = globaltimer_ns();
+  for (;;) {
+    for (int i = 0; i < 8; ++i)
+      if (mbar_try_wait_sleep(bar, phase, 2000u)) return true;
+    if (*fail) return false;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      report(status, DSPARK_ERR_TIMEOUT);
+      *fail = 1;
+      return false;
     }
-    if (b < 0 && t >= a && t < e) {
-      b = i;
-      q0 = a;
-      q1 = e;
+  }
+}
+
+// The same for a whole warp, with one answer.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t phase, volatile int* fail,
+                                          int32_t* status) {
+  return __all_sync(0xFFFFFFFFu, wait_on(bar, phase, fail, status));
+}
+
+// ---- the units of work -------------------------------------------------------------
+struct Request {
+  int q0, n, slot, len;
+};
+
+__device__ __forceinline__ Request load_request(const PagedAttentionParams& P, int b, bool tell) {
+  Request r;
+  const int a = P.query_start[b], e = P.query_start[b + 1];
+  r.slot = P.rsi[b];
+  r.len = P.seq_lens[b];
+  r.q0 = a;
+  r.n = e - a;
+  bool bad = false;
+  if (a < 0 || e < a || e > P.T) {
+    r.n = 0;
+    bad = true;
+  }
+  if (r.slot < 0) {
+    r.len = 0;
+  } else if (r.slot >= P.S || r.len < 0 ||
+             static_cast<int64_t>(r.len) > (static_cast<int64_t>(P.M) << P.page_shift)) {
+    r.len = 0;
+    bad = true;
+  }
+  if (bad && tell) report(P.status, DSPARK_ERR_BOUNDS);
+  return r;
+}
+
+// Key range [lo, hi) that tokens t0 .. t1 - 1 of a request can see.
+__device__ __forceinline__ void key_range(const PagedAttentionParams& P, int n, int len, int t0,
+                                          int t1, int& lo, int& hi) {
+  const int at = len - n;
+  hi = P.causal ? min(len, at + t1) : len;
+  lo = P.window > 0 ? max(0, at + t0 - P.window + 1) : 0;
+  if (hi <= lo) lo = hi = 0;
+}
+
+// Key tiles of a unit; a unit whose rows see nothing still has one (empty) tile.
+__device__ __forceinline__ void unit_tiles(const PagedAttentionParams& P, const Request& r, int tp,
+                                           int u, int& jb, int& je) {
+  int lo, hi;
+  key_range(P, r.n, r.len, u * 2 * tp, min(r.n, (u + 1) * 2 * tp), lo, hi);
+  jb = lo / kKeys;
+  je = max(jb + 1, (hi + kKeys - 1) / kKeys);
+}
+
+// A run of key tiles of one unit.
+struct Seg {
+  Request r;
+  int h;
+  int t0, t1;   // tokens of the unit within the request
+  int j0, j1;   // key tiles
+  bool pair, opens, closes;  // two row tiles; starts / ends with the unit
+  int c1;       // the last CTA that works on the unit
+  __device__ int tiles() const { return j1 - j0; }
+  // items (key tiles) of warpgroup w and the k-th one's tile
+  __device__ int items(int w) const { return pair ? tiles() : (tiles() + 1 - w) / 2; }
+  __device__ int tile(int w, int k) const { return pair ? j0 + k : j0 + 2 * k + w; }
+  __device__ int ahead() const { return pair ? 1 : 2; }  // key tiles loaded before the first values
+  // place of a tile's keys / values in the order in which the segment loads them
+  __device__ int k_place(int j) const {
+    const int i = j - j0, a = ahead();
+    return i < a ? i : 2 * i - a + 1;
+  }
+  __device__ int v_place(int j) const {
+    const int i = j - j0;
+    return i + min(tiles(), ahead() + i);
+  }
+};
+
+// The segments of this CTA in order.
+struct Walk {
+  const PagedAttentionParams& P;
+  int tp, b, h, u, jb, je, j, per;
+  long long pos, end;
+  Request r;
+  __device__ Walk(const PagedAttentionParams& P_, const Misc* m, int tp_)
+      : P(P_), tp(tp_), b(m->start_b), h(0), u(0), per(m->per), pos(m->pos), end(m->end) {
+    if (pos >= end) return;
+    r = load_request(P, b, false);
+    long long rem = m->start_rem;
+    h = static_cast<int>(rem / m->start_cost);
+    rem -= h * m->start_cost;
+    for (;; ++u) {
+      unit_tiles(P, r, tp, u, jb, je);
+      if (rem < je - jb) break;
+      rem -= je - jb;
     }
+    j = jb + static_cast<int>(rem);
   }
-  if (b < 0) return;
-  const int slot = P.rsi[b];
-  int64_t len = P.seq_lens[b];
-  const int64_t most = static_cast<int64_t>(P.M) << P.page_shift;
-  if (slot < 0) {
-    len = 0;
-  } else if (slot >= P.S || len < 0 || len > most) {
-    if (threadIdx.x == 0) report(P.status, DSPARK_ERR_BOUNDS);
-    len = 0;
+  __device__ bool next(Seg& s) {
+    if (pos >= end) return false;
+    s.r = r;
+    s.h = h;
+    s.t0 = u * 2 * tp;
+    s.t1 = min(r.n, s.t0 + 2 * tp);
+    s.pair = s.t1 - s.t0 > tp;
+    s.j0 = j;
+    s.j1 = static_cast<int>(min(static_cast<long long>(je), j + (end - pos)));
+    s.opens = j == jb;
+    s.closes = s.j1 == je;
+    s.c1 = static_cast<int>((pos + (je - j) - 1) / per);
+    pos += s.j1 - s.j0;
+    j = s.j1;
+    if (j == je && pos < end) {
+      if (++u * 2 * tp >= r.n) {
+        u = 0;
+        if (++h == P.kv.kv_heads) {
+          h = 0;
+          do {
+            r = load_request(P, ++b, false);
+          } while (r.n == 0);
+        }
+      }
+      unit_tiles(P, r, tp, u, jb, je);
+      j = jb;
+    }
+    return true;
   }
-  const int64_t pos = len - (q1 - q0) + (t - q0);
-  int64_t j0 = 0, j1 = len;
-  if (P.causal && pos + 1 < j1) j1 = pos + 1;
-  if (P.window > 0 && pos - P.window + 1 > j0) j0 = pos - P.window + 1;
-  const int h = hq / (P.Hq / P.kv.kv_heads);
-  float q[kPer], o[kPer];
-  for (int i = 0; i < kPer; ++i) {
-    q[i] = load_value(P.q, P.dtype, static_cast<int64_t>(t) * P.q_stride + hq * kDim + lane + 32 * i);
-    o[i] = 0.f;
+};
+
+// Where this CTA's run starts: the key tiles of every request summed up (one
+// request per thread, long prompts by whole warps), `pre` as scratch.
+template <int kThreads>
+__device__ void make_plan(const PagedAttentionParams& P, Misc* m, unsigned long long* pre, int tp) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int nw = kThreads / 32;
+  const int B = P.B;
+  unsigned long long sum = 0;
+  // each thread takes `each` consecutive requests, so that a scan of the
+  // threads' sums gives the prefix
+  const int each = (B + kThreads - 1) / kThreads;
+  for (int i = 0; i < each; ++i) {
+    const int b = tid * each + i;
+    Request r;
+    r.n = 0;
+    if (b < B) r = load_request(P, b, blockIdx.x == 0);
+    const int units = (r.n + 2 * tp - 1) / (2 * tp);
+    unsigned long long cost = 0;
+    const bool big = units > 4;
+    if (!big)
+      for (int u = 0; u < units; ++u) {
+        int jb, je;
+        unit_tiles(P, r, tp, u, jb, je);
+        cost += je - jb;
+      }
+    unsigned int todo = __ballot_sync(0xFFFFFFFFu, big);
+    while (todo) {
+      const int src = __ffs(todo) - 1;
+      todo &= todo - 1;
+      Request o;
+      o.n = __shfl_sync(0xFFFFFFFFu, r.n, src);
+      o.len = __shfl_sync(0xFFFFFFFFu, r.len, src);
+      const int ou = (o.n + 2 * tp - 1) / (2 * tp);
+      unsigned long long c = 0;
+      for (int u = lane; u < ou; u += 32) {
+        int jb, je;
+        unit_tiles(P, o, tp, u, jb, je);
+        c += je - jb;
+      }
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) c += __shfl_xor_sync(0xFFFFFFFFu, c, s);
+      if (lane == src) cost = c;
+    }
+    cost *= P.kv.kv_heads;
+    sum += cost;
+    if (b < B) pre[b] = sum;  // within the thread
   }
-  const float sk = P.scale * (P.kv.k_scale ? P.kv.k_scale[h] : 1.f);
-  float m = -INFINITY, l = 0.f;
-  for (int64_t j = j0 + warp; j < j1; j += kWarps) {
-    const int id = P.block_table[static_cast<int64_t>(slot) * P.M + (j >> P.page_shift)];
-    const bool have = id >= 0 && id < P.kv.num_blocks;
-    if (!have && lane == 0) report(P.status, DSPARK_ERR_BOUNDS);
-    const int64_t off = j & ((1 << P.page_shift) - 1);
-    const int64_t ka = id * P.kv.k_block_stride + h * P.kv.k_head_stride + off * P.kv.k_token_stride;
-    const int64_t va = id * P.kv.v_block_stride + h * P.kv.v_head_stride + off * P.kv.v_token_stride;
-    float x = 0.f;
-    for (int i = 0; i < kPer; ++i)
-      if (have) x = fmaf(q[i], load_value(P.kv.k, P.kv.dtype, ka + lane + 32 * i), x);
-    for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, s);
-    x *= sk;
-    const float mn = fmaxf(m, x);
-    const float base = mn == -INFINITY ? 0.f : mn;
-    const float keep = expf(m - base), p = expf(x - base);
-    l = l * keep + p;
-    for (int i = 0; i < kPer; ++i)
-      o[i] = fmaf(p, have ? load_value(P.kv.v, P.kv.dtype, va + lane + 32 * i) : 0.f, o[i] * keep);
-    m = mn;
+  unsigned long long v = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    if (lane >= o) v += u;
   }
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
-  for (int i = 0; i < kPer; ++i) s_o[warp][lane + 32 * i] = o[i];
+  if (lane == 31) m->warp_sum[warp] = v;
   __syncthreads();
-  float mt = -INFINITY, lt = 0.f;
-  for (int w = 0; w < kWarps; ++w) mt = fmaxf(mt, s_m[w]);
-  const float base = mt == -INFINITY ? 0.f : mt;
-  for (int w = 0; w < kWarps; ++w) lt += s_l[w] * expf(s_m[w] - base);
-  const float vs = P.kv.v_scale ? P.kv.v_scale[h] : 1.f;
-  const int64_t row = static_cast<int64_t>(t) * P.Hq + hq;
-  for (int d = threadIdx.x; d < kDim; d += 32 * kWarps) {
-    float v = 0.f;
-    for (int w = 0; w < kWarps; ++w) v += s_o[w][d] * expf(s_m[w] - base);
-    v = j1 > j0 ? v / lt * vs : 0.f;
-    static_cast<uint16_t*>(P.out)[row * kDim + d] =
-        P.dtype == DSPARK_F16 ? float_to_f16_bits(v) : float_to_bf16_bits(v);
+  unsigned long long base = v - sum, total = 0;
+  for (int w = 0; w < nw; ++w) {
+    if (w < warp) base += m->warp_sum[w];
+    total += m->warp_sum[w];
   }
-  if (P.lse && threadIdx.x == 0) P.lse[row] = j1 > j0 ? base + logf(lt) : -INFINITY;
+  unsigned long long per = (total + gridDim.x - 1) / gridDim.x;
+  if (per < kMinTiles) per = kMinTiles;
+  const unsigned long long pos = per * blockIdx.x;
+  if (tid == 0) {
+    m->per = static_cast<int>(per > 0x7FFFFFFF ? 0x7FFFFFFF : per);
+    m->pos = static_cast<long long>(pos);
+    m->end = static_cast<long long>(pos + per < total ? pos + per : total);
+    m->start_b = 0;
+  }
+  __syncthreads();
+  for (int i = 0; i < each; ++i) {
+    const int b = tid * each + i;
+    if (b >= B) break;
+    const unsigned long long lo = base + (i ? pre[b - 1] : 0), hi = base + pre[b];
+    if (lo <= pos && pos < hi) {
+      m->start_b = b;
+      m->start_rem = static_cast<long long>(pos - lo);
+      m->start_cost = static_cast<long long>((hi - lo) / P.kv.kv_heads);
+    }
+  }
+}
+
+// ---- the kernel ----------------------------------------------------------------------
+// kF16: the MMA's type is fp16 (fp16 rows, or an 8-bit cache), else bf16.
+template <int D, bool kF16, bool kQuant>
+__global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
+paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_k,
+                       const __grid_constant__ CUtensorMap tmap_v, PagedAttentionParams P) {
+  using C = Cfg<D, kQuant>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  Misc* m = reinterpret_cast<Misc*>(smem + C::misc);
+  float* row_scale = reinterpret_cast<float*>(smem + C::row_scale);
+  volatile int* fail = &m->fail;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = P.Hq / P.kv.kv_heads;
+  const int tp = kRows / G;  // tokens of a row tile
+  const Ws ws(D);
+  unsigned char* wsp = static_cast<unsigned char*>(P.workspace);
+
+  if (tid == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&m->kv_full[i], kQuant ? 4 : 1);
+      mbar_init(&m->kv_empty[i], 1);
+    }
+    for (int i = 0; i < C::kRaw; ++i) {
+      mbar_init(&m->raw_full[i], 1);
+      mbar_init(&m->raw_empty[i], 4);
+    }
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&m->s_full[w], 1);
+      mbar_init(&m->p_ready[w], 4);
+      mbar_init(&m->q_ready[w], 4);
+      mbar_init(&m->o_full[w], 1);
+      mbar_init(&m->scanned[w], 4);
+      m->bad[w] = m->skip_pv[w] = -1;
+    }
+    mbar_init(&m->merge, 4);
+    mbar_init(&m->merged, 4);
+    mbar_init(&m->drain, 1);
+    m->fail = 0;
+    fence_mbar_init();
+    tc::prefetch_tensormap(&tmap_k);
+    tc::prefetch_tensormap(&tmap_v);
+  }
+  if (warp == 9) {
+    tc::tmem_alloc(&m->tmem, 512);
+    tc::tmem_relinquish();
+  }
+  make_plan<C::kThreads>(P, m, reinterpret_cast<unsigned long long*>(smem + C::kv), tp);
+  fence_proxy_async_smem();  // the plan's scratch is TMA's from here on
+  tc::fence_before_thread_sync();
+  __syncthreads();
+  tc::fence_after_thread_sync();
+  const uint32_t tmem = m->tmem;
+  Walk walk(P, m, tp);
+  Seg s;
+
+  if (warp < 8) {
+    // ---- softmax ------------------------------------------------------------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
+    const int w = warp >> 2, row = tid & 127;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_t = tmem + lanes + w * kKeys;         // scores, then p
+    const uint32_t o_t = tmem + lanes + 256 + w * 128;     // O
+    unsigned char* q_s = smem + C::q + w * C::kTileBytes;
+    constexpr float kOff = kF16 ? 7.0f : 0.0f;
+    uint32_t n_seg = 0, n_item = 0, n_scan = 0, n_merge = 0;
+    uint32_t base = 0;  // tiles loaded before this segment
+    bool tail_split = false;
+    const float sl0 = fminf(fmaxf(fabsf(P.scale) * kLog2e, 1e-37f), 3e38f);
+    const uint32_t flip = P.scale < 0.f ? 0x80008000u : 0u;
+    bool ok = true;
+    while (ok && walk.next(s)) {
+      const int items = s.items(w);
+      const bool split = !(s.opens && s.closes);
+      const int first = s.t0 + (s.pair ? w * tp : 0);       // first token of the row tile
+      const int ntok = min(tp, s.t1 - first);
+      const int nrow = ntok * G;
+      const bool live = row < nrow;
+      const bool warp_live = (warp & 3) * 32 < nrow;
+      const int tok = row / G;                               // token within the row tile
+      int lo, hi;
+      key_range(P, s.r.n, s.r.len, first + tok, first + tok + 1, lo, hi);
+      if (!live) lo = hi = 0;
+      // keys seen by every row of the tile
+      int all_lo, all_hi, unused;
+      key_range(P, s.r.n, s.r.len, first, first + 1, unused, all_hi);
+      key_range(P, s.r.n, s.r.len, first + ntok - 1, first + ntok, all_lo, unused);
+      float sl = sl0 * (P.kv.k_scale ? P.kv.k_scale[s.h] : 1.f);
+      float r = -INFINITY, l = 0.f;  // reference (scaled), sum
+      if (items > 0) {
+        // query rows into shared memory, K-major, 128-byte swizzle
+        const uint16_t* src = static_cast<const uint16_t*>(P.q);
+        for (int i = row; i < nrow * (D / 8); i += kRows) {
+          const int rr = i / (D / 8), c = i % (D / 8);
+          const int t = rr / G, g = rr - t * G;
+          uint4 x = __ldg(reinterpret_cast<const uint4*>(
+              src + static_cast<int64_t>(s.r.q0 + first + t) * P.q_stride +
+              static_cast<int64_t>(s.h * G + g) * D + c * 8));
+          x.x ^= flip;
+          x.y ^= flip;
+          x.z ^= flip;
+          x.w ^= flip;
+          if constexpr (kQuant) {
+            // to fp16 with the row's largest value brought to 2^14: exact but
+            // for values 2^-28 below it. D / 8 neighbouring lanes hold a row.
+            float f[8];
+            uint32_t* xw = &x.x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (P.dtype == DSPARK_F16)
+                unpack_f16(xw[e], f[2 * e], f[2 * e + 1]);
+              else
+                unpack_bf16(xw[e], f[2 * e], f[2 * e + 1]);
+            }
+            uint32_t big = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) big = max(big, __float_as_uint(f[e]) & 0x7FFFFFFFu);
+            const unsigned int who = ((1u << (D / 8)) - 1u) << (lane & ~(D / 8 - 1));
+#pragma unroll
+            for (int o = D / 16; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(who, big, o));
+            const int ex = big == 0u ? 14 : max(static_cast<int>(big >> 23) - 127, -112);
+            const float up = __uint_as_float(static_cast<uint32_t>(14 - ex + 127) << 23);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) xw[e] = pack_f16(f[2 * e] * up, f[2 * e + 1] * up);
+            if (c == 0)
+              row_scale[w * kRows + rr] = __uint_as_float(static_cast<uint32_t>(ex - 14 + 127) << 23);
+          }
+          *reinterpret_cast<uint4*>(q_s + (c >> 3) * (kRows * 128) + rr * 128 +
+                                    (((c & 7) ^ (rr & 7)) << 4)) = x;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&m->q_ready[w]);
+        if constexpr (kQuant) {
+          if (!(ok = wait_warp(&m->q_ready[w], n_seg & 1, fail, P.status))) break;
+          if (live) sl *= row_scale[w * kRows + row];
+        }
+      }
+      for (int k = 0; k < items; ++k, ++n_item) {
+        const int key0 = s.tile(w, k) * kKeys;
+        if (!(ok = wait_warp(&m->s_full[w], n_item & 1, fail, P.status))) break;
+        tc::fence_after_thread_sync();
+        bool scan = false, tail = false;
+        const bool masked = key0 < all_lo || key0 + kKeys > all_hi;
+        if (masked) {
+          // keys past the request's end in this tile, and others that some row
+          // does not see
+          tail = key0 + kKeys > s.r.len;
+          scan = key0 < all_lo || min(key0 + kKeys, s.r.len) > all_hi;
+        }
+        if (warp_live) {
+          uint32_t x[kKeys];
+          tmem_ld32(s_t, x);
+          tmem_ld32(s_t + 32, x + 32);
+          tmem_ld32(s_t + 64, x + 64);
+          tmem_ld32(s_t + 96, x + 96);
+          tc::tmem_wait_ld();
+          if (masked) {
+            const int clo = lo - key0, chi = hi - key0;
+#pragma unroll
+            for (int c = 0; c < kKeys; ++c)
+              if (c < clo || c >= chi) x[c] = 0xFF800000u;
+          }
+          float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < kKeys; c += 4) {
+            mx0 = fmaxf(mx0, fmaxf(__uint_as_float(x[c]), __uint_as_float(x[c + 1])));
+            mx1 = fmaxf(mx1, fmaxf(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])));
+          }
+          const float mx = fmaxf(mx0, mx1) * sl;
+          float keep = 1.f;
+          const bool move = mx > r + kGrow;  // also the first finite maximum
+          if (move) {
+            keep = ex2_approx(r - mx);  // 0 the first time
+            r = mx;
+          }
+          if (k > 0 && __any_sync(0xFFFFFFFFu, move)) {
+            l *= keep;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(o_t + c, o);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+              tmem_st32(o_t + c, o);
+            }
+          }
+          const float neg = kOff - (r == -INFINITY ? 0.f : r);
+          const unsigned long long sl2 = f2_pack(sl, sl), neg2 = f2_pack(neg, neg);
+          unsigned long long sum = 0ull, sum1 = 0ull;
+#pragma unroll
+          for (int c = 0; c < kKeys; c += 4) {
+            float a, b, e, f;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sl2, neg2),
+                      a, b);
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), sl2,
+                             neg2), e, f);
+            a = ex2_approx(a);
+            b = ex2_approx(b);
+            e = ex2_approx(e);
+            f = ex2_approx(f);
+            sum = f2_add(sum, f2_pack(a, b));
+            sum1 = f2_add(sum1, f2_pack(e, f));
+            x[c / 2] = kF16 ? pack_f16(a, b) : pack_bf16(a, b);
+            x[c / 2 + 1] = kF16 ? pack_f16(e, f) : pack_bf16(e, f);
+          }
+          float a, b;
+          f2_unpack(f2_add(sum, sum1), a, b);
+          l += a + b;
+          tmem_st32(s_t, x);
+          tmem_st32(s_t + 32, x + 32);
+          tmem_wait_st();
+        }
+        if (tail || scan) {
+          // the tile's values: rows past the end become zero; a non-finite one
+          // that some row does not see takes P V off the tensor core
+          const uint32_t vi = base + s.v_place(s.tile(w, k));
+          unsigned char* v_s = smem + C::kv + (vi % C::kStages) * C::kTileBytes;
+          if (!(ok = wait_warp(&m->kv_full[vi % C::kStages], (vi / C::kStages) & 1, fail, P.status)))
+            break;
+          const int key = key0 + row;
+          if (key >= s.r.len) {
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c)
+              *reinterpret_cast<uint4*>(v_s + (c >> 3) * (kKeys * 128) + row * 128 +
+                                        ((c & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+          } else if (scan && (key >= all_hi || key < all_lo)) {
+            constexpr uint32_t kInf = kF16 ? 0x7C00u : 0x7F80u;
+            bool bad = false;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+              const uint4 v = *reinterpret_cast<const uint4*>(
+                  v_s + (c >> 3) * (kKeys * 128) + row * 128 + ((c & 7) << 4));
+              const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                bad |= (vw[e] & kInf) == kInf || ((vw[e] >> 16) & kInf) == kInf;
+            }
+            if (bad) m->bad[w] = static_cast<int>(n_item);
+          }
+          fence_proxy_async_smem();
+          if (scan) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&m->scanned[w]);
+            if (!(ok = wait_warp(&m->scanned[w], n_scan & 1, fail, P.status))) break;
+            ++n_scan;
+            if (*reinterpret_cast<volatile int*>(&m->bad[w]) == static_cast<int>(n_item)) {
+              // O += P V of this tile by hand, over the keys each row sees
+              if (warp_live) {
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                  uint32_t o[32];
+                  if (k > 0) {
+                    tmem_ld32(o_t + c0, o);
+                    tc::tmem_wait_ld();
+                  } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0u;
+                  }
+#pragma unroll 1
+                  for (int c = 0; c < kKeys; ++c) {
+                    const uint32_t pw = tmem_ld1(s_t + (c >> 1));
+                    tc::tmem_wait_ld();
+                    float p0, p1;
+                    if (kF16)
+                      unpack_f16(pw, p0, p1);
+                    else
+                      unpack_bf16(pw, p0, p1);
+                    const float p = (c & 1) ? p1 : p0;
+                    const bool sees = key0 + c >= lo && key0 + c < hi;
+                    const unsigned char* vr =
+                        v_s + (c0 >> 6) * (kKeys * 128) + c * 128;
+#pragma unroll
+                    for (int q4 = 0; q4 < 4; ++q4) {
+                      const uint4 v = *reinterpret_cast<const uint4*>(
+                          vr + (((((c0 >> 3) & 7) + q4) ^ (c & 7)) << 4));
+                      const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                      for (int e = 0; e < 4; ++e) {
+                        float v0, v1;
+                        if (kF16)
+                          unpack_f16(vw[e], v0, v1);
+                        else
+                          unpack_bf16(vw[e], v0, v1);
+                        uint32_t& o0 = o[8 * q4 + 2 * e];
+                        uint32_t& o1 = o[8 * q4 + 2 * e + 1];
+                        if (sees) {
+                          o0 = __float_as_uint(fmaf(p, v0, __uint_as_float(o0)));
+                          o1 = __float_as_uint(fmaf(p, v1, __uint_as_float(o1)));
+                        }
+                      }
+                    }
+                  }
+                  tmem_st32(o_t + c0, o);
+                }
+                tmem_wait_st();
+              }
+              if (lane == 0) m->skip_pv[w] = static_cast<int>(n_item);
+            }
+          }
+        }
+        tc::fence_before_thread_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&m->p_ready[w]);
+      }
+      if (!ok) break;
+      base += 2 * s.tiles();
+      if (items > 0) {
+        if (!(ok = wait_warp(&m->o_full[w], n_seg & 1, fail, P.status))) break;
+        tc::fence_after_thread_sync();
+        ++n_seg;
+      }
+      // ---- the segment's result -----------------------------------------------------
+      const bool joined = !s.pair && s.items(1) > 0;
+      if (!s.pair && w == 1) {
+        if (joined) {  // the first warpgroup takes it from here
+          m->x[row] = make_float2(r, l);
+          tc::fence_before_thread_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&m->merge);
+          if (!(ok = wait_warp(&m->merged, n_merge & 1, fail, P.status))) break;
+          ++n_merge;
+        }
+        continue;
+      }
+      float keep0 = 1.f, keep1 = 0.f;
+      if (joined) {
+        if (!(ok = wait_warp(&m->merge, n_merge & 1, fail, P.status))) break;
+        tc::fence_after_thread_sync();
+        ++n_merge;
+        const float2 x1 = m->x[row];
+        const float rn = fmaxf(r, x1.x);
+        if (rn != -INFINITY) {
+          keep0 = ex2_approx(r - rn);
+          keep1 = ex2_approx(x1.x - rn);
+        }
+        l = l * keep0 + x1.y * keep1;
+        r = rn;
+      }
+      if (warp_live) {
+        const bool none = l == 0.f;
+        const float inv = none ? 0.f : (P.kv.v_scale ? P.kv.v_scale[s.h] : 1.f) / l;
+        const int64_t trow = static_cast<int64_t>(s.r.q0 + first + tok) * P.Hq + s.h * G +
+                             (row - tok * G);
+        const int slot = s.opens ? 1 : 0;
+        const int64_t prow = ((static_cast<int64_t>(blockIdx.x) * 2 + slot) * 2 +
+                              (s.pair ? w : 0)) * kRows + row;
+        float* po = reinterpret_cast<float*>(wsp + ws.o) + prow * D;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(o_t + c, o);
+          if (joined) {
+            uint32_t o1[32];
+            tmem_ld32(o_t + 128 + c, o1);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              o[e] = __float_as_uint(__uint_as_float(o[e]) * keep0 +
+                                     __uint_as_float(o1[e]) * keep1);
+          } else {
+            tc::tmem_wait_ld();
+          }
+          if (!live) {
+          } else if (split) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<uint4*>(po + c + e) =
+                  none ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          } else {
+            uint16_t* out = static_cast<uint16_t*>(P.out) + trow * D + c;
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              uint32_t y[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float a = none ? 0.f : __uint_as_float(o[e + 2 * i]) * inv;
+                const float b = none ? 0.f : __uint_as_float(o[e + 2 * i + 1]) * inv;
+                y[i] = P.dtype == DSPARK_F16 ? pack_f16(a, b) : pack_bf16(a, b);
+              }
+              *reinterpret_cast<uint4*>(out + e) = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+          }
+          __syncwarp();
+        }
+        if (live) {
+          if (split) {
+            reinterpret_cast<float2*>(wsp + ws.stats)[prow] = make_float2(r, l);
+          } else if (P.lse) {
+            P.lse[trow] = none ? -INFINITY : (r - kOff + lg2_approx(l)) * kLn2;
+          }
+        }
+      }
+      if (joined) {
+        tc::fence_before_thread_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&m->merged);
+      }
+      if (split && s.opens) {
+        tail_split = true;
+        if (tid == 0) {
+          JoinDesc d;
+          d.parts = s.c1 - static_cast<int>(blockIdx.x) + 1;
+          d.token0 = s.r.q0 + s.t0;
+          d.tokens = s.t1 - s.t0;
+          d.h = s.h;
+          reinterpret_cast<JoinDesc*>(wsp + ws.desc)[blockIdx.x] = d;
+        }
+      }
+    }
+    if (tid == 0 && (!tail_split || !ok))
+      reinterpret_cast<JoinDesc*>(wsp + ws.desc)[blockIdx.x].parts = 0;
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
+    if (warp == 8) {
+      // ---- TMA producer: keys and values of the segments' tiles, page by page --------
+      const uint64_t pol = policy_evict_normal();
+      constexpr int kRing = kQuant ? C::kRaw : C::kStages;
+      constexpr int kBytes = kQuant ? C::kRawBytes : C::kTileBytes;
+      uint64_t* full = kQuant ? m->raw_full : m->kv_full;
+      uint64_t* empty = kQuant ? m->raw_empty : m->kv_empty;
+      unsigned char* ring = smem + (kQuant ? C::raw : C::kv);
+      const int page = 1 << P.page_shift;
+      const int box = page < kKeys ? page : kKeys;  // tokens of a TMA box
+      const int boxes = kKeys / box;                // boxes of a tile (<= 8)
+      uint32_t n = 0;  // tiles loaded
+      bool ok = true;
+      while (ok && walk.next(s)) {
+        int lo, hi;
+        key_range(P, s.r.n, s.r.len, s.t0, s.t1, lo, hi);
+        const int64_t row0 = static_cast<int64_t>(s.r.slot < 0 ? 0 : s.r.slot) * P.M;
+        // this lane's page of tile j; num_blocks (which TMA reads as zeros) where
+        // there is nothing to see
+        auto page_of = [&](int j) -> int {
+          const int key = j * kKeys + lane * box;
+          if (lane >= boxes || key >= hi || key + box <= lo) return P.kv.num_blocks;
+          const int id = P.block_table[row0 + (key >> P.page_shift)];
+          if (id >= 0 && id < P.kv.num_blocks) return id;
+          report(P.status, DSPARK_ERR_BOUNDS);
+          return P.kv.num_blocks;
+        };
+        auto load = [&](const CUtensorMap* map, int j, int id) -> bool {
+          const uint32_t st = n % kRing;
+          if (!wait_warp(&empty[st], ((n / kRing) & 1) ^ 1, fail, P.status)) return false;
+          if (lane == 0) mbar_arrive_expect_tx(&full[st], kBytes);
+          __syncwarp();
+          if (lane < boxes) {
+            unsigned char* dst = ring + st * kBytes;
+            const int y = (j * kKeys + lane * box) & (page - 1);
+            if constexpr (kQuant) {
+              tma_load_4d(dst + lane * box * D, map, 0, y, s.h, id, &full[st], pol);
+            } else {
+#pragma unroll
+              for (int c = 0; c < C::kHalves; ++c)
+                tma_load_4d(dst + c * (kKeys * 128) + lane * box * 128, map, c * 64, y, s.h, id,
+                            &full[st], pol);
+            }
+          }
+          ++n;
+          return true;
+        };
+        // keys run `a` tiles ahead of the values; the pages of a tile are looked
+        // up one tile before its keys are due
+        const int a = s.ahead();
+        int id_next = page_of(s.j0), id_v0 = 0, id_v1 = 0;  // tiles i, i - a, and between
+        const int nt = s.tiles();
+        for (int i = 0; i < nt + a && ok; ++i) {
+          // at step i: values of tile i - a, then keys of tile i
+          const int id_k = id_next;
+          if (i + 1 < nt) id_next = page_of(s.j0 + i + 1);
+          if (i >= a) ok = load(&tmap_v, s.j0 + i - a, a == 2 ? id_v1 : id_v0);
+          if (ok && i < nt) ok = load(&tmap_k, s.j0 + i, id_k);
+          id_v1 = id_v0;
+          id_v0 = id_k;
+        }
+      }
+      // every copy has landed before the CTA may exit
+      for (uint32_t i = n > kRing ? n - kRing : 0; i < n; ++i)
+        (void)mbar_wait(&full[i % kRing], (i / kRing) & 1, P.status);
+    } else if (warp == 9) {
+      // ---- MMA issuer ------------------------------------------------------------------
+      if (lane == 0) {
+        constexpr uint32_t id_qk = idesc_of(!kF16, false, kKeys);
+        constexpr uint32_t id_pv = idesc_of(!kF16, true, D);
+        const uint64_t q_desc = tc::sw128_kmajor_desc(smem_addr(smem + C::q));
+        const uint64_t k_desc = tc::sw128_kmajor_desc(smem_addr(smem + C::kv));
+        const uint64_t v_desc = sw128_mnmajor_desc(smem_addr(smem + C::kv));
+        uint32_t base = 0, n_item[2] = {0, 0}, n_seg[2] = {0, 0};
+        bool ok = true;
+        while (ok && walk.next(s)) {
+          const int nt = s.tiles(), ni = s.pair ? 2 * nt : nt;
+          auto scores = [&](int i) -> bool {  // S_w = Q_w K^T of item i
+            const int w = i & 1, t = s.pair ? i >> 1 : i;
+            if (i < 2 && !wait_on(&m->q_ready[w], n_seg[w] & 1, fail, P.status)) return false;
+            const uint32_t ki = base + s.k_place(s.j0 + t), st = ki % C::kStages;
+            if (!wait_on(&m->kv_full[st], (ki / C::kStages) & 1, fail, P.status)) return false;
+            tc::fence_after_thread_sync();
+            const uint64_t qd = q_desc + static_cast<uint32_t>((w * C::kTileBytes) >> 4);
+            const uint64_t kd = k_desc + static_cast<uint32_t>((st * C::kTileBytes) >> 4);
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              const uint32_t off = ((c >> 2) * (kRows * 128) + (c & 3) * 32) >> 4;
+              mma_ss(tmem + w * kKeys, qd + off, kd + off, id_qk, c != 0);
+            }
+            if (!s.pair || w == 1) tc::mma_commit(&m->kv_empty[st]);
+            tc::mma_commit(&m->s_full[w]);
+            return true;
+          };
+          for (int i = 0; i < 2 && i < ni && ok; ++i) ok = scores(i);
+          for (int i = 0; i < ni && ok; ++i) {  // O_w += P_w V of item i
+            const int w = i & 1, t = s.pair ? i >> 1 : i;
+            if (!(ok = wait_on(&m->p_ready[w], n_item[w] & 1, fail, P.status))) break;
+            const uint32_t vi = base + s.v_place(s.j0 + t), st = vi % C::kStages;
+            if (!(ok = wait_on(&m->kv_full[st], (vi / C::kStages) & 1, fail, P.status))) break;
+            tc::fence_after_thread_sync();
+            const uint64_t vd = v_desc + static_cast<uint32_t>((st * C::kTileBytes) >> 4);
+            if (*reinterpret_cast<volatile int*>(&m->skip_pv[w]) != static_cast<int>(n_item[w])) {
+#pragma unroll
+              for (int c = 0; c < kKeys / 16; ++c)
+                mma_ts(tmem + 256 + w * 128, tmem + w * kKeys + c * 8, vd + ((c * 2048) >> 4),
+                       id_pv, i >= 2 || c != 0);
+            }
+            ++n_item[w];
+            if (!s.pair || w == 1) tc::mma_commit(&m->kv_empty[st]);
+            if (i + 2 < ni)
+              ok = scores(i + 2);
+            else
+              tc::mma_commit(&m->o_full[w]);
+          }
+          base += 2 * nt;
+          n_seg[0] += 1;
+          n_seg[1] += ni > 1;
+        }
+        tc::mma_commit(&m->drain);
+        (void)mbar_wait(&m->drain, 0, P.status);
+      }
+    } else if (kQuant && warp >= 12) {
+      // ---- e4m3 tiles to fp16, in the MMA's layout ---------------------------------------
+      if constexpr (kQuant) {
+        long long tiles = 0;
+        tiles = m->end > m->pos ? 2 * (m->end - m->pos) : 0;
+        const int ct = tid - 12 * 32;  // 0..127: a key each
+        constexpr int kChunks = D / 16;
+        for (long long n = 0; n < tiles; ++n) {
+          const uint32_t rs = static_cast<uint32_t>(n % C::kRaw);
+          const uint32_t st = static_cast<uint32_t>(n % C::kStages);
+          if (!wait_warp(&m->raw_full[rs], static_cast<uint32_t>(n / C::kRaw) & 1, fail, P.status))
+            break;
+          const unsigned char* src = smem + C::raw + rs * C::kRawBytes + ct * D;
+          uint4 x[kChunks];
+          // TMA swizzled the 16-byte pieces of a row by the row: 8 rows of 128
+          // bytes, or of 64 bytes two to a 128-byte line
+          const int sw = D == 128 ? ct & 7 : (ct >> 1) & 3;
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c)
+            x[c] = *reinterpret_cast<const uint4*>(src + ((c ^ sw) << 4));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&m->raw_empty[rs]);
+          if (!wait_warp(&m->kv_empty[st], (static_cast<uint32_t>(n / C::kStages) & 1) ^ 1, fail,
+                       P.status))
+            break;
+          unsigned char* dst = smem + C::kv + st * C::kTileBytes + ct * 128;
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            const uint32_t xw[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int ch = 2 * c + e;  // 16-byte piece of the fp16 row
+              *reinterpret_cast<uint4*>(dst + (ch >> 3) * (kKeys * 128) +
+                                        (((ch & 7) ^ (ct & 7)) << 4)) =
+                  make_uint4(e4m3x2_to_f16x2(xw[2 * e] & 0xFFFFu), e4m3x2_to_f16x2(xw[2 * e] >> 16),
+                             e4m3x2_to_f16x2(xw[2 * e + 1] & 0xFFFFu),
+                             e4m3x2_to_f16x2(xw[2 * e + 1] >> 16));
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&m->kv_full[st]);
+        }
+      }
+    }
+  }
+  tc::fence_before_thread_sync();
+  __syncthreads();
+  if (warp == 9) {
+    tc::fence_after_thread_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the partial results of the units that more than one CTA worked on: the
+// unit that CTA blockIdx.x opened, from its tail part and the head parts of
+// the CTAs after it, in that order. A warp per row.
+template <int D>
+__global__ void __launch_bounds__(256) paged_join_kernel(PagedAttentionParams P, int off) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Ws ws(D);
+  const unsigned char* wsp = static_cast<const unsigned char*>(P.workspace);
+  const int c = blockIdx.x;
+  const JoinDesc d = reinterpret_cast<const JoinDesc*>(wsp + ws.desc)[c];
+  if (d.parts == 0) return;
+  const int G = P.Hq / P.kv.kv_heads, tp = kRows / G;
+  const int lane = threadIdx.x & 31;
+  const float2* stats = reinterpret_cast<const float2*>(wsp + ws.stats);
+  const float* po = reinterpret_cast<const float*>(wsp + ws.o);
+  constexpr int kPer = D / 32;
+  const float vs = P.kv.v_scale ? P.kv.v_scale[d.h] : 1.f;
+  const int rows = d.tokens * G;
+  for (int i = blockIdx.y * 8 + (threadIdx.x >> 5); i < rows; i += gridDim.y * 8) {
+    const int tok = i / G, g = i - tok * G;
+    const int place = (tok / tp) * kRows + (tok % tp) * G + g;  // row tile, row
+    auto at = [&](int p) -> int64_t {
+      return (static_cast<int64_t>(c + p) * 2 + (p == 0 ? 1 : 0)) * 2 * kRows + place;
+    };
+    float r = -INFINITY;
+    for (int p = lane; p < d.parts; p += 32) r = fmaxf(r, stats[at(p)].x);
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) r = fmaxf(r, __shfl_xor_sync(0xFFFFFFFFu, r, s));
+    const float rb = r == -INFINITY ? 0.f : r;
+    float l = 0.f, o[kPer];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) o[e] = 0.f;
+    for (int p = 0; p < d.parts; ++p) {
+      const int64_t a = at(p);
+      const float2 x = stats[a];
+      const float keep = ex2_approx(x.x - rb);
+      l = fmaf(x.y, keep, l);
+#pragma unroll
+      for (int e = 0; e < kPer; e += 2) {
+        const float2 v = *reinterpret_cast<const float2*>(po + a * D + lane * kPer + e);
+        o[e] = fmaf(v.x, keep, o[e]);
+        o[e + 1] = fmaf(v.y, keep, o[e + 1]);
+      }
+    }
+    const bool none = l == 0.f;
+    const float inv = none ? 0.f : vs / l;
+    const int64_t row = static_cast<int64_t>(d.token0 + tok) * P.Hq + d.h * G + g;
+    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(P.out) + row * D +
+                                                lane * kPer);
+#pragma unroll
+    for (int e = 0; e < kPer; e += 2) {
+      const float a = none ? 0.f : o[e] * inv, b = none ? 0.f : o[e + 1] * inv;
+      out[e / 2] = P.dtype == DSPARK_F16 ? pack_f16(a, b) : pack_bf16(a, b);
+    }
+    if (P.lse && lane == 0) P.lse[row] = none ? -INFINITY : (rb - off + lg2_approx(l)) * kLn2;
+  }
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                       &q) != cudaSuccess ||
+      q != cudaDriverEntryPointSuccess)
+    return nullptr;
+  return reinterpret_cast<EncodeTiledFn>(fn);
+}
+
+// [num_blocks, kv_heads, page_size, head_dim] with the cache's strides; a box
+// is 64 values (8-bit: a whole row) of up to 128 tokens of one page and head.
+bool make_map(CUtensorMap* map, void* base, const dspark_paged_kv& kv, int64_t block, int64_t head,
+              int64_t token) {
+  static const EncodeTiledFn encode = encode_fn();  // the driver's entry point
+  if (!encode) return false;
+  const bool quant = kv.dtype == DSPARK_E4M3;
+  const cuuint64_t es = quant ? 1 : 2;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(kv.head_dim),
+                              static_cast<cuuint64_t>(kv.page_size),
+                              static_cast<cuuint64_t>(kv.kv_heads),
+                              static_cast<cuuint64_t>(kv.num_blocks)};
+  // (the stride of an axis of one is not used)
+  const cuuint64_t strides[3] = {token * es, (kv.kv_heads > 1 ? head : token) * es,
+                                 (kv.num_blocks > 1 ? block : token) * es};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(quant ? kv.head_dim : 64),
+                             static_cast<cuuint32_t>(kv.page_size < kKeys ? kv.page_size : kKeys),
+                             1, 1};
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  const CUtensorMapDataType type = quant ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : kv.dtype == DSPARK_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                            : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUtensorMapSwizzle swizzle = quant && kv.head_dim == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                                : CU_TENSOR_MAP_SWIZZLE_128B;
+  return encode(map, type, 4, base, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+template <int D, bool kF16, bool kQuant>
+cudaError_t launch(const PagedAttentionParams& p, const CUtensorMap& mk, const CUtensorMap& mv,
+                   int sms, cudaStream_t stream) {
+  using C = Cfg<D, kQuant>;
+  cudaError_t err =
+      cudaFuncSetAttribute(paged_attention_kernel<D, kF16, kQuant>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
+  if (err != cudaSuccess) return err;
+  const int grid = sms < kMaxCtas ? sms : kMaxCtas;
+  paged_attention_kernel<D, kF16, kQuant><<<grid, C::kThreads, C::kBytes, stream>>>(mk, mv, p);
+  err = cudaGetLastError();
+  if (err != cudaSuccess) return err;
+  // the join starts when the last CTA of the launch before it ends
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 8);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, p, kF16 ? 7 : 0);
+}
+
+template <int D>
+cudaError_t launch_dim(const PagedAttentionParams& p, const CUtensorMap& mk, const CUtensorMap& mv,
+                       int sms, cudaStream_t stream) {
+  if (p.kv.dtype == DSPARK_E4M3) return launch<D, true, true>(p, mk, mv, sms, stream);
+  return p.dtype == DSPARK_F16 ? launch<D, true, false>(p, mk, mv, sms, stream)
+                               : launch<D, false, false>(p, mk, mv, sms, stream);
 }
 
 }  // namespace
@@ -132,17 +1179,22 @@ size_t paged_attention_workspace_bytes(int B, int Hq, int Hkv, int D) {
   (void)B;
   (void)Hq;
   (void)Hkv;
-  (void)D;
-  return 256;
+  return Ws(D).total;
 }
 
 cudaError_t launch_paged_attention(const PagedAttentionParams& p, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(p.T), static_cast<unsigned>(p.Hq));
-  if (p.kv.head_dim == 64)
-    paged_attention_kernel<64><<<grid, 32 * kWarps, 0, stream>>>(p);
-  else
-    paged_attention_kernel<128><<<grid, 32 * kWarps, 0, stream>>>(p);
-  return cudaGetLastError();
+  int dev = 0, sms = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err == cudaSuccess)
+    err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (err != cudaSuccess) return err;
+  CUtensorMap mk, mv;
+  const dspark_paged_kv& kv = p.kv;
+  if (!make_map(&mk, kv.k, kv, kv.k_block_stride, kv.k_head_stride, kv.k_token_stride) ||
+      !make_map(&mv, kv.v, kv, kv.v_block_stride, kv.v_head_stride, kv.v_token_stride))
+    return cudaErrorInvalidValue;
+  return kv.head_dim == 64 ? launch_dim<64>(p, mk, mv, sms, stream)
+                           : launch_dim<128>(p, mk, mv, sms, stream);
 }
 
 }  // namespace dspark
