@@ -28,10 +28,14 @@
 // per CTA and joined by paged_join_kernel in a fixed order.
 //
 // Warps: 0-3 and 4-7 softmax (thread = row = lane of tensor memory), 8 TMA
-// producer, 9 MMA issuer; with an 8-bit cache 12-15 convert e4m3 tiles to fp16
-// in shared memory (the 8-bit values are exact in fp16; an 8-bit MMA would want
-// the queries and p in 8 bits too) and query rows are brought to fp16 by a
-// power of two per row. Pages: a 128-key tile is 128 / page_size TMA boxes.
+// producer of the keys, 9 MMA issuer, 10 TMA producer of the values, 11 the
+// scout: it walks the units ahead of the others, loads their query rows (a ring
+// of two row tiles) and publishes what the others need to know of them. With an
+// 8-bit cache 8 loads keys and values, 10-11 are the scouts (query rows are
+// brought to fp16 by a power of two per row), and 12-15 convert e4m3 tiles to
+// fp16 in shared memory (the 8-bit values are exact in fp16; an 8-bit MMA would
+// want the queries and p in 8 bits too). Pages: a 128-key tile is
+// 128 / page_size TMA boxes.
 //
 // What a row does not see must not reach it: masked scores are replaced (not
 // added to), value rows past the request's last token are zeroed in shared
@@ -70,8 +74,8 @@ struct Cfg {
   static constexpr int kRaw = kQuant ? (D == 128 ? 3 : 6) : 0;
   static constexpr int kThreads = kQuant ? 512 : 384;
   // registers a thread after the split (the launch gives 128 or 168 to each)
-  static constexpr int kSoftmaxRegs = kQuant ? 192 : 216;
-  static constexpr int kOtherRegs = kQuant ? 64 : 72;
+  static constexpr int kSoftmaxRegs = kQuant ? 184 : 216;
+  static constexpr int kOtherRegs = 72;
   // shared memory, offsets from a 1024-byte aligned base
   static constexpr int q = 0;
   static constexpr int kv = q + 2 * kTileBytes;
@@ -82,13 +86,45 @@ struct Cfg {
   static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
 };
 
+struct Request {
+  int q0, n, slot, len;
+};
+
+// A run of key tiles of one unit.
+struct Seg {
+  Request r;
+  int h;
+  int t0, t1;   // tokens of the unit within the request
+  int j0, j1;   // key tiles
+  int c1;       // the last CTA that works on the unit
+  bool pair, opens, closes;  // two row tiles; starts / ends with the unit
+  bool end;     // no segment, the walk is over
+  __device__ int tiles() const { return j1 - j0; }
+  // items (key tiles) of warpgroup w and the k-th one's tile
+  __device__ int items(int w) const { return pair ? tiles() : (tiles() + 1 - w) / 2; }
+  __device__ int tile(int w, int k) const { return pair ? j0 + k : j0 + 2 * k + w; }
+  __device__ int ahead() const { return pair ? 1 : 2; }  // key tiles loaded before the first values
+  // place of a tile's keys / values in the order in which the segment loads them
+  __device__ int k_place(int j) const {
+    const int i = j - j0, a = ahead();
+    return i < a ? i : 2 * i - a + 1;
+  }
+  __device__ int v_place(int j) const {
+    const int i = j - j0;
+    return i + min(tiles(), ahead() + i);
+  }
+};
+
 struct Misc {
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
   uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];
-  uint64_t s_full[2], p_ready[2], q_ready[2], o_full[2], scanned[2];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t s_full[2], p_half[2], p_ready[2], o_full[2], scanned[2];
   uint64_t merge, merged, drain;
+  Seg seg[2];  // of the segment whose first row tile is in the slot
   uint32_t tmem;
   int fail;
+  int copies[kMaxStages];  // copies made into each stage of the TMA ring
   int bad[2];      // the last tile whose values were found non-finite, per warpgroup
   int skip_pv[2];  // the last item whose P V the warpgroup did itself
   int start_b, per;
@@ -245,10 +281,6 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t phase, volatil
 }
 
 // ---- the units of work -------------------------------------------------------------
-struct Request {
-  int q0, n, slot, len;
-};
-
 __device__ __forceinline__ Request load_request(const PagedAttentionParams& P, int b, bool tell) {
   Request r;
   const int a = P.query_start[b], e = P.query_start[b + 1];
@@ -290,30 +322,6 @@ __device__ __forceinline__ void unit_tiles(const PagedAttentionParams& P, const 
   je = max(jb + 1, (hi + kKeys - 1) / kKeys);
 }
 
-// A run of key tiles of one unit.
-struct Seg {
-  Request r;
-  int h;
-  int t0, t1;   // tokens of the unit within the request
-  int j0, j1;   // key tiles
-  bool pair, opens, closes;  // two row tiles; starts / ends with the unit
-  int c1;       // the last CTA that works on the unit
-  __device__ int tiles() const { return j1 - j0; }
-  // items (key tiles) of warpgroup w and the k-th one's tile
-  __device__ int items(int w) const { return pair ? tiles() : (tiles() + 1 - w) / 2; }
-  __device__ int tile(int w, int k) const { return pair ? j0 + k : j0 + 2 * k + w; }
-  __device__ int ahead() const { return pair ? 1 : 2; }  // key tiles loaded before the first values
-  // place of a tile's keys / values in the order in which the segment loads them
-  __device__ int k_place(int j) const {
-    const int i = j - j0, a = ahead();
-    return i < a ? i : 2 * i - a + 1;
-  }
-  __device__ int v_place(int j) const {
-    const int i = j - j0;
-    return i + min(tiles(), ahead() + i);
-  }
-};
-
 // The segments of this CTA in order.
 struct Walk {
   const PagedAttentionParams& P;
@@ -346,6 +354,7 @@ struct Walk {
     s.opens = j == jb;
     s.closes = s.j1 == je;
     s.c1 = static_cast<int>((pos + (je - j) - 1) / per);
+    s.end = false;
     pos += s.j1 - s.j0;
     j = s.j1;
     if (j == je && pos < end) {
@@ -451,7 +460,8 @@ __device__ void make_plan(const PagedAttentionParams& P, Misc* m, unsigned long 
 // kF16: the MMA's type is fp16 (fp16 rows, or an 8-bit cache), else bf16.
 template <int D, bool kF16, bool kQuant>
 __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
-paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_k,
+paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
+                       const __grid_constant__ CUtensorMap tmap_k,
                        const __grid_constant__ CUtensorMap tmap_v, PagedAttentionParams P) {
   using C = Cfg<D, kQuant>;
   extern __shared__ unsigned char smem_raw[];
@@ -476,17 +486,21 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_k,
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(&m->s_full[w], 1);
+      mbar_init(&m->q_full[w], kQuant ? 2 : 1);
+      mbar_init(&m->q_empty[w], 9);  // the MMAs, eight softmax warps
+      mbar_init(&m->p_half[w], 4);
       mbar_init(&m->p_ready[w], 4);
-      mbar_init(&m->q_ready[w], 4);
       mbar_init(&m->o_full[w], 1);
       mbar_init(&m->scanned[w], 4);
       m->bad[w] = m->skip_pv[w] = -1;
     }
+    for (int i = 0; i < kMaxStages; ++i) m->copies[i] = 0;
     mbar_init(&m->merge, 4);
     mbar_init(&m->merged, 4);
     mbar_init(&m->drain, 1);
     m->fail = 0;
     fence_mbar_init();
+    if (!kQuant) tc::prefetch_tensormap(&tmap_q);
     tc::prefetch_tensormap(&tmap_k);
     tc::prefetch_tensormap(&tmap_v);
   }
@@ -500,9 +514,6 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_k,
   __syncthreads();
   tc::fence_after_thread_sync();
   const uint32_t tmem = m->tmem;
-  Walk walk(P, m, tp);
-  Seg s;
-
   if (warp < 8) {
     // ---- softmax ------------------------------------------------------------------
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
@@ -510,15 +521,27 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_k,
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_t = tmem + lanes + w * kKeys;         // scores, then p
     const uint32_t o_t = tmem + lanes + 256 + w * 128;     // O
-    unsigned char* q_s = smem + C::q + w * C::kTileBytes;
     constexpr float kOff = kF16 ? 7.0f : 0.0f;
-    uint32_t n_seg = 0, n_item = 0, n_scan = 0, n_merge = 0;
+    uint32_t n_q = 0, n_seg = 0, n_item = 0, n_scan = 0, n_merge = 0;
     uint32_t base = 0;  // tiles loaded before this segment
     bool tail_split = false;
     const float sl0 = fminf(fmaxf(fabsf(P.scale) * kLog2e, 1e-37f), 3e38f);
-    const uint32_t flip = P.scale < 0.f ? 0x80008000u : 0u;
+    const int tok = row / G;  // token within the row tile
     bool ok = true;
-    while (ok && walk.next(s)) {
+    for (;;) {
+      if (!(ok = wait_warp(&m->q_full[n_q & 1], (n_q >> 1) & 1, fail, P.status))) break;
+      const Seg s = m->seg[n_q & 1];
+      if (s.end) break;
+      const uint32_t n_q1 = n_q + 1;
+      if (s.pair && !(ok = wait_warp(&m->q_full[n_q1 & 1], (n_q1 >> 1) & 1, fail, P.status))) break;
+      float sl = sl0 * (P.kv.k_scale ? P.kv.k_scale[s.h] : 1.f);
+      if constexpr (kQuant) sl *= row_scale[((n_q + (s.pair ? w : 0)) & 1) * kRows + row];
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&m->q_empty[n_q & 1]);
+        if (s.pair) mbar_arrive(&m->q_empty[n_q1 & 1]);
+      }
+      n_q += s.pair ? 2 : 1;
       const int items = s.items(w);
       const bool split = !(s.opens && s.closes);
       const int first = s.t0 + (s.pair ? w * tp : 0);       // first token of the row tile
@@ -526,7 +549,6 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_k,
       const int nrow = ntok * G;
       const bool live = row < nrow;
       const bool warp_live = (warp & 3) * 32 < nrow;
-      const int tok = row / G;                               // token within the row tile
       int lo, hi;
       key_range(P, s.r.n, s.r.len, first + tok, first + tok + 1, lo, hi);
       if (!live) lo = hi = 0;
@@ -534,57 +556,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_k,
       int all_lo, all_hi, unused;
       key_range(P, s.r.n, s.r.len, first, first + 1, unused, all_hi);
       key_range(P, s.r.n, s.r.len, first + ntok - 1, first + ntok, all_lo, unused);
-      float sl = sl0 * (P.kv.k_scale ? P.kv.k_scale[s.h] : 1.f);
       float r = -INFINITY, l = 0.f;  // reference (scaled), sum
-      if (items > 0) {
-        // query rows into shared memory, K-major, 128-byte swizzle
-        const uint16_t* src = static_cast<const uint16_t*>(P.q);
-        for (int i = row; i < nrow * (D / 8); i += kRows) {
-          const int rr = i / (D / 8), c = i % (D / 8);
-          const int t = rr / G, g = rr - t * G;
-          uint4 x = __ldg(reinterpret_cast<const uint4*>(
-              src + static_cast<int64_t>(s.r.q0 + first + t) * P.q_stride +
-              static_cast<int64_t>(s.h * G + g) * D + c * 8));
-          x.x ^= flip;
-          x.y ^= flip;
-          x.z ^= flip;
-          x.w ^= flip;
-          if constexpr (kQuant) {
-            // to fp16 with the row's largest value brought to 2^14: exact but
-            // for values 2^-28 below it. D / 8 neighbouring lanes hold a row.
-            float f[8];
-            uint32_t* xw = &x.x;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if (P.dtype == DSPARK_F16)
-                unpack_f16(xw[e], f[2 * e], f[2 * e + 1]);
-              else
-                unpack_bf16(xw[e], f[2 * e], f[2 * e + 1]);
-            }
-            uint32_t big = 0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) big = max(big, __float_as_uint(f[e]) & 0x7FFFFFFFu);
-            const unsigned int who = ((1u << (D / 8)) - 1u) << (lane & ~(D / 8 - 1));
-#pragma unroll
-            for (int o = D / 16; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(who, big, o));
-            const int ex = big == 0u ? 14 : max(static_cast<int>(big >> 23) - 127, -112);
-            const float up = __uint_as_float(static_cast<uint32_t>(14 - ex + 127) << 23);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) xw[e] = pack_f16(f[2 * e] * up, f[2 * e + 1] * up);
-            if (c == 0)
-              row_scale[w * kRows + rr] = __uint_as_float(static_cast<uint32_t>(ex - 14 + 127) << 23);
-          }
-          *reinterpret_cast<uint4*>(q_s + (c >> 3) * (kRows * 128) + rr * 128 +
-                                    (((c & 7) ^ (rr & 7)) << 4)) = x;
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&m->q_ready[w]);
-        if constexpr (kQuant) {
-          if (!(ok = wait_warp(&m->q_ready[w], n_seg & 1, fail, P.status))) break;
-          if (live) sl *= row_scale[w * kRows + row];
-        }
-      }
       for (int k = 0; k < items; ++k, ++n_item) {
         const int key0 = s.tile(w, k) * kKeys;
         if (!(ok = wait_warp(&m->s_full[w], n_item & 1, fail, P.status))) break;
@@ -640,6 +612,15 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_k,
           unsigned long long sum = 0ull, sum1 = 0ull;
 #pragma unroll
           for (int c = 0; c < kKeys; c += 4) {
+            if (c == kKeys / 2) {  // the first half's products may begin
+              tmem_st32(s_t, x);
+              if (!(tail || scan)) {
+                tmem_wait_st();
+                tc::fence_before_thread_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&m->p_half[w]);
+              }
+            }
             float a, b, e, f;
             f2_unpack(f2_fma(f2_pack(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sl2, neg2),
                       a, b);
@@ -657,7 +638,6 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_k,
           float a, b;
           f2_unpack(f2_add(sum, sum1), a, b);
           l += a + b;
-          tmem_st32(s_t, x);
           tmem_st32(s_t + 32, x + 32);
           tmem_wait_st();
         }
@@ -751,7 +731,10 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_k,
         }
         tc::fence_before_thread_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&m->p_ready[w]);
+        if (lane == 0) {
+          if (tail || scan || !warp_live) mbar_arrive(&m->p_half[w]);
+          mbar_arrive(&m->p_ready[w]);
+        }
       }
       if (!ok) break;
       base += 2 * s.tiles();
@@ -862,10 +845,10 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_k,
       reinterpret_cast<JoinDesc*>(wsp + ws.desc)[blockIdx.x].parts = 0;
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
-    if (warp == 8) {
-      // ---- TMA producer: keys and values of the segments' tiles, page by page --------
+    if (warp == 8 || (!kQuant && warp == 10)) {
+      // ---- TMA producers: keys and values of the segments' tiles, page by page -------
       const uint64_t pol = policy_evict_normal();
-      constexpr int kRing = kQuant ? C::kRaw : C::kStages;
+      constexpr uint32_t kRing = kQuant ? C::kRaw : C::kStages;
       constexpr int kBytes = kQuant ? C::kRawBytes : C::kTileBytes;
       uint64_t* full = kQuant ? m->raw_full : m->kv_full;
       uint64_t* empty = kQuant ? m->raw_empty : m->kv_empty;
@@ -873,8 +856,10 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_k,
       const int page = 1 << P.page_shift;
       const int box = page < kKeys ? page : kKeys;  // tokens of a TMA box
       const int boxes = kKeys / box;                // boxes of a tile (<= 8)
-      uint32_t n = 0;  // tiles loaded
+      uint32_t base = 0;                            // tiles loaded before this segment
       bool ok = true;
+      Walk walk(P, m, tp);
+      Seg s;
       while (ok && walk.next(s)) {
         int lo, hi;
         key_range(P, s.r.n, s.r.len, s.t0, s.t1, lo, hi);
@@ -889,9 +874,9 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_k,
           report(P.status, DSPARK_ERR_BOUNDS);
           return P.kv.num_blocks;
         };
-        auto load = [&](const CUtensorMap* map, int j, int id) -> bool {
-          const uint32_t st = n % kRing;
-          if (!wait_warp(&empty[st], ((n / kRing) & 1) ^ 1, fail, P.status)) return false;
+        auto load = [&](const CUtensorMap* map, int j, int id, int place) -> bool {
+          const uint32_t n = base + place, st = n % kRing, ph = (n / kRing) & 1;
+          if (!wait_warp(&empty[st], ph ^ 1, fail, P.status)) return false;
           if (lane == 0) mbar_arrive_expect_tx(&full[st], kBytes);
           __syncwarp();
           if (lane < boxes) {
@@ -906,46 +891,149 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_k,
                             &full[st], pol);
             }
           }
-          ++n;
+          if (lane == 0) m->copies[st] = static_cast<int>(n / kRing) + 1;
           return true;
         };
-        // keys run `a` tiles ahead of the values; the pages of a tile are looked
-        // up one tile before its keys are due
-        const int a = s.ahead();
-        int id_next = page_of(s.j0), id_v0 = 0, id_v1 = 0;  // tiles i, i - a, and between
+        // the pages of a tile are looked up a tile before it is due
         const int nt = s.tiles();
-        for (int i = 0; i < nt + a && ok; ++i) {
-          // at step i: values of tile i - a, then keys of tile i
-          const int id_k = id_next;
-          if (i + 1 < nt) id_next = page_of(s.j0 + i + 1);
-          if (i >= a) ok = load(&tmap_v, s.j0 + i - a, a == 2 ? id_v1 : id_v0);
-          if (ok && i < nt) ok = load(&tmap_k, s.j0 + i, id_k);
-          id_v1 = id_v0;
-          id_v0 = id_k;
+        int id_next = page_of(s.j0);
+        if constexpr (kQuant) {  // keys `a` tiles ahead of the values
+          const int a = s.ahead();
+          int id_v0 = 0, id_v1 = 0;  // of the tiles one and two before
+          for (int i = 0; i < nt + a && ok; ++i) {
+            const int j = s.j0 + i, id_k = id_next;
+            if (i + 1 < nt) id_next = page_of(j + 1);
+            if (i >= a) ok = load(&tmap_v, j - a, a == 2 ? id_v1 : id_v0, s.v_place(j - a));
+            if (ok && i < nt) ok = load(&tmap_k, j, id_k, s.k_place(j));
+            id_v1 = id_v0;
+            id_v0 = id_k;
+          }
+        } else {
+          const CUtensorMap* map = warp == 8 ? &tmap_k : &tmap_v;
+          for (int j = s.j0; j < s.j1 && ok; ++j) {
+            const int id = id_next;
+            if (j + 1 < s.j1) id_next = page_of(j + 1);
+            ok = load(map, j, id, warp == 8 ? s.k_place(j) : s.v_place(j));
+          }
         }
+        base += 2 * nt;
       }
-      // every copy has landed before the CTA may exit
-      for (uint32_t i = n > kRing ? n - kRing : 0; i < n; ++i)
-        (void)mbar_wait(&full[i % kRing], (i / kRing) & 1, P.status);
+    } else if (warp == 11 || (kQuant && warp == 10)) {
+      // ---- scout: segments and their query rows ---------------------------------------
+      uint32_t n_q = 0;
+      bool ok = true;
+      Walk walk(P, m, tp);
+      Seg s;
+      for (;;) {
+        const bool more = walk.next(s);
+        s.end = !more;
+        const int fills = more && s.pair ? 2 : 1;
+        for (int f = 0; f < fills && ok; ++f, ++n_q) {
+          const uint32_t sl = n_q & 1;
+          if (!(ok = wait_warp(&m->q_empty[sl], ((n_q >> 1) & 1) ^ 1, fail, P.status))) break;
+          if (f == 0 && warp == 11 && lane == 0) m->seg[sl] = s;
+          const int tok0 = s.r.q0 + s.t0 + f * tp;
+          if constexpr (!kQuant) {
+            if (lane == 0) {
+              if (more) {
+                mbar_arrive_expect_tx(&m->q_full[sl], C::kHalves * 128 * G * tp);
+#pragma unroll
+                for (int c = 0; c < C::kHalves; ++c)
+                  tc::tma_load_3d(smem + C::q + sl * C::kTileBytes + c * (kRows * 128), &tmap_q,
+                                  c * 64, s.h * G, tok0, &m->q_full[sl], policy_evict_normal());
+              } else {
+                mbar_arrive(&m->q_full[sl]);
+              }
+            }
+          } else {
+            // to fp16 with each row's largest value brought to 2^14: exact but for
+            // values 2^-28 below it. D / 8 neighbouring lanes hold a row.
+            const int nrow = more ? min(tp, s.t1 - s.t0 - f * tp) * G : 0;
+            unsigned char* q_s = smem + C::q + sl * C::kTileBytes;
+            const uint16_t* src = static_cast<const uint16_t*>(P.q);
+            const uint32_t flip = P.scale < 0.f ? 0x80008000u : 0u;
+            constexpr int kBatch = 4;
+            const int total = nrow * (D / 8);
+            for (int i0 = (warp - 10) * 32 + lane; i0 < total; i0 += 64 * kBatch) {
+              uint4 x[kBatch];
+#pragma unroll
+              for (int e = 0; e < kBatch; ++e) {
+                const int i = i0 + 64 * e, rr = i / (D / 8), c = i % (D / 8);
+                const int tk = rr / G, g = rr - tk * G;
+                if (i < total)
+                  x[e] = __ldg(reinterpret_cast<const uint4*>(
+                      src + static_cast<int64_t>(tok0 + tk) * P.q_stride +
+                      static_cast<int64_t>(s.h * G + g) * D + c * 8));
+              }
+#pragma unroll
+              for (int e = 0; e < kBatch; ++e) {
+                const int i = i0 + 64 * e, rr = i / (D / 8), c = i % (D / 8);
+                if (i >= total) break;
+                uint32_t xw[4] = {x[e].x ^ flip, x[e].y ^ flip, x[e].z ^ flip, x[e].w ^ flip};
+                float v[8];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                  if (P.dtype == DSPARK_F16)
+                    unpack_f16(xw[y], v[2 * y], v[2 * y + 1]);
+                  else
+                    unpack_bf16(xw[y], v[2 * y], v[2 * y + 1]);
+                }
+                uint32_t big = 0;
+#pragma unroll
+                for (int y = 0; y < 8; ++y) big = max(big, __float_as_uint(v[y]) & 0x7FFFFFFFu);
+                const unsigned int who = ((1u << (D / 8)) - 1u) << (lane & ~(D / 8 - 1));
+#pragma unroll
+                for (int o = D / 16; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(who, big, o));
+                const int ex = big == 0u ? 14 : max(static_cast<int>(big >> 23) - 127, -112);
+                const float up = __uint_as_float(static_cast<uint32_t>(14 - ex + 127) << 23);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) xw[y] = pack_f16(v[2 * y] * up, v[2 * y + 1] * up);
+                if (c == 0)
+                  row_scale[sl * kRows + rr] =
+                      __uint_as_float(static_cast<uint32_t>(ex - 14 + 127) << 23);
+                *reinterpret_cast<uint4*>(q_s + (c >> 3) * (kRows * 128) + rr * 128 +
+                                          (((c & 7) ^ (rr & 7)) << 4)) =
+                    make_uint4(xw[0], xw[1], xw[2], xw[3]);
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&m->q_full[sl]);
+          }
+        }
+        if (!more || !ok) break;
+      }
+      // the copies have landed before the CTA may exit
+      if (!kQuant && lane == 0)
+        for (uint32_t i = n_q > 2 ? n_q - 2 : 0; i < n_q; ++i)
+          (void)mbar_wait(&m->q_full[i & 1], (i >> 1) & 1, P.status);
     } else if (warp == 9) {
       // ---- MMA issuer ------------------------------------------------------------------
       if (lane == 0) {
-        constexpr uint32_t id_qk = idesc_of(!kF16, false, kKeys);
         constexpr uint32_t id_pv = idesc_of(!kF16, true, D);
+        // (a negative scale is a negated A; the scouts of an 8-bit cache see to it)
+        const uint32_t id_qk = idesc_of(!kF16, false, kKeys) |
+                               (!kQuant && P.scale < 0.f ? 1u << 13 : 0u);
         const uint64_t q_desc = tc::sw128_kmajor_desc(smem_addr(smem + C::q));
         const uint64_t k_desc = tc::sw128_kmajor_desc(smem_addr(smem + C::kv));
         const uint64_t v_desc = sw128_mnmajor_desc(smem_addr(smem + C::kv));
-        uint32_t base = 0, n_item[2] = {0, 0}, n_seg[2] = {0, 0};
+        uint32_t base = 0, n_q = 0, n_item[2] = {0, 0};
         bool ok = true;
-        while (ok && walk.next(s)) {
+        while (ok) {
+          if (!wait_on(&m->q_full[n_q & 1], (n_q >> 1) & 1, fail, P.status)) break;
+          const Seg s = m->seg[n_q & 1];
+          if (s.end) break;
+          const uint32_t n_q1 = n_q + 1;
+          if (s.pair && !wait_on(&m->q_full[n_q1 & 1], (n_q1 >> 1) & 1, fail, P.status)) break;
+          tc::fence_after_thread_sync();
           const int nt = s.tiles(), ni = s.pair ? 2 * nt : nt;
-          auto scores = [&](int i) -> bool {  // S_w = Q_w K^T of item i
+          auto scores = [&](int i) -> bool {  // S_w = Q K^T of item i
             const int w = i & 1, t = s.pair ? i >> 1 : i;
-            if (i < 2 && !wait_on(&m->q_ready[w], n_seg[w] & 1, fail, P.status)) return false;
             const uint32_t ki = base + s.k_place(s.j0 + t), st = ki % C::kStages;
             if (!wait_on(&m->kv_full[st], (ki / C::kStages) & 1, fail, P.status)) return false;
             tc::fence_after_thread_sync();
-            const uint64_t qd = q_desc + static_cast<uint32_t>((w * C::kTileBytes) >> 4);
+            const uint32_t sl = (n_q + (s.pair ? w : 0)) & 1;
+            const uint64_t qd = q_desc + static_cast<uint32_t>((sl * C::kTileBytes) >> 4);
             const uint64_t kd = k_desc + static_cast<uint32_t>((st * C::kTileBytes) >> 4);
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
@@ -953,23 +1041,33 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_k,
               mma_ss(tmem + w * kKeys, qd + off, kd + off, id_qk, c != 0);
             }
             if (!s.pair || w == 1) tc::mma_commit(&m->kv_empty[st]);
+            if (t == nt - 1) tc::mma_commit(&m->q_empty[sl]);
             tc::mma_commit(&m->s_full[w]);
             return true;
           };
           for (int i = 0; i < 2 && i < ni && ok; ++i) ok = scores(i);
-          for (int i = 0; i < ni && ok; ++i) {  // O_w += P_w V of item i
+          for (int i = 0; i < ni && ok; ++i) {  // O_w += P_w V of item i, in two halves
             const int w = i & 1, t = s.pair ? i >> 1 : i;
-            if (!(ok = wait_on(&m->p_ready[w], n_item[w] & 1, fail, P.status))) break;
             const uint32_t vi = base + s.v_place(s.j0 + t), st = vi % C::kStages;
-            if (!(ok = wait_on(&m->kv_full[st], (vi / C::kStages) & 1, fail, P.status))) break;
-            tc::fence_after_thread_sync();
             const uint64_t vd = v_desc + static_cast<uint32_t>((st * C::kTileBytes) >> 4);
-            if (*reinterpret_cast<volatile int*>(&m->skip_pv[w]) != static_cast<int>(n_item[w])) {
+            if (!(ok = wait_on(&m->kv_full[st], (vi / C::kStages) & 1, fail, P.status))) break;
+            bool skip = false;
 #pragma unroll
-              for (int c = 0; c < kKeys / 16; ++c)
-                mma_ts(tmem + 256 + w * 128, tmem + w * kKeys + c * 8, vd + ((c * 2048) >> 4),
-                       id_pv, i >= 2 || c != 0);
+            for (int half = 0; half < 2; ++half) {
+              uint64_t* bar = half ? &m->p_ready[w] : &m->p_half[w];
+              if (!(ok = wait_on(bar, n_item[w] & 1, fail, P.status))) break;
+              tc::fence_after_thread_sync();
+              if (half == 0)
+                skip = *reinterpret_cast<volatile int*>(&m->skip_pv[w]) ==
+                       static_cast<int>(n_item[w]);
+              if (!skip) {
+#pragma unroll
+                for (int c = half * 4; c < half * 4 + 4; ++c)
+                  mma_ts(tmem + 256 + w * 128, tmem + w * kKeys + c * 8, vd + ((c * 2048) >> 4),
+                         id_pv, i >= 2 || c != 0);
+              }
             }
+            if (!ok) break;
             ++n_item[w];
             if (!s.pair || w == 1) tc::mma_commit(&m->kv_empty[st]);
             if (i + 2 < ni)
@@ -978,8 +1076,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_k,
               tc::mma_commit(&m->o_full[w]);
           }
           base += 2 * nt;
-          n_seg[0] += 1;
-          n_seg[1] += ni > 1;
+          n_q += s.pair ? 2 : 1;
         }
         tc::mma_commit(&m->drain);
         (void)mbar_wait(&m->drain, 0, P.status);
@@ -1035,6 +1132,12 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_k,
   if (warp == 9) {
     tc::fence_after_thread_sync();
     tc::tmem_dealloc(tmem, 512);
+  }
+  if (tid == 0) {  // every copy has landed before the CTA exits
+    for (int i = 0; i < (kQuant ? C::kRaw : C::kStages); ++i)
+      if (m->copies[i] > 0)
+        (void)mbar_wait(kQuant ? &m->raw_full[i] : &m->kv_full[i], (m->copies[i] - 1) & 1,
+                        P.status);
   }
 }
 
@@ -1140,16 +1243,37 @@ bool make_map(CUtensorMap* map, void* base, const dspark_paged_kv& kv, int64_t b
          CUDA_SUCCESS;
 }
 
+// [T, q_heads, head_dim] with the tokens' stride; a box is 64 values of the
+// query heads of a key head, of as many tokens as a row tile holds.
+bool make_q_map(CUtensorMap* map, const PagedAttentionParams& p) {
+  static const EncodeTiledFn encode = encode_fn();
+  if (!encode) return false;
+  const int G = p.Hq / p.kv.kv_heads, D = p.kv.head_dim;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(p.Hq),
+                              static_cast<cuuint64_t>(p.T)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2,
+                                 static_cast<cuuint64_t>(p.q_stride) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(kRows / G)};
+  const cuuint32_t one[3] = {1, 1, 1};
+  return encode(map,
+                p.dtype == DSPARK_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                      : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                3, const_cast<void*>(p.q), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, bool kF16, bool kQuant>
-cudaError_t launch(const PagedAttentionParams& p, const CUtensorMap& mk, const CUtensorMap& mv,
-                   int sms, cudaStream_t stream) {
+cudaError_t launch(const PagedAttentionParams& p, const CUtensorMap& mq, const CUtensorMap& mk,
+                   const CUtensorMap& mv, int sms, cudaStream_t stream) {
   using C = Cfg<D, kQuant>;
   cudaError_t err =
       cudaFuncSetAttribute(paged_attention_kernel<D, kF16, kQuant>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
   if (err != cudaSuccess) return err;
   const int grid = sms < kMaxCtas ? sms : kMaxCtas;
-  paged_attention_kernel<D, kF16, kQuant><<<grid, C::kThreads, C::kBytes, stream>>>(mk, mv, p);
+  paged_attention_kernel<D, kF16, kQuant><<<grid, C::kThreads, C::kBytes, stream>>>(mq, mk, mv,
+                                                                              p);
   err = cudaGetLastError();
   if (err != cudaSuccess) return err;
   // the join starts when the last CTA of the launch before it ends
@@ -1166,11 +1290,11 @@ cudaError_t launch(const PagedAttentionParams& p, const CUtensorMap& mk, const C
 }
 
 template <int D>
-cudaError_t launch_dim(const PagedAttentionParams& p, const CUtensorMap& mk, const CUtensorMap& mv,
-                       int sms, cudaStream_t stream) {
-  if (p.kv.dtype == DSPARK_E4M3) return launch<D, true, true>(p, mk, mv, sms, stream);
-  return p.dtype == DSPARK_F16 ? launch<D, true, false>(p, mk, mv, sms, stream)
-                               : launch<D, false, false>(p, mk, mv, sms, stream);
+cudaError_t launch_dim(const PagedAttentionParams& p, const CUtensorMap& mq, const CUtensorMap& mk,
+                       const CUtensorMap& mv, int sms, cudaStream_t stream) {
+  if (p.kv.dtype == DSPARK_E4M3) return launch<D, true, true>(p, mq, mk, mv, sms, stream);
+  return p.dtype == DSPARK_F16 ? launch<D, true, false>(p, mq, mk, mv, sms, stream)
+                               : launch<D, false, false>(p, mq, mk, mv, sms, stream);
 }
 
 }  // namespace
@@ -1188,13 +1312,14 @@ cudaError_t launch_paged_attention(const PagedAttentionParams& p, cudaStream_t s
   if (err == cudaSuccess)
     err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (err != cudaSuccess) return err;
-  CUtensorMap mk, mv;
+  CUtensorMap mq = {}, mk, mv;
   const dspark_paged_kv& kv = p.kv;
   if (!make_map(&mk, kv.k, kv, kv.k_block_stride, kv.k_head_stride, kv.k_token_stride) ||
       !make_map(&mv, kv.v, kv, kv.v_block_stride, kv.v_head_stride, kv.v_token_stride))
     return cudaErrorInvalidValue;
-  return kv.head_dim == 64 ? launch_dim<64>(p, mk, mv, sms, stream)
-                           : launch_dim<128>(p, mk, mv, sms, stream);
+  if (kv.dtype != DSPARK_E4M3 && !make_q_map(&mq, p)) return cudaErrorInvalidValue;
+  return kv.head_dim == 64 ? launch_dim<64>(p, mq, mk, mv, sms, stream)
+                           : launch_dim<128>(p, mq, mk, mv, sms, stream);
 }
 
 }  // namespace dspark
