@@ -184,6 +184,12 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+__device__ __forceinline__ bool elect_one() {  // one lane of a converged warp
+  uint32_t p;
+  asm volatile("{ .reg .pred q; elect.sync _|q, 0xFFFFFFFF; selp.u32 %0, 1, 0, q; }" : "=r"(p));
+  return p != 0;
+}
+
 // D[tmem] (+)= A * B^T, kind::f16, A from shared (ss) or tensor (ts) memory.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                        uint32_t acc) {
@@ -653,14 +659,14 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
 #pragma unroll
             for (int c = 0; c < D / 8; ++c)
               *reinterpret_cast<uint4*>(v_s + (c >> 3) * (kKeys * 128) + row * 128 +
-                                        ((c & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                                        (((c ^ row) & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
           } else if (scan && (key >= all_hi || key < all_lo)) {
             constexpr uint32_t kInf = kF16 ? 0x7C00u : 0x7F80u;
             bool bad = false;
 #pragma unroll
             for (int c = 0; c < D / 8; ++c) {
               const uint4 v = *reinterpret_cast<const uint4*>(
-                  v_s + (c >> 3) * (kKeys * 128) + row * 128 + ((c & 7) << 4));
+                  v_s + (c >> 3) * (kKeys * 128) + row * 128 + (((c ^ row) & 7) << 4));
               const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
               for (int e = 0; e < 4; ++e)
@@ -1009,32 +1015,35 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
           (void)mbar_wait(&m->q_full[i & 1], (i >> 1) & 1, P.status);
     } else if (warp == 9) {
       // ---- MMA issuer ------------------------------------------------------------------
-      if (lane == 0) {
-        constexpr uint32_t id_pv = idesc_of(!kF16, true, D);
-        // (a negative scale is a negated A; the scouts of an 8-bit cache see to it)
-        const uint32_t id_qk = idesc_of(!kF16, false, kKeys) |
-                               (!kQuant && P.scale < 0.f ? 1u << 13 : 0u);
-        const uint64_t q_desc = tc::sw128_kmajor_desc(smem_addr(smem + C::q));
-        const uint64_t k_desc = tc::sw128_kmajor_desc(smem_addr(smem + C::kv));
-        const uint64_t v_desc = sw128_mnmajor_desc(smem_addr(smem + C::kv));
-        uint32_t base = 0, n_q = 0, n_item[2] = {0, 0};
-        bool ok = true;
-        while (ok) {
-          if (!wait_on(&m->q_full[n_q & 1], (n_q >> 1) & 1, fail, P.status)) break;
-          const Seg s = m->seg[n_q & 1];
-          if (s.end) break;
-          const uint32_t n_q1 = n_q + 1;
-          if (s.pair && !wait_on(&m->q_full[n_q1 & 1], (n_q1 >> 1) & 1, fail, P.status)) break;
+      // The whole warp runs the loop, so that descriptors stay in uniform
+      // registers; one elected lane issues.
+      constexpr uint32_t id_pv = idesc_of(!kF16, true, D);
+      // (a negative scale is a negated A; the scouts of an 8-bit cache see to it)
+      const uint32_t id_qk = idesc_of(!kF16, false, kKeys) |
+                             (!kQuant && P.scale < 0.f ? 1u << 13 : 0u);
+      const bool leader = elect_one();
+      const uint64_t q_desc = tc::sw128_kmajor_desc(smem_addr(smem + C::q));
+      const uint64_t k_desc = tc::sw128_kmajor_desc(smem_addr(smem + C::kv));
+      const uint64_t v_desc = sw128_mnmajor_desc(smem_addr(smem + C::kv));
+      uint32_t base = 0, n_q = 0, n_item0 = 0, n_item1 = 0;
+      bool ok = true;
+      while (ok) {
+        if (!wait_warp(&m->q_full[n_q & 1], (n_q >> 1) & 1, fail, P.status)) break;
+        const Seg s = m->seg[n_q & 1];
+        if (s.end) break;
+        const uint32_t n_q1 = n_q + 1;
+        if (s.pair && !wait_warp(&m->q_full[n_q1 & 1], (n_q1 >> 1) & 1, fail, P.status)) break;
+        tc::fence_after_thread_sync();
+        const int nt = s.tiles(), ni = s.pair ? 2 * nt : nt;
+        auto scores = [&](int i) -> bool {  // S_w = Q K^T of item i
+          const int w = i & 1, t = s.pair ? i >> 1 : i;
+          const uint32_t ki = base + s.k_place(s.j0 + t), st = ki % C::kStages;
+          if (!wait_warp(&m->kv_full[st], (ki / C::kStages) & 1, fail, P.status)) return false;
           tc::fence_after_thread_sync();
-          const int nt = s.tiles(), ni = s.pair ? 2 * nt : nt;
-          auto scores = [&](int i) -> bool {  // S_w = Q K^T of item i
-            const int w = i & 1, t = s.pair ? i >> 1 : i;
-            const uint32_t ki = base + s.k_place(s.j0 + t), st = ki % C::kStages;
-            if (!wait_on(&m->kv_full[st], (ki / C::kStages) & 1, fail, P.status)) return false;
-            tc::fence_after_thread_sync();
-            const uint32_t sl = (n_q + (s.pair ? w : 0)) & 1;
-            const uint64_t qd = q_desc + static_cast<uint32_t>((sl * C::kTileBytes) >> 4);
-            const uint64_t kd = k_desc + static_cast<uint32_t>((st * C::kTileBytes) >> 4);
+          const uint32_t sl = (n_q + (s.pair ? w : 0)) & 1;
+          const uint64_t qd = q_desc + static_cast<uint32_t>((sl * C::kTileBytes) >> 4);
+          const uint64_t kd = k_desc + static_cast<uint32_t>((st * C::kTileBytes) >> 4);
+          if (leader) {
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
               const uint32_t off = ((c >> 2) * (kRows * 128) + (c & 3) * 32) >> 4;
@@ -1043,41 +1052,47 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
             if (!s.pair || w == 1) tc::mma_commit(&m->kv_empty[st]);
             if (t == nt - 1) tc::mma_commit(&m->q_empty[sl]);
             tc::mma_commit(&m->s_full[w]);
-            return true;
-          };
-          for (int i = 0; i < 2 && i < ni && ok; ++i) ok = scores(i);
-          for (int i = 0; i < ni && ok; ++i) {  // O_w += P_w V of item i, in two halves
-            const int w = i & 1, t = s.pair ? i >> 1 : i;
-            const uint32_t vi = base + s.v_place(s.j0 + t), st = vi % C::kStages;
-            const uint64_t vd = v_desc + static_cast<uint32_t>((st * C::kTileBytes) >> 4);
-            if (!(ok = wait_on(&m->kv_full[st], (vi / C::kStages) & 1, fail, P.status))) break;
-            bool skip = false;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              uint64_t* bar = half ? &m->p_ready[w] : &m->p_half[w];
-              if (!(ok = wait_on(bar, n_item[w] & 1, fail, P.status))) break;
-              tc::fence_after_thread_sync();
-              if (half == 0)
-                skip = *reinterpret_cast<volatile int*>(&m->skip_pv[w]) ==
-                       static_cast<int>(n_item[w]);
-              if (!skip) {
-#pragma unroll
-                for (int c = half * 4; c < half * 4 + 4; ++c)
-                  mma_ts(tmem + 256 + w * 128, tmem + w * kKeys + c * 8, vd + ((c * 2048) >> 4),
-                         id_pv, i >= 2 || c != 0);
-              }
-            }
-            if (!ok) break;
-            ++n_item[w];
-            if (!s.pair || w == 1) tc::mma_commit(&m->kv_empty[st]);
-            if (i + 2 < ni)
-              ok = scores(i + 2);
-            else
-              tc::mma_commit(&m->o_full[w]);
           }
-          base += 2 * nt;
-          n_q += s.pair ? 2 : 1;
+          __syncwarp();
+          return true;
+        };
+        for (int i = 0; i < 2 && i < ni && ok; ++i) ok = scores(i);
+        for (int i = 0; i < ni && ok; ++i) {  // O_w += P_w V of item i, in two halves
+          const int w = i & 1, t = s.pair ? i >> 1 : i;
+          const uint32_t vi = base + s.v_place(s.j0 + t), st = vi % C::kStages;
+          const uint64_t vd = v_desc + static_cast<uint32_t>((st * C::kTileBytes) >> 4);
+          if (!(ok = wait_warp(&m->kv_full[st], (vi / C::kStages) & 1, fail, P.status))) break;
+          const uint32_t n = w ? n_item1 : n_item0;
+          bool skip = false;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint64_t* bar = half ? &m->p_ready[w] : &m->p_half[w];
+            if (!(ok = wait_warp(bar, n & 1, fail, P.status))) break;
+            tc::fence_after_thread_sync();
+            if (half == 0)
+              skip = *reinterpret_cast<volatile int*>(&m->skip_pv[w]) == static_cast<int>(n);
+            if (leader && !skip) {
+#pragma unroll
+              for (int c = half * 4; c < half * 4 + 4; ++c)
+                mma_ts(tmem + 256 + w * 128, tmem + w * kKeys + c * 8, vd + ((c * 2048) >> 4),
+                       id_pv, i >= 2 || c != 0);
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+          n_item0 += w == 0;
+          n_item1 += w == 1;
+          if (leader) {
+            if (!s.pair || w == 1) tc::mma_commit(&m->kv_empty[st]);
+            if (i + 2 >= ni) tc::mma_commit(&m->o_full[w]);
+          }
+          __syncwarp();
+          if (i + 2 < ni) ok = scores(i + 2);
         }
+        base += 2 * nt;
+        n_q += s.pair ? 2 : 1;
+      }
+      if (leader) {
         tc::mma_commit(&m->drain);
         (void)mbar_wait(&m->drain, 0, P.status);
       }
