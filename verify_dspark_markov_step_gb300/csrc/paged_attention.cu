@@ -27,15 +27,18 @@
 // without atomics. A unit that a run's ends cut is written as partial (O, r, l)
 // per CTA and joined by paged_join_kernel in a fixed order.
 //
-// Warps: 0-3 and 4-7 softmax (thread = row = lane of tensor memory), 8 TMA
-// producer of the keys, 9 MMA issuer, 10 TMA producer of the values, 11 the
-// scout: it walks the units ahead of the others, loads their query rows (a ring
-// of two row tiles) and publishes what the others need to know of them. With an
-// 8-bit cache 8 loads keys and values, 10-11 are the scouts (query rows are
-// brought to fp16 by a power of two per row), and 12-15 convert e4m3 tiles to
-// fp16 in shared memory (the 8-bit values are exact in fp16; an 8-bit MMA would
-// want the queries and p in 8 bits too). Pages: a 128-key tile is
-// 128 / page_size TMA boxes.
+// Warps: 0-3 and 4-7 softmax (thread = row = lane of tensor memory), 9 issues
+// the MMAs (the warpgroups' in turn, which keeps one's softmax beside the other's
+// products; waits and commits cost it time that the tensor core then idles, so
+// an item has two waits and one commit, and the softmax warps release what the
+// committed MMAs have read), 8 and 12
+// are the TMA producers (keys and values go through one ring; each issues half of
+// a tile's boxes), 11 the scout: it walks the units ahead of the others, loads
+// their query rows (a ring of two row tiles) and publishes what the others need
+// to know of them. With an 8-bit cache 8 loads alone, the scout brings query rows to fp16 by a power of two per row, and
+// 12-15 convert e4m3 tiles to fp16 in shared memory (the 8-bit values are exact
+// in fp16; an 8-bit MMA would want the queries and p in 8 bits too). Pages: a
+// 128-key tile is 128 / page_size TMA boxes.
 //
 // What a row does not see must not reach it: masked scores are replaced (not
 // added to), value rows past the request's last token are zeroed in shared
@@ -72,9 +75,9 @@ struct Cfg {
   static constexpr int kRawBytes = kKeys * D;               // 128 x D in 8 bits
   static constexpr int kStages = kQuant ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 10);
   static constexpr int kRaw = kQuant ? (D == 128 ? 3 : 6) : 0;
-  static constexpr int kThreads = kQuant ? 512 : 384;
-  // registers a thread after the split (the launch gives 128 or 168 to each)
-  static constexpr int kSoftmaxRegs = kQuant ? 184 : 216;
+  static constexpr int kThreads = 512;
+  // registers a thread after the split: 2 x 184 + 2 x 72 = the launch's 4 x 128
+  static constexpr int kSoftmaxRegs = 184;
   static constexpr int kOtherRegs = 72;
   // shared memory, offsets from a 1024-byte aligned base
   static constexpr int q = 0;
@@ -124,7 +127,7 @@ struct Misc {
   Seg seg[2];  // of the segment whose first row tile is in the slot
   uint32_t tmem;
   int fail;
-  int copies[kMaxStages];  // copies made into each stage of the TMA ring
+  uint32_t filling;  // tiles of the MMA's ring whose stage is being filled, or was
   int bad[2];      // the last tile whose values were found non-finite, per warpgroup
   int skip_pv[2];  // the last item whose P V the warpgroup did itself
   int start_b, per;
@@ -182,6 +185,13 @@ __device__ __forceinline__ uint32_t tmem_ld1(uint32_t a) {
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+template <int kCount>
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)),
+               "n"(kCount)
+               : "memory");
 }
 
 __device__ __forceinline__ bool elect_one() {  // one lane of a converged warp
@@ -284,6 +294,38 @@ __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t phase, volatile 
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t phase, volatile int* fail,
                                           int32_t* status) {
   return __all_sync(0xFFFFFFFFu, wait_on(bar, phase, fail, status));
+}
+
+// Two barriers at once (their latencies overlap when both are through).
+__device__ __forceinline__ bool wait_warp2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb,
+                                           volatile int* fail, int32_t* status) {
+  const bool ra = mbar_try_wait(a, pa), rb = mbar_try_wait(b, pb);
+  if (__all_sync(0xFFFFFFFFu, ra && rb)) return true;
+  return wait_warp(a, pa, fail, status) && wait_warp(b, pb, fail, status);
+}
+
+// A softmax warp's wait for tile n of a ring of kStages. A barrier only tells the
+// parity of its phase, and this waiter has not seen every one before (as the MMA
+// warp and the producers have), so the wait begins when the tile's stage is being
+// filled, from when on the parity is unambiguous.
+template <int kStages>
+__device__ __forceinline__ bool wait_tile(Misc* m, uint32_t n, int32_t* status) {
+  volatile int* fail = &m->fail;
+  bool ok = true;
+  if (static_cast<int>(*const_cast<volatile uint32_t*>(&m->filling) - n) <= 0) {
+    const unsigned long long t0 = globaltimer_ns();
+    do {
+      __nanosleep(20);
+      if (*fail) ok = false;
+      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        report(status, DSPARK_ERR_TIMEOUT);
+        *fail = 1;
+        ok = false;
+      }
+    } while (ok && static_cast<int>(*const_cast<volatile uint32_t*>(&m->filling) - n) <= 0);
+  }
+  ok = ok && wait_on(&m->kv_full[n % kStages], (n / kStages) & 1, fail, status);
+  return __all_sync(0xFFFFFFFFu, ok);
 }
 
 // ---- the units of work -------------------------------------------------------------
@@ -483,8 +525,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
 
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(&m->kv_full[i], kQuant ? 4 : 1);
-      mbar_init(&m->kv_empty[i], 1);
+      mbar_init(&m->kv_full[i], kQuant ? 4 : 2);
+      mbar_init(&m->kv_empty[i], 2);
     }
     for (int i = 0; i < C::kRaw; ++i) {
       mbar_init(&m->raw_full[i], 1);
@@ -492,15 +534,15 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(&m->s_full[w], 1);
-      mbar_init(&m->q_full[w], kQuant ? 2 : 1);
-      mbar_init(&m->q_empty[w], 9);  // the MMAs, eight softmax warps
+      mbar_init(&m->q_full[w], 1);
+      mbar_init(&m->q_empty[w], 8);  // the softmax warps
       mbar_init(&m->p_half[w], 4);
       mbar_init(&m->p_ready[w], 4);
       mbar_init(&m->o_full[w], 1);
       mbar_init(&m->scanned[w], 4);
       m->bad[w] = m->skip_pv[w] = -1;
     }
-    for (int i = 0; i < kMaxStages; ++i) m->copies[i] = 0;
+    m->filling = 0;
     mbar_init(&m->merge, 4);
     mbar_init(&m->merged, 4);
     mbar_init(&m->drain, 1);
@@ -542,13 +584,16 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
       if (s.pair && !(ok = wait_warp(&m->q_full[n_q1 & 1], (n_q1 >> 1) & 1, fail, P.status))) break;
       float sl = sl0 * (P.kv.k_scale ? P.kv.k_scale[s.h] : 1.f);
       if constexpr (kQuant) sl *= row_scale[((n_q + (s.pair ? w : 0)) & 1) * kRows + row];
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&m->q_empty[n_q & 1]);
-        if (s.pair) mbar_arrive(&m->q_empty[n_q1 & 1]);
-      }
-      n_q += s.pair ? 2 : 1;
       const int items = s.items(w);
+      // one thread of the warpgroup gives back what its MMAs have read: a tile
+      // once, or twice where the other warpgroup has no use for it
+      const bool giver = (warp & 3) == 0 && lane == 0;
+      auto give_tile = [&](uint32_t n) {
+        if (s.pair)
+          mbar_arrive(&m->kv_empty[n % C::kStages]);
+        else
+          mbar_arrive_n<2>(&m->kv_empty[n % C::kStages]);
+      };
       const bool split = !(s.opens && s.closes);
       const int first = s.t0 + (s.pair ? w * tp : 0);       // first token of the row tile
       const int ntok = min(tp, s.t1 - first);
@@ -567,6 +612,11 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         const int key0 = s.tile(w, k) * kKeys;
         if (!(ok = wait_warp(&m->s_full[w], n_item & 1, fail, P.status))) break;
         tc::fence_after_thread_sync();
+        if (giver) {  // these scores are there: the keys, and the values before
+          give_tile(base + s.k_place(s.tile(w, k)));
+          if (k > 0) give_tile(base + s.v_place(s.tile(w, k - 1)));
+        }
+        __syncwarp();
         bool scan = false, tail = false;
         const bool masked = key0 < all_lo || key0 + kKeys > all_hi;
         if (masked) {
@@ -585,8 +635,14 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
           if (masked) {
             const int clo = lo - key0, chi = hi - key0;
 #pragma unroll
-            for (int c = 0; c < kKeys; ++c)
-              if (c < clo || c >= chi) x[c] = 0xFF800000u;
+            for (int g = 0; g < kKeys; g += 32) {  // bit c: the row sees key g + c
+              const int a = min(max(clo - g, 0), 32), z = min(max(chi - g, 0), 32);
+              const uint32_t below = z == 32 ? 0xFFFFFFFFu : (1u << z) - 1u;
+              const uint32_t sees = a == 32 ? 0u : below >> a << a;
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!(sees >> c & 1u)) x[g + c] = 0xFF800000u;
+            }
           }
           float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
@@ -652,8 +708,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
           // that some row does not see takes P V off the tensor core
           const uint32_t vi = base + s.v_place(s.tile(w, k));
           unsigned char* v_s = smem + C::kv + (vi % C::kStages) * C::kTileBytes;
-          if (!(ok = wait_warp(&m->kv_full[vi % C::kStages], (vi / C::kStages) & 1, fail, P.status)))
-            break;
+          if (!(ok = wait_tile<C::kStages>(m, vi, P.status))) break;
           const int key = key0 + row;
           if (key >= s.r.len) {
 #pragma unroll
@@ -743,12 +798,20 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         }
       }
       if (!ok) break;
-      base += 2 * s.tiles();
       if (items > 0) {
         if (!(ok = wait_warp(&m->o_full[w], n_seg & 1, fail, P.status))) break;
         tc::fence_after_thread_sync();
         ++n_seg;
+        if (giver) give_tile(base + s.v_place(s.tile(w, items - 1)));
       }
+      base += 2 * s.tiles();
+      // the query rows and the segment's description (every warp has its copy)
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&m->q_empty[n_q & 1]);
+        if (s.pair) mbar_arrive(&m->q_empty[n_q1 & 1]);
+      }
+      n_q += s.pair ? 2 : 1;
       // ---- the segment's result -----------------------------------------------------
       const bool joined = !s.pair && s.items(1) > 0;
       if (!s.pair && w == 1) {
@@ -851,7 +914,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
       reinterpret_cast<JoinDesc*>(wsp + ws.desc)[blockIdx.x].parts = 0;
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
-    if (warp == 8 || (!kQuant && warp == 10)) {
+    if (warp == 8 || (!kQuant && warp == 12)) {
       // ---- TMA producers: keys and values of the segments' tiles, page by page -------
       const uint64_t pol = policy_evict_normal();
       constexpr uint32_t kRing = kQuant ? C::kRaw : C::kStages;
@@ -861,7 +924,13 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
       unsigned char* ring = smem + (kQuant ? C::raw : C::kv);
       const int page = 1 << P.page_shift;
       const int box = page < kKeys ? page : kKeys;  // tokens of a TMA box
-      const int boxes = kKeys / box;                // boxes of a tile (<= 8)
+      const int boxes = kKeys / box;                // boxes of a tile's 128 bytes of width
+      // this warp's boxes: every second one, one to a lane (8-bit: all)
+      const int pi = kQuant ? 0 : warp == 12;
+      const int bi = kQuant ? lane : 2 * lane + pi;
+      const int nb = boxes * (kQuant ? 1 : C::kHalves);
+      const int mine = kQuant ? nb : (nb + 1 - pi) / 2;
+      const int bc = bi / boxes, bk = (bi - bc * boxes) * box;  // half of the row, first key
       uint32_t base = 0;                            // tiles loaded before this segment
       bool ok = true;
       Walk walk(P, m, tp);
@@ -873,8 +942,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         // this lane's page of tile j; num_blocks (which TMA reads as zeros) where
         // there is nothing to see
         auto page_of = [&](int j) -> int {
-          const int key = j * kKeys + lane * box;
-          if (lane >= boxes || key >= hi || key + box <= lo) return P.kv.num_blocks;
+          const int key = j * kKeys + bk;
+          if (bi >= nb || key >= hi || key + box <= lo) return P.kv.num_blocks;
           const int id = P.block_table[row0 + (key >> P.page_shift)];
           if (id >= 0 && id < P.kv.num_blocks) return id;
           report(P.status, DSPARK_ERR_BOUNDS);
@@ -883,48 +952,35 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         auto load = [&](const CUtensorMap* map, int j, int id, int place) -> bool {
           const uint32_t n = base + place, st = n % kRing, ph = (n / kRing) & 1;
           if (!wait_warp(&empty[st], ph ^ 1, fail, P.status)) return false;
-          if (lane == 0) mbar_arrive_expect_tx(&full[st], kBytes);
-          __syncwarp();
-          if (lane < boxes) {
-            unsigned char* dst = ring + st * kBytes;
-            const int y = (j * kKeys + lane * box) & (page - 1);
-            if constexpr (kQuant) {
-              tma_load_4d(dst + lane * box * D, map, 0, y, s.h, id, &full[st], pol);
-            } else {
-#pragma unroll
-              for (int c = 0; c < C::kHalves; ++c)
-                tma_load_4d(dst + c * (kKeys * 128) + lane * box * 128, map, c * 64, y, s.h, id,
-                            &full[st], pol);
-            }
+          if (lane == 0) {
+            if (!kQuant && pi == 0) *const_cast<volatile uint32_t*>(&m->filling) = n + 1;
+            if (mine > 0)
+              mbar_arrive_expect_tx(&full[st], mine * box * (kQuant ? D : 128));
+            else
+              mbar_arrive(&full[st]);
           }
-          if (lane == 0) m->copies[st] = static_cast<int>(n / kRing) + 1;
+          __syncwarp();
+          if (bi < nb) {
+            const int y = (j * kKeys + bk) & (page - 1);
+            unsigned char* dst = ring + st * kBytes + bk * (kQuant ? D : 128);
+            tma_load_4d(dst + bc * (kKeys * 128), map, bc * 64, y, s.h, id, &full[st], pol);
+          }
           return true;
         };
         // the pages of a tile are looked up a tile before it is due
-        const int nt = s.tiles();
-        int id_next = page_of(s.j0);
-        if constexpr (kQuant) {  // keys `a` tiles ahead of the values
-          const int a = s.ahead();
-          int id_v0 = 0, id_v1 = 0;  // of the tiles one and two before
-          for (int i = 0; i < nt + a && ok; ++i) {
-            const int j = s.j0 + i, id_k = id_next;
-            if (i + 1 < nt) id_next = page_of(j + 1);
-            if (i >= a) ok = load(&tmap_v, j - a, a == 2 ? id_v1 : id_v0, s.v_place(j - a));
-            if (ok && i < nt) ok = load(&tmap_k, j, id_k, s.k_place(j));
-            id_v1 = id_v0;
-            id_v0 = id_k;
-          }
-        } else {
-          const CUtensorMap* map = warp == 8 ? &tmap_k : &tmap_v;
-          for (int j = s.j0; j < s.j1 && ok; ++j) {
-            const int id = id_next;
-            if (j + 1 < s.j1) id_next = page_of(j + 1);
-            ok = load(map, j, id, warp == 8 ? s.k_place(j) : s.v_place(j));
-          }
+        const int nt = s.tiles(), a = s.ahead();  // keys `a` tiles ahead of the values
+        int id_next = page_of(s.j0), id_v0 = 0, id_v1 = 0;  // of the tiles one and two before
+        for (int i = 0; i < nt + a && ok; ++i) {
+          const int j = s.j0 + i, id_k = id_next;
+          if (i + 1 < nt) id_next = page_of(j + 1);
+          if (i >= a) ok = load(&tmap_v, j - a, a == 2 ? id_v1 : id_v0, s.v_place(j - a));
+          if (ok && i < nt) ok = load(&tmap_k, j, id_k, s.k_place(j));
+          id_v1 = id_v0;
+          id_v0 = id_k;
         }
         base += 2 * nt;
       }
-    } else if (warp == 11 || (kQuant && warp == 10)) {
+    } else if (warp == 11) {
       // ---- scout: segments and their query rows ---------------------------------------
       uint32_t n_q = 0;
       bool ok = true;
@@ -937,7 +993,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         for (int f = 0; f < fills && ok; ++f, ++n_q) {
           const uint32_t sl = n_q & 1;
           if (!(ok = wait_warp(&m->q_empty[sl], ((n_q >> 1) & 1) ^ 1, fail, P.status))) break;
-          if (f == 0 && warp == 11 && lane == 0) m->seg[sl] = s;
+          if (f == 0 && lane == 0) m->seg[sl] = s;
           const int tok0 = s.r.q0 + s.t0 + f * tp;
           if constexpr (!kQuant) {
             if (lane == 0) {
@@ -960,11 +1016,11 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
             const uint32_t flip = P.scale < 0.f ? 0x80008000u : 0u;
             constexpr int kBatch = 4;
             const int total = nrow * (D / 8);
-            for (int i0 = (warp - 10) * 32 + lane; i0 < total; i0 += 64 * kBatch) {
+            for (int i0 = lane; i0 < total; i0 += 32 * kBatch) {
               uint4 x[kBatch];
 #pragma unroll
               for (int e = 0; e < kBatch; ++e) {
-                const int i = i0 + 64 * e, rr = i / (D / 8), c = i % (D / 8);
+                const int i = i0 + 32 * e, rr = i / (D / 8), c = i % (D / 8);
                 const int tk = rr / G, g = rr - tk * G;
                 if (i < total)
                   x[e] = __ldg(reinterpret_cast<const uint4*>(
@@ -973,7 +1029,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
               }
 #pragma unroll
               for (int e = 0; e < kBatch; ++e) {
-                const int i = i0 + 64 * e, rr = i / (D / 8), c = i % (D / 8);
+                const int i = i0 + 32 * e, rr = i / (D / 8), c = i % (D / 8);
                 if (i >= total) break;
                 uint32_t xw[4] = {x[e].x ^ flip, x[e].y ^ flip, x[e].z ^ flip, x[e].w ^ flip};
                 float v[8];
@@ -1009,16 +1065,12 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         }
         if (!more || !ok) break;
       }
-      // the copies have landed before the CTA may exit
-      if (!kQuant && lane == 0)
-        for (uint32_t i = n_q > 2 ? n_q - 2 : 0; i < n_q; ++i)
-          (void)mbar_wait(&m->q_full[i & 1], (i >> 1) & 1, P.status);
     } else if (warp == 9) {
       // ---- MMA issuer ------------------------------------------------------------------
       // The whole warp runs the loop, so that descriptors stay in uniform
       // registers; one elected lane issues.
       constexpr uint32_t id_pv = idesc_of(!kF16, true, D);
-      // (a negative scale is a negated A; the scouts of an 8-bit cache see to it)
+      // (a negative scale is a negated A; the scout of an 8-bit cache sees to it)
       const uint32_t id_qk = idesc_of(!kF16, false, kKeys) |
                              (!kQuant && P.scale < 0.f ? 1u << 13 : 0u);
       const bool leader = elect_one();
@@ -1035,59 +1087,69 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         if (s.pair && !wait_warp(&m->q_full[n_q1 & 1], (n_q1 >> 1) & 1, fail, P.status)) break;
         tc::fence_after_thread_sync();
         const int nt = s.tiles(), ni = s.pair ? 2 * nt : nt;
-        auto scores = [&](int i) -> bool {  // S_w = Q K^T of item i
-          const int w = i & 1, t = s.pair ? i >> 1 : i;
-          const uint32_t ki = base + s.k_place(s.j0 + t), st = ki % C::kStages;
-          if (!wait_warp(&m->kv_full[st], (ki / C::kStages) & 1, fail, P.status)) return false;
-          tc::fence_after_thread_sync();
+        auto keys_of = [&](int i) { return base + s.k_place(s.j0 + (s.pair ? i >> 1 : i)); };
+        auto scores = [&](int i, uint32_t ki) {  // S_w = Q K^T of item i
+          const int w = i & 1;
           const uint32_t sl = (n_q + (s.pair ? w : 0)) & 1;
           const uint64_t qd = q_desc + static_cast<uint32_t>((sl * C::kTileBytes) >> 4);
-          const uint64_t kd = k_desc + static_cast<uint32_t>((st * C::kTileBytes) >> 4);
-          if (leader) {
+          const uint64_t kd =
+              k_desc + static_cast<uint32_t>(((ki % C::kStages) * C::kTileBytes) >> 4);
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
-              const uint32_t off = ((c >> 2) * (kRows * 128) + (c & 3) * 32) >> 4;
-              mma_ss(tmem + w * kKeys, qd + off, kd + off, id_qk, c != 0);
-            }
-            if (!s.pair || w == 1) tc::mma_commit(&m->kv_empty[st]);
-            if (t == nt - 1) tc::mma_commit(&m->q_empty[sl]);
-            tc::mma_commit(&m->s_full[w]);
+          for (int c = 0; c < D / 16; ++c) {
+            const uint32_t off = ((c >> 2) * (kRows * 128) + (c & 3) * 32) >> 4;
+            mma_ss(tmem + w * kKeys, qd + off, kd + off, id_qk, c != 0);
+          }
+          tc::mma_commit(&m->s_full[w]);
+        };
+        for (int i = 0; i < 2 && i < ni; ++i) {
+          const uint32_t ki = keys_of(i);
+          if (!(ok = wait_warp(&m->kv_full[ki % C::kStages], (ki / C::kStages) & 1, fail,
+                               P.status)))
+            break;
+          tc::fence_after_thread_sync();
+          if (leader) scores(i, ki);
+          __syncwarp();
+        }
+        for (int i = 0; i < ni && ok; ++i) {  // O_w += P_w V of item i, in two halves
+          const int w = i & 1;
+          const uint32_t vi = base + s.v_place(s.j0 + (s.pair ? i >> 1 : i));
+          const uint32_t n = w ? n_item1 : n_item0;
+          if (!(ok = wait_warp2(&m->kv_full[vi % C::kStages], (vi / C::kStages) & 1, &m->p_half[w],
+                                n & 1, fail, P.status)))
+            break;
+          tc::fence_after_thread_sync();
+          const bool skip = *reinterpret_cast<volatile int*>(&m->skip_pv[w]) == static_cast<int>(n);
+          const uint64_t vd =
+              v_desc + static_cast<uint32_t>(((vi % C::kStages) * C::kTileBytes) >> 4);
+          const uint32_t o_d = tmem + 256 + w * 128, p_d = tmem + w * kKeys;
+          if (leader && !skip) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              mma_ts(o_d, p_d + c * 8, vd + ((c * 2048) >> 4), id_pv, i >= 2 || c != 0);
           }
           __syncwarp();
-          return true;
-        };
-        for (int i = 0; i < 2 && i < ni && ok; ++i) ok = scores(i);
-        for (int i = 0; i < ni && ok; ++i) {  // O_w += P_w V of item i, in two halves
-          const int w = i & 1, t = s.pair ? i >> 1 : i;
-          const uint32_t vi = base + s.v_place(s.j0 + t), st = vi % C::kStages;
-          const uint64_t vd = v_desc + static_cast<uint32_t>((st * C::kTileBytes) >> 4);
-          if (!(ok = wait_warp(&m->kv_full[st], (vi / C::kStages) & 1, fail, P.status))) break;
-          const uint32_t n = w ? n_item1 : n_item0;
-          bool skip = false;
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint64_t* bar = half ? &m->p_ready[w] : &m->p_half[w];
-            if (!(ok = wait_warp(bar, n & 1, fail, P.status))) break;
-            tc::fence_after_thread_sync();
-            if (half == 0)
-              skip = *reinterpret_cast<volatile int*>(&m->skip_pv[w]) == static_cast<int>(n);
-            if (leader && !skip) {
-#pragma unroll
-              for (int c = half * 4; c < half * 4 + 4; ++c)
-                mma_ts(tmem + 256 + w * 128, tmem + w * kKeys + c * 8, vd + ((c * 2048) >> 4),
-                       id_pv, i >= 2 || c != 0);
-            }
-            __syncwarp();
-          }
+          // the second half, and the warpgroup's next scores
+          const bool more = i + 2 < ni;
+          const uint32_t ki = keys_of(more ? i + 2 : i);
+          ok = more ? wait_warp2(&m->kv_full[ki % C::kStages], (ki / C::kStages) & 1,
+                                 &m->p_ready[w], n & 1, fail, P.status)
+                    : wait_warp(&m->p_ready[w], n & 1, fail, P.status);
           if (!ok) break;
+          tc::fence_after_thread_sync();
+          if (leader) {
+            if (!skip) {
+#pragma unroll
+              for (int c = 4; c < 8; ++c)
+                mma_ts(o_d, p_d + c * 8, vd + ((c * 2048) >> 4), id_pv, 1);
+            }
+            if (more)
+              scores(i + 2, ki);
+            else
+              tc::mma_commit(&m->o_full[w]);
+          }
+          __syncwarp();
           n_item0 += w == 0;
           n_item1 += w == 1;
-          if (leader) {
-            if (!s.pair || w == 1) tc::mma_commit(&m->kv_empty[st]);
-            if (i + 2 >= ni) tc::mma_commit(&m->o_full[w]);
-          }
-          __syncwarp();
-          if (i + 2 < ni) ok = scores(i + 2);
         }
         base += 2 * nt;
         n_q += s.pair ? 2 : 1;
@@ -1121,6 +1183,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
           if (!wait_warp(&m->kv_empty[st], (static_cast<uint32_t>(n / C::kStages) & 1) ^ 1, fail,
                        P.status))
             break;
+          if (ct == 0) *const_cast<volatile uint32_t*>(&m->filling) = static_cast<uint32_t>(n) + 1;
           unsigned char* dst = smem + C::kv + st * C::kTileBytes + ct * 128;
 #pragma unroll
           for (int c = 0; c < kChunks; ++c) {
@@ -1148,11 +1211,11 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     tc::fence_after_thread_sync();
     tc::tmem_dealloc(tmem, 512);
   }
-  if (tid == 0) {  // every copy has landed before the CTA exits
-    for (int i = 0; i < (kQuant ? C::kRaw : C::kStages); ++i)
-      if (m->copies[i] > 0)
-        (void)mbar_wait(kQuant ? &m->raw_full[i] : &m->kv_full[i], (m->copies[i] - 1) & 1,
-                        P.status);
+  // Every copy was waited for by the MMAs that read it; after a failed wait some
+  // may still be on their way: they land before the CTA exits.
+  if (tid == 0 && *fail) {
+    const unsigned long long t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
   }
 }
 
