@@ -31,7 +31,7 @@
 // the MMAs (the warpgroups' in turn, which keeps one's softmax beside the other's
 // products; waits and commits cost it time that the tensor core then idles, so
 // an item has two waits and one commit, and the softmax warps release what the
-// committed MMAs have read), 8 and 12
+// committed MMAs have read), 8 and 10
 // are the TMA producers (keys and values go through one ring; each issues half of
 // a tile's boxes), 11 the scout: it walks the units ahead of the others, loads
 // their query rows (a ring of two row tiles) and publishes what the others need
@@ -75,9 +75,10 @@ struct Cfg {
   static constexpr int kRawBytes = kKeys * D;               // 128 x D in 8 bits
   static constexpr int kStages = kQuant ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 10);
   static constexpr int kRaw = kQuant ? (D == 128 ? 3 : 6) : 0;
-  static constexpr int kThreads = 512;
-  // registers a thread after the split: 2 x 184 + 2 x 72 = the launch's 4 x 128
-  static constexpr int kSoftmaxRegs = 184;
+  static constexpr int kThreads = kQuant ? 512 : 384;
+  // registers a thread after the split: 2 x 216 + 72 = the launch's 3 x 168, or
+  // 2 x 184 + 2 x 72 = 4 x 128
+  static constexpr int kSoftmaxRegs = kQuant ? 184 : 216;
   static constexpr int kOtherRegs = 72;
   // shared memory, offsets from a 1024-byte aligned base
   static constexpr int q = 0;
@@ -914,7 +915,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
       reinterpret_cast<JoinDesc*>(wsp + ws.desc)[blockIdx.x].parts = 0;
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
-    if (warp == 8 || (!kQuant && warp == 12)) {
+    if (warp == 8 || (!kQuant && warp == 10)) {
       // ---- TMA producers: keys and values of the segments' tiles, page by page -------
       const uint64_t pol = policy_evict_normal();
       constexpr uint32_t kRing = kQuant ? C::kRaw : C::kStages;
@@ -926,7 +927,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
       const int box = page < kKeys ? page : kKeys;  // tokens of a TMA box
       const int boxes = kKeys / box;                // boxes of a tile's 128 bytes of width
       // this warp's boxes: every second one, one to a lane (8-bit: all)
-      const int pi = kQuant ? 0 : warp == 12;
+      const int pi = kQuant ? 0 : warp == 10;
       const int bi = kQuant ? lane : 2 * lane + pi;
       const int nb = boxes * (kQuant ? 1 : C::kHalves);
       const int mine = kQuant ? nb : (nb + 1 - pi) / 2;
