@@ -123,7 +123,7 @@ struct Misc {
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
   uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];
   uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2], p_half[2], p_ready[2], o_full[2], scanned[2];
+  uint64_t s_full[2], p_ready[2], o_full[2], scanned[2];
   uint64_t merge, merged, drain;
   Seg seg[2];  // of the segment whose first row tile is in the slot
   uint32_t tmem;
@@ -272,6 +272,31 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
   uint32_t r;
   asm("{ .reg .b16 h; cvt.u16.u32 h, %1; cvt.rn.f16x2.e4m3x2 %0, h; }" : "=r"(r) : "r"(w));
   return r;
+}
+
+// Lane j of a quad holds four 16-byte parts y[4 i ..] of its own row; afterwards
+// it holds part j of the quad's rows i = 0 .. 3 (two exchanges, as a 4 x 4
+// matrix of parts is transposed).
+__device__ __forceinline__ void quad_transpose16(uint32_t (&y)[16]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int d = 1; d <= 2; d <<= 1) {
+    const bool up = lane & d;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & d) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t& lo = y[4 * i + e];
+        uint32_t& hi = y[4 * (i + d) + e];
+        const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? lo : hi, d);
+        if (up)
+          lo = got;
+        else
+          hi = got;
+      }
+    }
+  }
 }
 
 // A wait that gives up after kWaitLimitNs or when another warp has.
@@ -537,7 +562,6 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
       mbar_init(&m->s_full[w], 1);
       mbar_init(&m->q_full[w], 1);
       mbar_init(&m->q_empty[w], 8);  // the softmax warps
-      mbar_init(&m->p_half[w], 4);
       mbar_init(&m->p_ready[w], 4);
       mbar_init(&m->o_full[w], 1);
       mbar_init(&m->scanned[w], 4);
@@ -675,15 +699,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
           unsigned long long sum = 0ull, sum1 = 0ull;
 #pragma unroll
           for (int c = 0; c < kKeys; c += 4) {
-            if (c == kKeys / 2) {  // the first half's products may begin
-              tmem_st32(s_t, x);
-              if (!(tail || scan)) {
-                tmem_wait_st();
-                tc::fence_before_thread_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&m->p_half[w]);
-              }
-            }
+            if (c == kKeys / 2) tmem_st32(s_t, x);
             float a, b, e, f;
             f2_unpack(f2_fma(f2_pack(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sl2, neg2),
                       a, b);
@@ -793,10 +809,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         }
         tc::fence_before_thread_sync();
         __syncwarp();
-        if (lane == 0) {
-          if (tail || scan || !warp_live) mbar_arrive(&m->p_half[w]);
-          mbar_arrive(&m->p_ready[w]);
-        }
+        if (lane == 0) mbar_arrive(&m->p_ready[w]);
       }
       if (!ok) break;
       if (items > 0) {
@@ -842,49 +855,61 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
       }
       if (warp_live) {
         const bool none = l == 0.f;
-        const float inv = none ? 0.f : (P.kv.v_scale ? P.kv.v_scale[s.h] : 1.f) / l;
         const int64_t trow = static_cast<int64_t>(s.r.q0 + first + tok) * P.Hq + s.h * G +
                              (row - tok * G);
-        const int slot = s.opens ? 1 : 0;
-        const int64_t prow = ((static_cast<int64_t>(blockIdx.x) * 2 + slot) * 2 +
+        const int64_t prow = ((static_cast<int64_t>(blockIdx.x) * 2 + (s.opens ? 1 : 0)) * 2 +
                               (s.pair ? w : 0)) * kRows + row;
-        float* po = reinterpret_cast<float*>(wsp + ws.o) + prow * D;
+        // a piece is 64 bytes of a row: 32 output values, or 16 of a partial O.
+        // A lane's own row would cost a store a line each; the four lanes of a
+        // quad trade 16-byte parts and write 64 bytes of each other's rows.
+        const float f = none ? 0.f : split ? 1.f : (P.kv.v_scale ? P.kv.v_scale[s.h] : 1.f) / l;
+        const float f0 = joined ? f * keep0 : f, f1 = f * keep1;
+        unsigned char* mine = split ? wsp + ws.o + prow * D * 4
+                                    : static_cast<unsigned char*>(P.out) + trow * D * 2;
+        if (!live) mine = nullptr;
+        unsigned char* to[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          to[i] = reinterpret_cast<unsigned char*>(__shfl_sync(
+                      0xFFFFFFFFu, reinterpret_cast<unsigned long long>(mine), (lane & ~3) + i));
+        const int step = split ? 16 : 32;
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
+        for (int c = 0; c < D; c += step) {
           uint32_t o[32];
-          tmem_ld32(o_t + c, o);
+          tmem_ld32(o_t + (split ? c & ~31 : c), o);
           if (joined) {
             uint32_t o1[32];
-            tmem_ld32(o_t + 128 + c, o1);
+            tmem_ld32(o_t + 128 + (split ? c & ~31 : c), o1);
             tc::tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              o[e] = __float_as_uint(__uint_as_float(o[e]) * keep0 +
-                                     __uint_as_float(o1[e]) * keep1);
+              o[e] = __float_as_uint(__uint_as_float(o[e]) * f0 + __uint_as_float(o1[e]) * f1);
           } else {
             tc::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f0);
           }
-          if (!live) {
-          } else if (split) {
+          uint32_t y[16];
+          if (split) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4*>(po + c + e) =
-                  none ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            for (int e = 0; e < 16; ++e) y[e] = c & 16 ? o[16 + e] : o[e];
           } else {
-            uint16_t* out = static_cast<uint16_t*>(P.out) + trow * D + c;
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint32_t y[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float a = none ? 0.f : __uint_as_float(o[e + 2 * i]) * inv;
-                const float b = none ? 0.f : __uint_as_float(o[e + 2 * i + 1]) * inv;
-                y[i] = P.dtype == DSPARK_F16 ? pack_f16(a, b) : pack_bf16(a, b);
-              }
-              *reinterpret_cast<uint4*>(out + e) = make_uint4(y[0], y[1], y[2], y[3]);
+            for (int e = 0; e < 16; ++e) {
+              const float a = __uint_as_float(o[2 * e]), b = __uint_as_float(o[2 * e + 1]);
+              y[e] = P.dtype == DSPARK_F16 ? pack_f16(a, b) : pack_bf16(a, b);
             }
           }
-          __syncwarp();
+          if (none) {  // (O may hold anything)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] = 0u;
+          }
+          quad_transpose16(y);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (to[i])
+              *reinterpret_cast<uint4*>(to[i] + (split ? c * 4 : c * 2) + (lane & 3) * 16) =
+                  make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
         }
         if (live) {
           if (split) {
@@ -1111,44 +1136,37 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
           if (leader) scores(i, ki);
           __syncwarp();
         }
-        for (int i = 0; i < ni && ok; ++i) {  // O_w += P_w V of item i, in two halves
+        for (int i = 0; i < ni && ok; ++i) {  // O_w += P_w V of item i, S_w of item i + 2
           const int w = i & 1;
           const uint32_t vi = base + s.v_place(s.j0 + (s.pair ? i >> 1 : i));
           const uint32_t n = w ? n_item1 : n_item0;
-          if (!(ok = wait_warp2(&m->kv_full[vi % C::kStages], (vi / C::kStages) & 1, &m->p_half[w],
-                                n & 1, fail, P.status)))
+          const bool more = i + 2 < ni;
+          const uint32_t ki = keys_of(more ? i + 2 : i);
+          if (!(ok = wait_warp2(&m->kv_full[vi % C::kStages], (vi / C::kStages) & 1,
+                                &m->p_ready[w], n & 1, fail, P.status)))
             break;
           tc::fence_after_thread_sync();
           const bool skip = *reinterpret_cast<volatile int*>(&m->skip_pv[w]) == static_cast<int>(n);
           const uint64_t vd =
               v_desc + static_cast<uint32_t>(((vi % C::kStages) * C::kTileBytes) >> 4);
           const uint32_t o_d = tmem + 256 + w * 128, p_d = tmem + w * kKeys;
-          if (leader && !skip) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              mma_ts(o_d, p_d + c * 8, vd + ((c * 2048) >> 4), id_pv, i >= 2 || c != 0);
-          }
-          __syncwarp();
-          // the second half, and the warpgroup's next scores
-          const bool more = i + 2 < ni;
-          const uint32_t ki = keys_of(more ? i + 2 : i);
-          ok = more ? wait_warp2(&m->kv_full[ki % C::kStages], (ki / C::kStages) & 1,
-                                 &m->p_ready[w], n & 1, fail, P.status)
-                    : wait_warp(&m->p_ready[w], n & 1, fail, P.status);
-          if (!ok) break;
-          tc::fence_after_thread_sync();
           if (leader) {
             if (!skip) {
 #pragma unroll
-              for (int c = 4; c < 8; ++c)
-                mma_ts(o_d, p_d + c * 8, vd + ((c * 2048) >> 4), id_pv, 1);
+              for (int c = 0; c < kKeys / 16; ++c)
+                mma_ts(o_d, p_d + c * 8, vd + ((c * 2048) >> 4), id_pv, i >= 2 || c != 0);
             }
-            if (more)
-              scores(i + 2, ki);
-            else
-              tc::mma_commit(&m->o_full[w]);
+            if (!more) tc::mma_commit(&m->o_full[w]);
           }
           __syncwarp();
+          if (more) {
+            if (!(ok = wait_warp(&m->kv_full[ki % C::kStages], (ki / C::kStages) & 1, fail,
+                                 P.status)))
+              break;
+            tc::fence_after_thread_sync();
+            if (leader) scores(i + 2, ki);
+            __syncwarp();
+          }
           n_item0 += w == 0;
           n_item1 += w == 1;
         }
