@@ -18,5 +18,6 @@ def __getattr__(name):
                 "paged_tables", "kv_append", "paged_attention",
                 "paged_attention_workspace_bytes"):
         from . import _lib
-        return getattr(_lib, name)
+        globals()[name] = value = getattr(_lib, name)
+        return value
     raise AttributeError(name)

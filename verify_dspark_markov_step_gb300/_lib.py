@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -461,58 +462,86 @@ _PAGED_DTYPES = {torch.bfloat16: DSPARK_BF16, torch.float16: DSPARK_F16,
                  torch.float8_e4m3fn: DSPARK_E4M3}
 
 
+# The calls below are made once a layer and step, some for a few microseconds of
+# work, so their marshalling is kept lean: one pass over a tensor's properties,
+# the raw stream handle, one packed struct.
+_kv = threading.local()
+_KV_FIELDS = struct.Struct("=4Q6q5i")
+
+
 def _of(t, name, dtype, shape=None):
     """Address of a contiguous CUDA tensor of one dtype (and shape)."""
+    try:
+        if t.is_cuda and t.dtype is dtype and t.is_contiguous() and (
+                shape is None or t.shape == shape):
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
 def _maybe(t, name, dtype, shape=None):
     return None if t is None else _of(t, name, dtype, shape)
 
 
-def _rows(t, name, heads=None):
+def _raw_stream(stream, t):
+    """The handle of `stream`, or of the current stream of t's device."""
+    return (torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None
+            else stream.cuda_stream)
+
+
+def _rows(t, name):
     """[T, H, D] rows whose tokens may be further apart than H * D (a view into
     a fused projection): (address, dtype, elements between tokens)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype is not torch.bfloat16 and t.dtype is not torch.float16:
-        raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    dt = t.dtype
+    if dt is not torch.bfloat16 and dt is not torch.float16:
+        raise TypeError(f"{name} must be bfloat16 or float16, got {dt}")
     if t.dim() != 3:
         raise ValueError(f"{name} must be [T, heads, head_dim]")
     T, H, D = t.shape
     st, sh, sd = t.stride()
     if (sd != 1 and D > 1) or (sh != D and H > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), _PAGED_DTYPES[t.dtype], H * D if T < 2 else st
+    return t.data_ptr(), _PAGED_DTYPES[dt], H * D if T < 2 else st
 
 
 def _paged_kv(k_cache, v_cache, k_scale, v_scale):
     """The dspark_paged_kv of caches [num_blocks, kv_heads, page_size, head_dim]
-    of any strides with contiguous head_dim."""
+    of any strides with contiguous head_dim (this thread's, until its next call),
+    kv_heads and head_dim."""
     for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{name} must be a CUDA tensor")
-        if t.dtype not in _PAGED_DTYPES:
-            raise TypeError(f"{name} must be bfloat16, float16 or float8_e4m3fn, got {t.dtype}")
-        if t.dim() != 4 or t.stride(3) != 1:
-            raise ValueError(f"{name} must be [num_blocks, kv_heads, page_size, head_dim] with "
-                             "contiguous head_dim")
-    if k_cache.dtype != v_cache.dtype or k_cache.shape != v_cache.shape:
+    dt, shape = k_cache.dtype, k_cache.shape
+    if dt is not v_cache.dtype or shape != v_cache.shape:
         raise ValueError("k_cache and v_cache must have the same dtype and shape")
-    N, H, P, D = k_cache.shape
-    return PagedKv(k_cache.data_ptr(), v_cache.data_ptr(),
-                   _maybe(k_scale, "k_scale", torch.float32, (H,)),
-                   _maybe(v_scale, "v_scale", torch.float32, (H,)),
-                   *k_cache.stride()[:3], *v_cache.stride()[:3],
-                   _PAGED_DTYPES[k_cache.dtype], N, H, P, D)
+    if dt not in _PAGED_DTYPES:
+        raise TypeError(f"k_cache must be bfloat16, float16 or float8_e4m3fn, got {dt}")
+    if len(shape) != 4:
+        raise ValueError("k_cache must be [num_blocks, kv_heads, page_size, head_dim]")
+    N, H, P, D = shape
+    kb, kh, kt, kd = k_cache.stride()
+    vb, vh, vt, vd = v_cache.stride()
+    if (kd != 1 or vd != 1) and D > 1:
+        raise ValueError("k_cache and v_cache: the values of a token must be contiguous")
+    try:
+        kv = _kv.kv
+    except AttributeError:
+        kv = _kv.kv = PagedKv()
+    _KV_FIELDS.pack_into(
+        kv, 0, k_cache.data_ptr(), v_cache.data_ptr(),
+        0 if k_scale is None else _of(k_scale, "k_scale", torch.float32, (H,)),
+        0 if v_scale is None else _of(v_scale, "v_scale", torch.float32, (H,)),
+        kb, kh, kt, vb, vh, vt, _PAGED_DTYPES[dt], N, H, P, D)
+    return kv, H, D
 
 
 def paged_tables(req_state_idx, new_lens, cached_lens, block_table, held_blocks, free_blocks,
@@ -525,7 +554,7 @@ def paged_tables(req_state_idx, new_lens, cached_lens, block_table, held_blocks,
     i32, i64 = torch.int32, torch.int64
     B, (S, M) = req_state_idx.shape[0], block_table.shape
     N, T = free_blocks.shape[0], slot_map.shape[0]
-    code = lib().dspark_paged_tables(
+    code = (_lib or lib()).dspark_paged_tables(
         _of(req_state_idx, "req_state_idx", i32, (B,)), _of(new_lens, "new_lens", i32, (B,)),
         _of(cached_lens, "cached_lens", i32, (S,)),
         _maybe(num_accepted, "num_accepted", i32, (B,)),
@@ -533,8 +562,10 @@ def paged_tables(req_state_idx, new_lens, cached_lens, block_table, held_blocks,
         _of(free_blocks, "free_blocks", i32, (N,)), _of(pool, "pool", i32, (2,)),
         _of(query_start, "query_start", i32, (B + 1,)), _of(seq_lens, "seq_lens", i32, (B,)),
         _of(positions, "positions", i64, (T,)), _of(slot_map, "slot_map", i64, (T,)),
-        B, S, M, N, T, page_size, _maybe(status, "status", i32), _stream(stream))
-    _check(code, "dspark_paged_tables")
+        B, S, M, N, T, page_size, _maybe(status, "status", i32),
+        _raw_stream(stream, query_start))
+    if code:
+        _check(code, "dspark_paged_tables")
 
 
 def kv_append(k, v, k_cache, v_cache, slot_map, k_scale=None, v_scale=None, status=None,
@@ -542,17 +573,18 @@ def kv_append(k, v, k_cache, v_cache, slot_map, k_scale=None, v_scale=None, stat
     """dspark_kv_append on torch tensors (see include/dspark.h): rows k, v
     [T, kv_heads, head_dim] (views of a fused projection will do) into the
     caches [num_blocks, kv_heads, page_size, head_dim]."""
-    cache = _paged_kv(k_cache, v_cache, k_scale, v_scale)
+    cache, H, D = _paged_kv(k_cache, v_cache, k_scale, v_scale)
     T = slot_map.shape[0]
-    want = (T, cache.kv_heads, cache.head_dim)
+    want = (T, H, D)
     kp, dt, ks = _rows(k, "k")
     vp, vdt, vs = _rows(v, "v")
     if k.shape != want or v.shape != want or dt != vdt:
         raise ValueError(f"k and v must be {list(want)} of one dtype")
-    code = lib().dspark_kv_append(kp, vp, dt, ks, vs, cache,
-                                  _of(slot_map, "slot_map", torch.int64, (T,)), T,
-                                  _maybe(status, "status", torch.int32), _stream(stream))
-    _check(code, "dspark_kv_append")
+    code = (_lib or lib()).dspark_kv_append(
+        kp, vp, dt, ks, vs, cache, _of(slot_map, "slot_map", torch.int64, (T,)), T,
+        _maybe(status, "status", torch.int32), _raw_stream(stream, slot_map))
+    if code:
+        _check(code, "dspark_kv_append")
 
 
 def paged_attention_workspace_bytes(B, q_heads, kv_heads, head_dim) -> int:
@@ -566,26 +598,27 @@ def paged_attention(q, k_cache, v_cache, block_table, req_state_idx, query_start
     attention of rows q [T, q_heads, head_dim] (a view of a fused projection
     will do) over the caches, into out and, if given, lse [T, q_heads]. scale
     is 1 / sqrt(head_dim) if not given."""
-    cache = _paged_kv(k_cache, v_cache, k_scale, v_scale)
+    cache, H, cd = _paged_kv(k_cache, v_cache, k_scale, v_scale)
     qp, dt, qs = _rows(q, "q")
     T, Hq, D = q.shape
     B, (S, M) = req_state_idx.shape[0], block_table.shape
-    if D != cache.head_dim:
+    if D != cd:
         raise ValueError("q and the caches must have the same head_dim")
     if workspace_buf is None:
-        need = paged_attention_workspace_bytes(B, Hq, cache.kv_heads, D)
+        need = paged_attention_workspace_bytes(B, Hq, H, D)
         if stream is None:
             workspace_buf = workspace(need, q.device)
         else:  # memory of the stream that uses it
             with torch.cuda.stream(stream):
                 workspace_buf = workspace(need, q.device)
     i32 = torch.int32
-    code = lib().dspark_paged_attention(
+    code = (_lib or lib()).dspark_paged_attention(
         qp, dt, qs, cache, _of(block_table, "block_table", i32),
         _of(req_state_idx, "req_state_idx", i32, (B,)),
         _of(query_start, "query_start", i32, (B + 1,)), _of(seq_lens, "seq_lens", i32, (B,)),
         _of(out, "out", q.dtype, q.shape), _maybe(lse, "lse", torch.float32, (T, Hq)),
         D ** -0.5 if scale is None else scale, bool(causal), window, Hq, B, S, M, T,
-        workspace_buf.data_ptr(), workspace_buf.numel() * workspace_buf.element_size(),
-        _maybe(status, "status", i32), _stream(stream))
-    _check(code, "dspark_paged_attention")
+        workspace_buf.data_ptr(), workspace_buf.nbytes, _maybe(status, "status", i32),
+        _raw_stream(stream, q))
+    if code:
+        _check(code, "dspark_paged_attention")

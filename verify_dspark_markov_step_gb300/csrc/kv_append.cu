@@ -1,10 +1,15 @@
 // kv_append.cu -- the keys and values of new tokens into their pages.
 //
-// A copy with an address per token: 16 bytes (8 values) of a key or value row
-// per thread, read from the tokens' side (which may be a view into a fused
-// projection) and written into the page, as they are or divided by the
-// head's scale and rounded to 8 bits. Bound by memory for long prompts (each
-// value read once and written once), by latency for a decode step.
+// A copy with an address per token: a thread owns a 16-byte piece (8 values) of
+// the token's keys or values and takes it for several tokens, read from the
+// tokens' side (which may be a view into a fused projection) and written into
+// the page, as it is or divided by the head's scale and rounded to 8 bits. The
+// quotient is the IEEE one (temp_div2, by products with the scale's reciprocal
+// and a correction: 8 divisions a piece would cost as much time as the memory).
+//
+// Bound by memory for long prompts (each value read once and written once), by
+// latency for a decode step, where a CTA takes one token a thread instead of
+// kBatch, so that 256 tokens are spread over the GPU.
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -17,6 +22,7 @@ namespace dspark {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kBatch = 4;  // tokens per thread, all loaded before the first is stored
 
 __device__ __forceinline__ float half_bits_to_float(uint32_t bits) {
   float f;
@@ -35,7 +41,8 @@ __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
 }
 
 template <bool kF16>
-__device__ __forceinline__ uint32_t quantise_pair(uint32_t w, float scale) {
+__device__ __forceinline__ uint32_t quantise_pair(uint32_t w, unsigned long long r2,
+                                                  unsigned long long nt2, bool slow) {
   float a, b;
   if constexpr (kF16) {
     a = half_bits_to_float(w & 0xFFFFu);
@@ -44,57 +51,97 @@ __device__ __forceinline__ uint32_t quantise_pair(uint32_t w, float scale) {
     a = __uint_as_float(w << 16);
     b = __uint_as_float(w & 0xFFFF0000u);
   }
-  return e4m3_pair(__fdiv_rn(a, scale), __fdiv_rn(b, scale));
+  f2_unpack(temp_div2(f2_pack(a, b), r2, nt2, slow), a, b);
+  return e4m3_pair(a, b);
+}
+
+// `width` threads share a token, `abreast` tokens are taken at a time.
+template <bool kQuantise, bool kF16, int kPer>
+__global__ void __launch_bounds__(kThreads)
+kv_append_kernel(KvAppendParams P, int width, int abreast) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int sub = threadIdx.x / width;
+  if (sub >= abreast) return;
+  const int t0 = blockIdx.x * (abreast * kPer) + sub;
+  int64_t slot[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int t = t0 + i * abreast;
+    slot[i] = t < P.T ? P.slot_map[t] : -1;
+    if (slot[i] >= P.num_slots) {
+      report(P.status, DSPARK_ERR_BOUNDS);
+      slot[i] = -1;
+    }
+  }
+  const int cd = P.D / 8, chunks = P.H * cd;  // pieces of a head, of a token's keys
+  for (int p = threadIdx.x - sub * width; p < 2 * chunks; p += width) {
+    const int which = p >= chunks ? 1 : 0;  // keys, then values
+    const int c = p - which * chunks, h = c / cd;
+    const uint16_t* src = static_cast<const uint16_t*>(P.src[which]) + c * 8;
+    uint4 x[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (slot[i] >= 0)
+        x[i] = *reinterpret_cast<const uint4*>(
+            src + static_cast<int64_t>(t0 + i * abreast) * P.src_stride[which]);
+    const int64_t head = h * P.head_stride[which] + (c - h * cd) * 8;
+    float scale = 1.f;
+    if (kQuantise && P.scale[which]) scale = P.scale[which][h];
+    const bool slow = !temp_div_t_ok(scale);
+    const float rcp = __frcp_rn(scale);
+    const unsigned long long r2 = f2_pack(rcp, rcp), nt2 = f2_pack(-scale, -scale);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (slot[i] < 0) continue;
+      const int64_t at = (slot[i] >> P.page_shift) * P.block_stride[which] +
+                         (slot[i] & ((1 << P.page_shift) - 1)) * P.token_stride[which] + head;
+      if constexpr (kQuantise) {
+        const uint32_t lo = quantise_pair<kF16>(x[i].x, r2, nt2, slow) |
+                            (quantise_pair<kF16>(x[i].y, r2, nt2, slow) << 16);
+        const uint32_t hi = quantise_pair<kF16>(x[i].z, r2, nt2, slow) |
+                            (quantise_pair<kF16>(x[i].w, r2, nt2, slow) << 16);
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(P.dst[which]) + at) = make_uint2(lo, hi);
+      } else {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.dst[which]) + at) = x[i];
+      }
+    }
+  }
+}
+
+template <bool kQuantise, bool kF16, int kPer>
+cudaError_t launch(const KvAppendParams& p, int width, int abreast, cudaStream_t stream) {
+  const int per = abreast * kPer;
+  // (may be set up while the kernel before it ends, and waits for it)
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((p.T + per - 1) / per));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_append_kernel<kQuantise, kF16, kPer>, p, width, abreast);
 }
 
 template <bool kQuantise, bool kF16>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(KvAppendParams P) {
-  const int chunks = P.H * P.D / 8;  // 16-byte pieces of a token's keys (or values)
-  const int64_t n = static_cast<int64_t>(P.T) * 2 * chunks;
-  const int cd = P.D / 8;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n;
-       i += static_cast<int64_t>(gridDim.x) * kThreads) {
-    const int t = static_cast<int>(i / (2 * chunks));
-    int c = static_cast<int>(i - static_cast<int64_t>(t) * 2 * chunks);
-    const int which = c >= chunks ? 1 : 0;  // keys, then values
-    c -= which * chunks;
-    const int64_t slot = P.slot_map[t];
-    if (slot < 0) continue;
-    if (slot >= P.num_slots) {
-      report(P.status, DSPARK_ERR_BOUNDS);
-      continue;
-    }
-    const int h = c / cd, d = (c - h * cd) * 8;
-    const uint16_t* src = static_cast<const uint16_t*>(P.src[which]) +
-                          static_cast<int64_t>(t) * P.src_stride[which] + c * 8;
-    const uint4 x = *reinterpret_cast<const uint4*>(src);
-    const int64_t at = (slot >> P.page_shift) * P.block_stride[which] + h * P.head_stride[which] +
-                       (slot & ((1 << P.page_shift) - 1)) * P.token_stride[which] + d;
-    if constexpr (kQuantise) {
-      const float s = P.scale[which] ? P.scale[which][h] : 1.f;
-      const uint32_t lo = quantise_pair<kF16>(x.x, s) | (quantise_pair<kF16>(x.y, s) << 16);
-      const uint32_t hi = quantise_pair<kF16>(x.z, s) | (quantise_pair<kF16>(x.w, s) << 16);
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(P.dst[which]) + at) = make_uint2(lo, hi);
-    } else {
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.dst[which]) + at) = x;
-    }
-  }
+cudaError_t launch_per(const KvAppendParams& p, cudaStream_t stream) {
+  const int pieces = 2 * (p.H * p.D / 8);
+  const int width = pieces < kThreads ? pieces : kThreads;
+  const int abreast = kThreads / width;
+  // up to four CTAs an SM with a token a thread, kBatch tokens a thread beyond
+  return p.T <= 152 * 4 * abreast
+             ? launch<kQuantise, kF16, 1>(p, width, abreast, stream)
+             : launch<kQuantise, kF16, kBatch>(p, width, abreast, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t stream) {
-  const int64_t n = static_cast<int64_t>(p.T) * 2 * (p.H * p.D / 8);
-  int64_t ctas = (n + kThreads - 1) / kThreads;
-  if (ctas > 152 * 64) ctas = 152 * 64;
-  const dim3 grid(static_cast<unsigned>(ctas));
-  if (p.cache_dtype != DSPARK_E4M3)
-    kv_append_kernel<false, false><<<grid, kThreads, 0, stream>>>(p);
-  else if (p.dtype == DSPARK_F16)
-    kv_append_kernel<true, true><<<grid, kThreads, 0, stream>>>(p);
-  else
-    kv_append_kernel<true, false><<<grid, kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  if (p.cache_dtype != DSPARK_E4M3) return launch_per<false, false>(p, stream);
+  return p.dtype == DSPARK_F16 ? launch_per<true, true>(p, stream)
+                               : launch_per<true, false>(p, stream);
 }
 
 }  // namespace dspark

@@ -132,7 +132,9 @@ struct Misc {
   int bad[2];      // the last tile whose values were found non-finite, per warpgroup
   int skip_pv[2];  // the last item whose P V the warpgroup did itself
   int start_b, per;
-  long long start_rem, start_cost, pos, end;
+  Request start_r;
+  int start_h;
+  long long start_rem, pos, end;
   unsigned long long warp_sum[17];
   float2 x[kRows];  // r, l of the second warpgroup in a joined unit
 };
@@ -405,10 +407,9 @@ struct Walk {
   __device__ Walk(const PagedAttentionParams& P_, const Misc* m, int tp_)
       : P(P_), tp(tp_), b(m->start_b), h(0), u(0), per(m->per), pos(m->pos), end(m->end) {
     if (pos >= end) return;
-    r = load_request(P, b, false);
+    r = m->start_r;
+    h = m->start_h;
     long long rem = m->start_rem;
-    h = static_cast<int>(rem / m->start_cost);
-    rem -= h * m->start_cost;
     for (;; ++u) {
       unit_tiles(P, r, tp, u, jb, je);
       if (rem < je - jb) break;
@@ -459,9 +460,9 @@ __device__ void make_plan(const PagedAttentionParams& P, Misc* m, unsigned long 
   // each thread takes `each` consecutive requests, so that a scan of the
   // threads' sums gives the prefix
   const int each = (B + kThreads - 1) / kThreads;
+  Request r;
   for (int i = 0; i < each; ++i) {
     const int b = tid * each + i;
-    Request r;
     r.n = 0;
     if (b < B) r = load_request(P, b, blockIdx.x == 0);
     const int units = (r.n + 2 * tp - 1) / (2 * tp);
@@ -524,8 +525,13 @@ __device__ void make_plan(const PagedAttentionParams& P, Misc* m, unsigned long 
     const unsigned long long lo = base + (i ? pre[b - 1] : 0), hi = base + pre[b];
     if (lo <= pos && pos < hi) {
       m->start_b = b;
-      m->start_rem = static_cast<long long>(pos - lo);
-      m->start_cost = static_cast<long long>((hi - lo) / P.kv.kv_heads);
+      m->start_r = each == 1 ? r : load_request(P, b, false);
+      const unsigned long long cost = (hi - lo) / P.kv.kv_heads;  // of a head
+      const unsigned long long h =
+          (hi - lo) >> 32 ? (pos - lo) / cost
+                          : static_cast<unsigned int>(pos - lo) / static_cast<unsigned int>(cost);
+      m->start_h = static_cast<int>(h);
+      m->start_rem = static_cast<long long>(pos - lo - h * cost);
     }
   }
 }
@@ -549,6 +555,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
   const Ws ws(D);
   unsigned char* wsp = static_cast<unsigned char*>(P.workspace);
 
+  // the launch after this one may be set up; the one before it ends further down
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&m->kv_full[i], kQuant ? 4 : 2);
@@ -581,6 +589,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     tc::tmem_alloc(&m->tmem, 512);
     tc::tmem_relinquish();
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   make_plan<C::kThreads>(P, m, reinterpret_cast<unsigned long long*>(smem + C::kv), tp);
   fence_proxy_async_smem();  // the plan's scratch is TMA's from here on
   tc::fence_before_thread_sync();
@@ -1243,6 +1252,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
 // the CTAs after it, in that order. A warp per row.
 template <int D>
 __global__ void __launch_bounds__(256) paged_join_kernel(PagedAttentionParams P, int off) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Ws ws(D);
   const unsigned char* wsp = static_cast<const unsigned char*>(P.workspace);
@@ -1369,20 +1379,22 @@ cudaError_t launch(const PagedAttentionParams& p, const CUtensorMap& mq, const C
                            cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
   if (err != cudaSuccess) return err;
   const int grid = sms < kMaxCtas ? sms : kMaxCtas;
-  paged_attention_kernel<D, kF16, kQuant><<<grid, C::kThreads, C::kBytes, stream>>>(mq, mk, mv,
-                                                                              p);
-  err = cudaGetLastError();
-  if (err != cudaSuccess) return err;
-  // the join starts when the last CTA of the launch before it ends
+  // both launches may be set up while the one before them ends, and wait for it
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, 8);
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  err = cudaLaunchKernelEx(&cfg, paged_attention_kernel<D, kF16, kQuant>, mq, mk, mv, p);
+  if (err != cudaSuccess) return err;
+  cfg.gridDim = dim3(grid, 8);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, p, kF16 ? 7 : 0);
 }
 

@@ -75,6 +75,8 @@ __device__ unsigned long long block_scan(unsigned long long v, unsigned long lon
 
 __global__ void __launch_bounds__(1024) paged_tables_kernel(PagedTablesParams P) {
   __shared__ TablesSmem sm;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
   const int B = P.B, M = P.M, N = P.N, T = P.T, sh = P.page_shift;
   const bool first = blockIdx.x == 0;  // reports errors
@@ -233,8 +235,17 @@ cudaError_t launch_paged_tables(const PagedTablesParams& p, cudaStream_t stream)
   int ctas = (p.T + kTokensPerCta - 1) / kTokensPerCta;
   if (ctas < 1) ctas = 1;
   if (ctas > 304) ctas = 304;
-  paged_tables_kernel<<<ctas, threads, 0, stream>>>(p);
-  return cudaGetLastError();
+  // (may be set up while the kernel before it ends, and waits for it)
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_tables_kernel, p);
 }
 
 }  // namespace dspark
