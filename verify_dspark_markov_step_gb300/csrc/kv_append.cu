@@ -4,8 +4,8 @@
 // the token's keys or values and takes it for several tokens, read from the
 // tokens' side (which may be a view into a fused projection) and written into
 // the page, as it is or divided by the head's scale and rounded to 8 bits. The
-// quotient is the IEEE one (temp_div2, by products with the scale's reciprocal
-// and a correction: 8 divisions a piece would cost as much time as the memory).
+// quotient is the IEEE one, by products with the scale's reciprocal and a
+// correction: 8 divisions a piece would cost as much time as the memory.
 //
 // Bound by memory for long prompts (each value read once and written once), by
 // latency for a decode step, where a CTA takes one token a thread instead of
@@ -40,6 +40,12 @@ __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
   return r;
 }
 
+// x / scale of two values, rounded to 8 bits. With r = rn(1 / scale), q = rn(x r)
+// and the residual x - q scale (exact in an FMA), rn(q + (x - q scale) r) is the
+// correctly rounded quotient (Markstein's theorem, as for temp_div2) wherever
+// nothing over- or underflows. What underflows is far below the smallest 8-bit
+// value; overflow, infinities and NaN make the sum NaN, and those, and scales
+// outside [2^-30, 2^30] (`slow`), take the division itself.
 template <bool kF16>
 __device__ __forceinline__ uint32_t quantise_pair(uint32_t w, unsigned long long r2,
                                                   unsigned long long nt2, bool slow) {
@@ -51,8 +57,16 @@ __device__ __forceinline__ uint32_t quantise_pair(uint32_t w, unsigned long long
     a = __uint_as_float(w << 16);
     b = __uint_as_float(w & 0xFFFF0000u);
   }
-  f2_unpack(temp_div2(f2_pack(a, b), r2, nt2, slow), a, b);
-  return e4m3_pair(a, b);
+  const unsigned long long z = f2_pack(a, b), q = f2_mul(z, r2);
+  float x0, x1;
+  f2_unpack(f2_fma(f2_fma(q, nt2, z), r2, q), x0, x1);
+  if (slow || !(x0 + x1 == x0 + x1)) {  // (no sum of two quotients overflows here)
+    float t0, t1;
+    f2_unpack(nt2, t0, t1);
+    x0 = __fdiv_rn(a, -t0);
+    x1 = __fdiv_rn(b, -t1);
+  }
+  return e4m3_pair(x0, x1);
 }
 
 // `width` threads share a token, `abreast` tokens are taken at a time.

@@ -557,30 +557,34 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
 
   // the launch after this one may be set up; the one before it ends further down
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (tid == 0) {
-    for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(&m->kv_full[i], kQuant ? 4 : 2);
-      mbar_init(&m->kv_empty[i], 2);
+  if (warp == 8) {  // a lane per index
+    if (lane < C::kStages) {
+      mbar_init(&m->kv_full[lane], kQuant ? 4 : 2);
+      mbar_init(&m->kv_empty[lane], 2);
     }
-    for (int i = 0; i < C::kRaw; ++i) {
-      mbar_init(&m->raw_full[i], 1);
-      mbar_init(&m->raw_empty[i], 4);
+    if (lane < C::kRaw) {
+      mbar_init(&m->raw_full[lane], 1);
+      mbar_init(&m->raw_empty[lane], 4);
     }
-    for (int w = 0; w < 2; ++w) {
-      mbar_init(&m->s_full[w], 1);
-      mbar_init(&m->q_full[w], 1);
-      mbar_init(&m->q_empty[w], 8);  // the softmax warps
-      mbar_init(&m->p_ready[w], 4);
-      mbar_init(&m->o_full[w], 1);
-      mbar_init(&m->scanned[w], 4);
-      m->bad[w] = m->skip_pv[w] = -1;
+    if (lane < 2) {
+      mbar_init(&m->q_full[lane], 1);
+      mbar_init(&m->q_empty[lane], 8);  // the softmax warps
+      mbar_init(&m->s_full[lane], 1);
+      mbar_init(&m->p_ready[lane], 4);
+      mbar_init(&m->o_full[lane], 1);
+      mbar_init(&m->scanned[lane], 4);
+      m->bad[lane] = m->skip_pv[lane] = -1;
     }
-    m->filling = 0;
-    mbar_init(&m->merge, 4);
-    mbar_init(&m->merged, 4);
-    mbar_init(&m->drain, 1);
-    m->fail = 0;
+    if (lane == 0) {
+      mbar_init(&m->merge, 4);
+      mbar_init(&m->merged, 4);
+      mbar_init(&m->drain, 1);
+      m->filling = 0;
+      m->fail = 0;
+    }
     fence_mbar_init();
+  }
+  if (tid == 0) {
     if (!kQuant) tc::prefetch_tensormap(&tmap_q);
     tc::prefetch_tensormap(&tmap_k);
     tc::prefetch_tensormap(&tmap_v);
@@ -1249,7 +1253,9 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
 
 // Joins the partial results of the units that more than one CTA worked on: the
 // unit that CTA blockIdx.x opened, from its tail part and the head parts of
-// the CTAs after it, in that order. A warp per row.
+// the CTAs after it, in that order. A warp per row; its lanes split the row, and
+// eight parts are loaded at a time, beside the statistics that weigh them (one
+// part after the other, 19 parts of a long request took 7 us of latency).
 template <int D>
 __global__ void __launch_bounds__(256) paged_join_kernel(PagedAttentionParams P, int off) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -1263,7 +1269,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(PagedAttentionParams P,
   const int lane = threadIdx.x & 31;
   const float2* stats = reinterpret_cast<const float2*>(wsp + ws.stats);
   const float* po = reinterpret_cast<const float*>(wsp + ws.o);
-  constexpr int kPer = D / 32;
+  constexpr int kPer = D / 32, kBatch = 8;
   const float vs = P.kv.v_scale ? P.kv.v_scale[d.h] : 1.f;
   const int rows = d.tokens * G;
   for (int i = blockIdx.y * 8 + (threadIdx.x >> 5); i < rows; i += gridDim.y * 8) {
@@ -1272,24 +1278,40 @@ __global__ void __launch_bounds__(256) paged_join_kernel(PagedAttentionParams P,
     auto at = [&](int p) -> int64_t {
       return (static_cast<int64_t>(c + p) * 2 + (p == 0 ? 1 : 0)) * 2 * kRows + place;
     };
-    float r = -INFINITY;
-    for (int p = lane; p < d.parts; p += 32) r = fmaxf(r, stats[at(p)].x);
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) r = fmaxf(r, __shfl_xor_sync(0xFFFFFFFFu, r, s));
-    const float rb = r == -INFINITY ? 0.f : r;
-    float l = 0.f, o[kPer];
+    float r = -INFINITY, l = 0.f, o[kPer];
 #pragma unroll
     for (int e = 0; e < kPer; ++e) o[e] = 0.f;
-    for (int p = 0; p < d.parts; ++p) {
-      const int64_t a = at(p);
-      const float2 x = stats[a];
-      const float keep = ex2_approx(x.x - rb);
-      l = fmaf(x.y, keep, l);
+    for (int p0 = 0; p0 < d.parts; p0 += kBatch) {
+      float2 x = make_float2(-INFINITY, 0.f);
+      if (lane < kBatch && p0 + lane < d.parts) x = stats[at(p0 + lane)];
+      float v[kBatch][kPer];
 #pragma unroll
-      for (int e = 0; e < kPer; e += 2) {
-        const float2 v = *reinterpret_cast<const float2*>(po + a * D + lane * kPer + e);
-        o[e] = fmaf(v.x, keep, o[e]);
-        o[e + 1] = fmaf(v.y, keep, o[e + 1]);
+      for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+        for (int e = 0; e < kPer; e += 2) {
+          float2 y = make_float2(0.f, 0.f);
+          if (p0 + b < d.parts)
+            y = *reinterpret_cast<const float2*>(po + at(p0 + b) * D + lane * kPer + e);
+          v[b][e] = y.x;
+          v[b][e + 1] = y.y;
+        }
+      float m = x.x;
+#pragma unroll
+      for (int s = kBatch / 2; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
+      const float rn = fmaxf(r, __shfl_sync(0xFFFFFFFFu, m, 0));
+      const float rb = rn == -INFINITY ? 0.f : rn;
+      const float old = ex2_approx(r - rb);
+      r = rn;
+      l *= old;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) o[e] *= old;
+      const float keep = ex2_approx(x.x - rb), mass = x.y * keep;
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        l += __shfl_sync(0xFFFFFFFFu, mass, b);
+        const float k = __shfl_sync(0xFFFFFFFFu, keep, b);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) o[e] = fmaf(v[b][e], k, o[e]);
       }
     }
     const bool none = l == 0.f;
@@ -1302,7 +1324,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(PagedAttentionParams P,
       const float a = none ? 0.f : o[e] * inv, b = none ? 0.f : o[e + 1] * inv;
       out[e / 2] = P.dtype == DSPARK_F16 ? pack_f16(a, b) : pack_bf16(a, b);
     }
-    if (P.lse && lane == 0) P.lse[row] = none ? -INFINITY : (rb - off + lg2_approx(l)) * kLn2;
+    if (P.lse && lane == 0) P.lse[row] = none ? -INFINITY : (r - off + lg2_approx(l)) * kLn2;
   }
 }
 
@@ -1392,7 +1414,7 @@ cudaError_t launch(const PagedAttentionParams& p, const CUtensorMap& mq, const C
   cfg.numAttrs = 1;
   err = cudaLaunchKernelEx(&cfg, paged_attention_kernel<D, kF16, kQuant>, mq, mk, mv, p);
   if (err != cudaSuccess) return err;
-  cfg.gridDim = dim3(grid, 8);
+  cfg.gridDim = dim3(grid, 16);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, p, kF16 ? 7 : 0);
