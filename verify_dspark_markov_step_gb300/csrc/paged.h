@@ -59,10 +59,11 @@ struct PagedAttentionParams {
   int causal, window;
   int dtype;
   int Hq, B, S, M, T, page_shift;
+  int whole;  // no unit is split over CTAs (set at launch)
   void* workspace;
   int32_t* status;
 };
 size_t paged_attention_workspace_bytes(int B, int Hq, int Hkv, int D);
-cudaError_t launch_paged_attention(const PagedAttentionParams& p, cudaStream_t stream);
+cudaError_t launch_paged_attention(PagedAttentionParams p, cudaStream_t stream);
 
 }  // namespace dspark

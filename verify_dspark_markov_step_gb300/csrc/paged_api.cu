@@ -181,6 +181,7 @@ dspark_status dspark_paged_attention(const void* q, dspark_dtype dtype, int64_t 
   p.M = M;
   p.T = T;
   p.page_shift = page_shift_of(cache->page_size);
+  p.whole = 0;
   p.workspace = workspace;
   p.status = status;
   if (dspark::launch_paged_attention(p, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)

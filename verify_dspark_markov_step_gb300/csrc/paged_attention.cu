@@ -64,6 +64,9 @@ constexpr int kMaxStages = 10;
 constexpr int kMaxRaw = 8;
 constexpr int kMaxCtas = 160;
 constexpr int kMinTiles = 2;  // key tiles a CTA takes at least
+// Units of at most this many key tiles are not split over CTAs: the second launch
+// that joins parts costs about as much as five tiles.
+constexpr int kWholeTiles = 4;
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kGrow = 8.0f;  // the reference moves when the maximum passes it by 2^8
@@ -124,7 +127,7 @@ struct Misc {
   uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_ready[2], o_full[2], scanned[2];
-  uint64_t merge, merged, drain;
+  uint64_t merge[2], merged, drain;
   Seg seg[2];  // of the segment whose first row tile is in the slot
   uint32_t tmem;
   int fail;
@@ -136,7 +139,7 @@ struct Misc {
   int start_h;
   long long start_rem, pos, end;
   unsigned long long warp_sum[17];
-  float2 x[kRows];  // r, l of the second warpgroup in a joined unit
+  float2 x[kRows];  // joined unit: r, l of the second warpgroup, then f0, f1
 };
 static_assert(sizeof(Misc) <= 2048, "Misc fits its place");
 
@@ -416,6 +419,26 @@ struct Walk {
       rem -= je - jb;
     }
     j = jb + static_cast<int>(rem);
+    if (P.whole && rem != 0) {  // the CTA before takes the unit to its end
+      pos += je - j;
+      j = je;
+      advance();
+    }
+  }
+  // To the next unit, if the run goes on.
+  __device__ void advance() {
+    if (j != je || pos >= end) return;
+    if (++u * 2 * tp >= r.n) {
+      u = 0;
+      if (++h == P.kv.kv_heads) {
+        h = 0;
+        do {
+          r = load_request(P, ++b, false);
+        } while (r.n == 0);
+      }
+    }
+    unit_tiles(P, r, tp, u, jb, je);
+    j = jb;
   }
   __device__ bool next(Seg& s) {
     if (pos >= end) return false;
@@ -425,26 +448,14 @@ struct Walk {
     s.t1 = min(r.n, s.t0 + 2 * tp);
     s.pair = s.t1 - s.t0 > tp;
     s.j0 = j;
-    s.j1 = static_cast<int>(min(static_cast<long long>(je), j + (end - pos)));
+    s.j1 = P.whole ? je : static_cast<int>(min(static_cast<long long>(je), j + (end - pos)));
     s.opens = j == jb;
     s.closes = s.j1 == je;
     s.c1 = static_cast<int>((pos + (je - j) - 1) / per);
     s.end = false;
     pos += s.j1 - s.j0;
     j = s.j1;
-    if (j == je && pos < end) {
-      if (++u * 2 * tp >= r.n) {
-        u = 0;
-        if (++h == P.kv.kv_heads) {
-          h = 0;
-          do {
-            r = load_request(P, ++b, false);
-          } while (r.n == 0);
-        }
-      }
-      unit_tiles(P, r, tp, u, jb, je);
-      j = jb;
-    }
+    advance();
     return true;
   }
 };
@@ -454,7 +465,6 @@ struct Walk {
 template <int kThreads>
 __device__ void make_plan(const PagedAttentionParams& P, Misc* m, unsigned long long* pre, int tp) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int nw = kThreads / 32;
   const int B = P.B;
   unsigned long long sum = 0;
   // each thread takes `each` consecutive requests, so that a scan of the
@@ -505,20 +515,20 @@ __device__ void make_plan(const PagedAttentionParams& P, Misc* m, unsigned long 
   if (lane == 31) m->warp_sum[warp] = v;
   __syncthreads();
   unsigned long long base = v - sum, total = 0;
-  for (int w = 0; w < nw; ++w) {
+  const int used = (B + 32 * each - 1) / (32 * each);  // warps that have requests
+  for (int w = 0; w < used; ++w) {
     if (w < warp) base += m->warp_sum[w];
     total += m->warp_sum[w];
   }
-  unsigned long long per = (total + gridDim.x - 1) / gridDim.x;
+  unsigned long long per = total >> 31 ? (total + gridDim.x - 1) / gridDim.x
+                                       : (static_cast<unsigned int>(total) + gridDim.x - 1) / gridDim.x;
   if (per < kMinTiles) per = kMinTiles;
   const unsigned long long pos = per * blockIdx.x;
   if (tid == 0) {
     m->per = static_cast<int>(per > 0x7FFFFFFF ? 0x7FFFFFFF : per);
     m->pos = static_cast<long long>(pos);
     m->end = static_cast<long long>(pos + per < total ? pos + per : total);
-    m->start_b = 0;
   }
-  __syncthreads();
   for (int i = 0; i < each; ++i) {
     const int b = tid * each + i;
     if (b >= B) break;
@@ -572,12 +582,12 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
       mbar_init(&m->s_full[lane], 1);
       mbar_init(&m->p_ready[lane], 4);
       mbar_init(&m->o_full[lane], 1);
+      mbar_init(&m->merge[lane], 4);
       mbar_init(&m->scanned[lane], 4);
       m->bad[lane] = m->skip_pv[lane] = -1;
     }
     if (lane == 0) {
-      mbar_init(&m->merge, 4);
-      mbar_init(&m->merged, 4);
+      mbar_init(&m->merged, 8);
       mbar_init(&m->drain, 1);
       m->filling = 0;
       m->fail = 0;
@@ -840,34 +850,49 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
       }
       n_q += s.pair ? 2 : 1;
       // ---- the segment's result -----------------------------------------------------
+      // A joined segment's is f0 O_0 + f1 O_1: the first warpgroup works out the
+      // factors, and each writes half of the columns.
       const bool joined = !s.pair && s.items(1) > 0;
-      if (!s.pair && w == 1) {
-        if (joined) {  // the first warpgroup takes it from here
-          m->x[row] = make_float2(r, l);
+      if (!s.pair && w == 1 && !joined) continue;
+      float f0 = 1.f, f1 = 0.f;
+      if (joined && w == 1) {
+        m->x[row] = make_float2(r, l);
+        tc::fence_before_thread_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&m->merge[1]);
+        if (!(ok = wait_warp(&m->merge[0], n_merge & 1, fail, P.status))) break;
+        tc::fence_after_thread_sync();
+        const float2 f = m->x[row];
+        f0 = f.x;
+        f1 = f.y;
+      } else {
+        float keep1 = 0.f;
+        if (joined) {
+          if (!(ok = wait_warp(&m->merge[1], n_merge & 1, fail, P.status))) break;
+          tc::fence_after_thread_sync();
+          const float2 x1 = m->x[row];
+          const float rn = fmaxf(r, x1.x);
+          if (rn != -INFINITY) {
+            f0 = ex2_approx(r - rn);
+            keep1 = ex2_approx(x1.x - rn);
+          }
+          l = l * f0 + x1.y * keep1;
+          r = rn;
+        }
+        const float f = l == 0.f ? 0.f
+                        : split  ? 1.f
+                                 : (P.kv.v_scale ? P.kv.v_scale[s.h] : 1.f) / l;
+        f0 *= f;
+        f1 = keep1 * f;
+        if (joined) {
+          m->x[row] = make_float2(f0, f1);
           tc::fence_before_thread_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&m->merge);
-          if (!(ok = wait_warp(&m->merged, n_merge & 1, fail, P.status))) break;
-          ++n_merge;
+          if (lane == 0) mbar_arrive(&m->merge[0]);
         }
-        continue;
-      }
-      float keep0 = 1.f, keep1 = 0.f;
-      if (joined) {
-        if (!(ok = wait_warp(&m->merge, n_merge & 1, fail, P.status))) break;
-        tc::fence_after_thread_sync();
-        ++n_merge;
-        const float2 x1 = m->x[row];
-        const float rn = fmaxf(r, x1.x);
-        if (rn != -INFINITY) {
-          keep0 = ex2_approx(r - rn);
-          keep1 = ex2_approx(x1.x - rn);
-        }
-        l = l * keep0 + x1.y * keep1;
-        r = rn;
       }
       if (warp_live) {
-        const bool none = l == 0.f;
+        const bool none = f0 == 0.f && f1 == 0.f;  // nothing seen: O may hold anything
         const int64_t trow = static_cast<int64_t>(s.r.q0 + first + tok) * P.Hq + s.h * G +
                              (row - tok * G);
         const int64_t prow = ((static_cast<int64_t>(blockIdx.x) * 2 + (s.opens ? 1 : 0)) * 2 +
@@ -875,8 +900,6 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         // a piece is 64 bytes of a row: 32 output values, or 16 of a partial O.
         // A lane's own row would cost a store a line each; the four lanes of a
         // quad trade 16-byte parts and write 64 bytes of each other's rows.
-        const float f = none ? 0.f : split ? 1.f : (P.kv.v_scale ? P.kv.v_scale[s.h] : 1.f) / l;
-        const float f0 = joined ? f * keep0 : f, f1 = f * keep1;
         unsigned char* mine = split ? wsp + ws.o + prow * D * 4
                                     : static_cast<unsigned char*>(P.out) + trow * D * 2;
         if (!live) mine = nullptr;
@@ -885,14 +908,15 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         for (int i = 0; i < 4; ++i)
           to[i] = reinterpret_cast<unsigned char*>(__shfl_sync(
                       0xFFFFFFFFu, reinterpret_cast<unsigned long long>(mine), (lane & ~3) + i));
-        const int step = split ? 16 : 32;
+        const uint32_t o_own = tmem + lanes + 256 + (joined ? 0 : w * 128);
+        const int c0 = joined && w == 1 ? D / 2 : 0, c1 = joined && w == 0 ? D / 2 : D;
 #pragma unroll 1
-        for (int c = 0; c < D; c += step) {
+        for (int c = c0; c < c1; c += 32) {
           uint32_t o[32];
-          tmem_ld32(o_t + (split ? c & ~31 : c), o);
+          tmem_ld32(o_own + c, o);
           if (joined) {
             uint32_t o1[32];
-            tmem_ld32(o_t + 128 + (split ? c & ~31 : c), o1);
+            tmem_ld32(o_own + 128 + c, o1);
             tc::tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 32; ++e)
@@ -902,40 +926,46 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f0);
           }
-          uint32_t y[16];
-          if (split) {
+          if (none) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) y[e] = c & 16 ? o[16 + e] : o[e];
-          } else {
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+          }
+#pragma unroll 1
+          for (int q = 0; q < (split ? 2 : 1); ++q) {
+            uint32_t y[16];
+            if (split) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float a = __uint_as_float(o[2 * e]), b = __uint_as_float(o[2 * e + 1]);
-              y[e] = P.dtype == DSPARK_F16 ? pack_f16(a, b) : pack_bf16(a, b);
+              for (int e = 0; e < 16; ++e) y[e] = q ? o[16 + e] : o[e];
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float a = __uint_as_float(o[2 * e]), b = __uint_as_float(o[2 * e + 1]);
+                y[e] = P.dtype == DSPARK_F16 ? pack_f16(a, b) : pack_bf16(a, b);
+              }
             }
-          }
-          if (none) {  // (O may hold anything)
+            quad_transpose16(y);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) y[e] = 0u;
+            for (int i = 0; i < 4; ++i)
+              if (to[i])
+                *reinterpret_cast<uint4*>(to[i] + (split ? (c + 16 * q) * 4 : c * 2) +
+                                          (lane & 3) * 16) =
+                    make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
           }
-          quad_transpose16(y);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (to[i])
-              *reinterpret_cast<uint4*>(to[i] + (split ? c * 4 : c * 2) + (lane & 3) * 16) =
-                  make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
         }
-        if (live) {
+        if (live && !(joined && w == 1)) {
           if (split) {
             reinterpret_cast<float2*>(wsp + ws.stats)[prow] = make_float2(r, l);
           } else if (P.lse) {
-            P.lse[trow] = none ? -INFINITY : (r - kOff + lg2_approx(l)) * kLn2;
+            P.lse[trow] = l == 0.f ? -INFINITY : (r - kOff + lg2_approx(l)) * kLn2;
           }
         }
       }
-      if (joined) {
+      if (joined) {  // neither goes on while the other reads its O
         tc::fence_before_thread_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&m->merged);
+        if (!(ok = wait_warp(&m->merged, n_merge & 1, fail, P.status))) break;
+        ++n_merge;
       }
       if (split && s.opens) {
         tail_split = true;
@@ -949,7 +979,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         }
       }
     }
-    if (tid == 0 && (!tail_split || !ok))
+    if (tid == 0 && !P.whole && (!tail_split || !ok))
       reinterpret_cast<JoinDesc*>(wsp + ws.desc)[blockIdx.x].parts = 0;
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
@@ -1193,14 +1223,18 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     } else if (kQuant && warp >= 12) {
       // ---- e4m3 tiles to fp16, in the MMA's layout ---------------------------------------
       if constexpr (kQuant) {
-        long long tiles = 0;
-        tiles = m->end > m->pos ? 2 * (m->end - m->pos) : 0;
         const int ct = tid - 12 * 32;  // 0..127: a key each
         constexpr int kChunks = D / 16;
-        for (long long n = 0; n < tiles; ++n) {
-          const uint32_t rs = static_cast<uint32_t>(n % C::kRaw);
-          const uint32_t st = static_cast<uint32_t>(n % C::kStages);
-          if (!wait_warp(&m->raw_full[rs], static_cast<uint32_t>(n / C::kRaw) & 1, fail, P.status))
+        Walk walk(P, m, tp);
+        Seg s;
+        uint32_t left = 0;  // tiles of the segment
+        for (uint32_t n = 0;; ++n, --left) {
+          if (left == 0) {
+            if (!walk.next(s)) break;
+            left = 2 * s.tiles();
+          }
+          const uint32_t rs = n % C::kRaw, st = n % C::kStages;
+          if (!wait_warp(&m->raw_full[rs], (n / C::kRaw) & 1, fail, P.status))
             break;
           const unsigned char* src = smem + C::raw + rs * C::kRawBytes + ct * D;
           uint4 x[kChunks];
@@ -1212,10 +1246,10 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
             x[c] = *reinterpret_cast<const uint4*>(src + ((c ^ sw) << 4));
           __syncwarp();
           if (lane == 0) mbar_arrive(&m->raw_empty[rs]);
-          if (!wait_warp(&m->kv_empty[st], (static_cast<uint32_t>(n / C::kStages) & 1) ^ 1, fail,
+          if (!wait_warp(&m->kv_empty[st], ((n / C::kStages) & 1) ^ 1, fail,
                        P.status))
             break;
-          if (ct == 0) *const_cast<volatile uint32_t*>(&m->filling) = static_cast<uint32_t>(n) + 1;
+          if (ct == 0) *const_cast<volatile uint32_t*>(&m->filling) = n + 1;
           unsigned char* dst = smem + C::kv + st * C::kTileBytes + ct * 128;
 #pragma unroll
           for (int c = 0; c < kChunks; ++c) {
@@ -1413,7 +1447,7 @@ cudaError_t launch(const PagedAttentionParams& p, const CUtensorMap& mq, const C
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   err = cudaLaunchKernelEx(&cfg, paged_attention_kernel<D, kF16, kQuant>, mq, mk, mv, p);
-  if (err != cudaSuccess) return err;
+  if (err != cudaSuccess || p.whole) return err;
   cfg.gridDim = dim3(grid, 16);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
@@ -1437,7 +1471,7 @@ size_t paged_attention_workspace_bytes(int B, int Hq, int Hkv, int D) {
   return Ws(D).total;
 }
 
-cudaError_t launch_paged_attention(const PagedAttentionParams& p, cudaStream_t stream) {
+cudaError_t launch_paged_attention(PagedAttentionParams p, cudaStream_t stream) {
   int dev = 0, sms = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err == cudaSuccess)
@@ -1445,6 +1479,10 @@ cudaError_t launch_paged_attention(const PagedAttentionParams& p, cudaStream_t s
   if (err != cudaSuccess) return err;
   CUtensorMap mq = {}, mk, mv;
   const dspark_paged_kv& kv = p.kv;
+  // the most key tiles a unit can have
+  int64_t keys = static_cast<int64_t>(p.M) << p.page_shift;
+  if (p.window > 0 && p.window + 2 * kRows < keys) keys = p.window + 2 * kRows;
+  p.whole = (keys + kKeys - 1) / kKeys + (p.window > 0 ? 1 : 0) <= kWholeTiles;
   if (!make_map(&mk, kv.k, kv, kv.k_block_stride, kv.k_head_stride, kv.k_token_stride) ||
       !make_map(&mv, kv.v, kv, kv.v_block_stride, kv.v_head_stride, kv.v_token_stride))
     return cudaErrorInvalidValue;
