@@ -64,9 +64,11 @@ constexpr int kMaxStages = 10;
 constexpr int kMaxRaw = 8;
 constexpr int kMaxCtas = 160;
 constexpr int kMinTiles = 2;  // key tiles a CTA takes at least
-// Units of at most this many key tiles are not split over CTAs: the second launch
-// that joins parts costs about as much as five tiles.
-constexpr int kWholeTiles = 4;
+// Units of at most this many key tiles are not split over CTAs: each part costs a
+// CTA a segment, and the launch that joins them 4 to 9 us (32 requests x 8 tokens
+// over 1400: 41 us whole, 50 split; one token over 600: 13 and 17). With units for
+// few of the SMs long ones gain more from more SMs (one token over 1400: 20 and 18).
+constexpr int kWholeTiles = 12, kWholeTilesFewUnits = 8;
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kGrow = 8.0f;  // the reference moves when the maximum passes it by 2^8
@@ -618,6 +620,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     const uint32_t s_t = tmem + lanes + w * kKeys;         // scores, then p
     const uint32_t o_t = tmem + lanes + 256 + w * 128;     // O
     constexpr float kOff = kF16 ? 7.0f : 0.0f;
+    constexpr int kCols = kQuant ? 64 : 128;  // scores held at a time
     uint32_t n_q = 0, n_seg = 0, n_item = 0, n_scan = 0, n_merge = 0;
     uint32_t base = 0;  // tiles loaded before this segment
     bool tail_split = false;
@@ -674,31 +677,39 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
           scan = key0 < all_lo || min(key0 + kKeys, s.r.len) > all_hi;
         }
         if (warp_live) {
-          uint32_t x[kKeys];
-          tmem_ld32(s_t, x);
-          tmem_ld32(s_t + 32, x + 32);
-          tmem_ld32(s_t + 64, x + 64);
-          tmem_ld32(s_t + 96, x + 96);
-          tc::tmem_wait_ld();
-          if (masked) {
-            const int clo = lo - key0, chi = hi - key0;
+          // (all 128 scores at once where the registers hold them, else 64 at a
+          // time, read twice)
+          uint32_t x[kCols];
+          auto load = [&](int c0) {
 #pragma unroll
-            for (int g = 0; g < kKeys; g += 32) {  // bit c: the row sees key g + c
-              const int a = min(max(clo - g, 0), 32), z = min(max(chi - g, 0), 32);
-              const uint32_t below = z == 32 ? 0xFFFFFFFFu : (1u << z) - 1u;
-              const uint32_t sees = a == 32 ? 0u : below >> a << a;
+            for (int c = 0; c < kCols; c += 32) tmem_ld32(s_t + c0 + c, x + c);
+            tc::tmem_wait_ld();
+            if (masked) {
+              const int clo = lo - key0 - c0, chi = hi - key0 - c0;
 #pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (!(sees >> c & 1u)) x[g + c] = 0xFF800000u;
+              for (int g = 0; g < kCols; g += 32) {  // bit c: the row sees key g + c
+                const int a = min(max(clo - g, 0), 32), z = min(max(chi - g, 0), 32);
+                const uint32_t below = z == 32 ? 0xFFFFFFFFu : (1u << z) - 1u;
+                const uint32_t sees = a == 32 ? 0u : below >> a << a;
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  if (!(sees >> c & 1u)) x[g + c] = 0xFF800000u;
+              }
             }
-          }
-          float mx0 = -INFINITY, mx1 = -INFINITY;
+          };
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int c0 = 0; c0 < kKeys; c0 += kCols) {
+            load(c0);
+            float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < kKeys; c += 4) {
-            mx0 = fmaxf(mx0, fmaxf(__uint_as_float(x[c]), __uint_as_float(x[c + 1])));
-            mx1 = fmaxf(mx1, fmaxf(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])));
+            for (int c = 0; c < kCols; c += 4) {
+              mx0 = fmaxf(mx0, fmaxf(__uint_as_float(x[c]), __uint_as_float(x[c + 1])));
+              mx1 = fmaxf(mx1, fmaxf(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])));
+            }
+            mx = fmaxf(mx, fmaxf(mx0, mx1));
           }
-          const float mx = fmaxf(mx0, mx1) * sl;
+          mx *= sl;
           float keep = 1.f;
           const bool move = mx > r + kGrow;  // also the first finite maximum
           if (move) {
@@ -720,27 +731,32 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
           const float neg = kOff - (r == -INFINITY ? 0.f : r);
           const unsigned long long sl2 = f2_pack(sl, sl), neg2 = f2_pack(neg, neg);
           unsigned long long sum = 0ull, sum1 = 0ull;
+#pragma unroll 1
+          for (int c0 = 0; c0 < kKeys; c0 += kCols) {
+            if (kCols < kKeys) load(c0);
 #pragma unroll
-          for (int c = 0; c < kKeys; c += 4) {
-            if (c == kKeys / 2) tmem_st32(s_t, x);
-            float a, b, e, f;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sl2, neg2),
-                      a, b);
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), sl2,
-                             neg2), e, f);
-            a = ex2_approx(a);
-            b = ex2_approx(b);
-            e = ex2_approx(e);
-            f = ex2_approx(f);
-            sum = f2_add(sum, f2_pack(a, b));
-            sum1 = f2_add(sum1, f2_pack(e, f));
-            x[c / 2] = kF16 ? pack_f16(a, b) : pack_bf16(a, b);
-            x[c / 2 + 1] = kF16 ? pack_f16(e, f) : pack_bf16(e, f);
+            for (int c = 0; c < kCols; c += 4) {
+              if (c == 64) tmem_st32(s_t, x);
+              float a, b, e, f;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sl2, neg2),
+                        a, b);
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), sl2,
+                               neg2), e, f);
+              a = ex2_approx(a);
+              b = ex2_approx(b);
+              e = ex2_approx(e);
+              f = ex2_approx(f);
+              sum = f2_add(sum, f2_pack(a, b));
+              sum1 = f2_add(sum1, f2_pack(e, f));
+              x[c / 2] = kF16 ? pack_f16(a, b) : pack_bf16(a, b);
+              x[c / 2 + 1] = kF16 ? pack_f16(e, f) : pack_bf16(e, f);
+            }
+            // p takes the place of scores that have been read: columns c0 / 2 ..
+            tmem_st32(s_t + (c0 + kCols) / 2 - 32, x + kCols / 2 - 32);
           }
           float a, b;
           f2_unpack(f2_add(sum, sum1), a, b);
           l += a + b;
-          tmem_st32(s_t + 32, x + 32);
           tmem_wait_st();
         }
         if (tail || scan) {
@@ -1482,7 +1498,8 @@ cudaError_t launch_paged_attention(PagedAttentionParams p, cudaStream_t stream) 
   // the most key tiles a unit can have
   int64_t keys = static_cast<int64_t>(p.M) << p.page_shift;
   if (p.window > 0 && p.window + 2 * kRows < keys) keys = p.window + 2 * kRows;
-  p.whole = (keys + kKeys - 1) / kKeys + (p.window > 0 ? 1 : 0) <= kWholeTiles;
+  p.whole = (keys + kKeys - 1) / kKeys + (p.window > 0 ? 1 : 0) <=
+            (3 * p.B * kv.kv_heads >= sms ? kWholeTiles : kWholeTilesFewUnits);
   if (!make_map(&mk, kv.k, kv, kv.k_block_stride, kv.k_head_stride, kv.k_token_stride) ||
       !make_map(&mv, kv.v, kv, kv.v_block_stride, kv.v_head_stride, kv.v_token_stride))
     return cudaErrorInvalidValue;
