@@ -6,6 +6,8 @@ The computation lives in the CUDA library built from ``csrc/`` (C ABI in
 * ``build``      -- compiles ``_build/libdspark.so`` with nvcc for sm_103a
 * ``_lib``       -- the binding (argument marshalling only)
 * ``step``       -- one decode step (Markov loop + verification) on device tensors
+* ``paged``      -- the paged key/value cache of the verification pass, and a
+                    speculative decoding loop on it
 * ``workloads``  -- seeded synthetic inputs
 """
 

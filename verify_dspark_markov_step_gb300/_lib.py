@@ -462,6 +462,8 @@ _PAGED_DTYPES = {torch.bfloat16: DSPARK_BF16, torch.float16: DSPARK_F16,
                  torch.float8_e4m3fn: DSPARK_E4M3}
 
 
+MAX_PAGED_BATCH = 1024  # DSPARK_MAX_PAGED_BATCH
+
 # The calls below are made once a layer and step, some for a few microseconds of
 # work, so their marshalling is kept lean: one pass over a tensor's properties,
 # the raw stream handle, one packed struct.

@@ -306,6 +306,17 @@ __device__ __forceinline__ void quad_transpose16(uint32_t (&y)[16]) {
   }
 }
 
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t phase) {  // no waiting
+  uint32_t ok;
+  asm volatile(
+      "{ .reg .pred p; mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n"
+      "selp.u32 %0, 1, 0, p; }"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(phase)
+      : "memory");
+  return ok != 0;
+}
+
 // A wait that gives up after kWaitLimitNs or when another warp has.
 __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t phase, volatile int* fail,
                                         int32_t* status) {
@@ -329,10 +340,15 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t phase, volatil
   return __all_sync(0xFFFFFFFFu, wait_on(bar, phase, fail, status));
 }
 
-// Two barriers at once (their latencies overlap when both are through).
+// Two barriers at once (their latencies overlap when both are through), and a
+// third one that is only looked at: `c_through` says whether to, and comes back
+// as whether it was through.
 __device__ __forceinline__ bool wait_warp2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb,
+                                           uint64_t* c, uint32_t pc, bool& c_through,
                                            volatile int* fail, int32_t* status) {
   const bool ra = mbar_try_wait(a, pa), rb = mbar_try_wait(b, pb);
+  const bool rc = c_through && mbar_test_wait(c, pc);
+  c_through = __all_sync(0xFFFFFFFFu, rc);
   if (__all_sync(0xFFFFFFFFu, ra && rb)) return true;
   return wait_warp(a, pa, fail, status) && wait_warp(b, pb, fail, status);
 }
@@ -1201,8 +1217,12 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
           const uint32_t n = w ? n_item1 : n_item0;
           const bool more = i + 2 < ni;
           const uint32_t ki = keys_of(more ? i + 2 : i);
+          // values, probabilities; the next keys, if they are there already (behind
+          // the converters of an 8-bit cache they hardly ever are)
+          bool keys = more && !kQuant;
           if (!(ok = wait_warp2(&m->kv_full[vi % C::kStages], (vi / C::kStages) & 1,
-                                &m->p_ready[w], n & 1, fail, P.status)))
+                                &m->p_ready[w], n & 1, &m->kv_full[ki % C::kStages],
+                                (ki / C::kStages) & 1, keys, fail, P.status)))
             break;
           tc::fence_after_thread_sync();
           const bool skip = *reinterpret_cast<volatile int*>(&m->skip_pv[w]) == static_cast<int>(n);
@@ -1216,9 +1236,10 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 mma_ts(o_d, p_d + c * 8, vd + ((c * 2048) >> 4), id_pv, i >= 2 || c != 0);
             }
             if (!more) tc::mma_commit(&m->o_full[w]);
+            if (keys) scores(i + 2, ki);
           }
           __syncwarp();
-          if (more) {
+          if (more && !keys) {
             if (!(ok = wait_warp(&m->kv_full[ki % C::kStages], (ki / C::kStages) & 1, fail,
                                  P.status)))
               break;
@@ -1236,10 +1257,10 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         tc::mma_commit(&m->drain);
         (void)mbar_wait(&m->drain, 0, P.status);
       }
-    } else if (kQuant && warp >= 12) {
+    } else if (kQuant && (warp == 10 || warp >= 13)) {
       // ---- e4m3 tiles to fp16, in the MMA's layout ---------------------------------------
       if constexpr (kQuant) {
-        const int ct = tid - 12 * 32;  // 0..127: a key each
+        const int ct = warp == 10 ? lane : tid - 12 * 32;  // 0..127: a key each
         constexpr int kChunks = D / 16;
         Walk walk(P, m, tp);
         Seg s;

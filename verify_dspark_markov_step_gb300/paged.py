@@ -1,0 +1,201 @@
+"""The paged key/value cache of the target model's verification pass, and a
+speculative decoding loop that runs on it.
+
+``PagedCache`` holds the buffers (the caches of every layer, the block tables, the
+free blocks, a step's offsets and slots) and makes the three library calls; every
+length stays on the device, so a step follows from the last one's accept counts
+without the host. ``main`` runs whole steps of a small random model: the drafter's
+Markov loop, the target's forward over anchor and drafts (projections in torch, cache
+and attention in the library), the rejection sampler.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import _lib
+
+
+class PagedCache:
+    """Caches of ``layers`` layers for ``slots`` request slots of up to ``max_len``
+    tokens, ``num_blocks`` blocks of ``page_size`` tokens shared by all slots (the same
+    tables serve every layer). ``cache_dtype`` is the rows' dtype or float8_e4m3fn;
+    ``k_scale``/``v_scale`` [layers, kv_heads] belong to the latter."""
+
+    def __init__(self, *, layers, slots, max_len, num_blocks, page_size, q_heads, kv_heads,
+                 head_dim, dtype=torch.bfloat16, cache_dtype=None, k_scale=None, v_scale=None,
+                 device="cuda"):
+        self.page_size, self.q_heads = page_size, q_heads
+        shape = (num_blocks, kv_heads, page_size, head_dim)
+        cache_dtype = cache_dtype or dtype
+        self.k, self.v = ([torch.zeros(shape, dtype=cache_dtype, device=device)
+                           for _ in range(layers)] for _ in range(2))
+        self.k_scale, self.v_scale = k_scale, v_scale
+
+        def ints(shape, value=0):
+            return torch.full(shape, value, dtype=torch.int32, device=device)
+        self.block_table = ints((slots, -(-max_len // page_size)), -1)
+        self.held_blocks, self.cached_lens = ints((slots,)), ints((slots,))
+        self.free_blocks = torch.arange(num_blocks - 1, -1, -1, dtype=torch.int32, device=device)
+        self.pool = torch.tensor([num_blocks, 0], dtype=torch.int32, device=device)
+        self.status = ints((1,))
+        self._dims = (q_heads, kv_heads, head_dim)
+        self._made = {}
+        self._workspace = None
+
+    def plan(self, req_state_idx, new_lens, max_tokens, num_accepted=None, stream=None):
+        """Block tables and slots of a step in which request b brings new_lens[b] tokens
+        (at most max_tokens in all); with num_accepted the slots' lengths first grow by
+        what the last step's verification kept. Returns (query_start, seq_lens,
+        positions, slot_map), which the next plan of as many requests and tokens
+        overwrites."""
+        B = req_state_idx.shape[0]
+        if (B, max_tokens) not in self._made:
+            dev = self.pool.device
+            self._made[B, max_tokens] = (
+                torch.empty(B + 1, dtype=torch.int32, device=dev),
+                torch.empty(B, dtype=torch.int32, device=dev),
+                torch.empty(max_tokens, dtype=torch.int64, device=dev),
+                torch.empty(max_tokens, dtype=torch.int64, device=dev))
+        self.req_state_idx = req_state_idx
+        self.step = self._made[B, max_tokens]
+        _lib.paged_tables(req_state_idx, new_lens, self.cached_lens, self.block_table,
+                          self.held_blocks, self.free_blocks, self.pool, *self.step,
+                          self.page_size, num_accepted=num_accepted, status=self.status,
+                          stream=stream)
+        return self.step
+
+    def _scales(self, layer):
+        return {"k_scale": None if self.k_scale is None else self.k_scale[layer],
+                "v_scale": None if self.v_scale is None else self.v_scale[layer]}
+
+    def append(self, layer, k, v, stream=None):
+        """The planned step's keys and values [max_tokens, kv_heads, head_dim] into the
+        pages of a layer."""
+        _lib.kv_append(k, v, self.k[layer], self.v[layer], self.step[3], status=self.status,
+                       stream=stream, **self._scales(layer))
+
+    def attend(self, layer, q, out, causal=True, window=0, scale=None, lse=None, stream=None):
+        """The planned step's attention of q [max_tokens, q_heads, head_dim] over a
+        layer's pages, into out."""
+        if self._workspace is None:
+            need = _lib.paged_attention_workspace_bytes(_lib.MAX_PAGED_BATCH, *self._dims)
+            self._workspace = _lib.workspace(need, self.pool.device)
+        _lib.paged_attention(q, self.k[layer], self.v[layer], self.block_table,
+                             self.req_state_idx, self.step[0], self.step[1], out, scale=scale,
+                             causal=causal, window=window, lse=lse,
+                             workspace_buf=self._workspace, status=self.status, stream=stream,
+                             **self._scales(layer))
+
+    def status_code(self) -> int:
+        return int(self.status.item())
+
+
+class ToyTarget:
+    """A random transformer without feed-forward blocks: embedding, ``layers`` of
+    attention with a residual, and the embedding again as the output head."""
+
+    def __init__(self, V, layers, q_heads, kv_heads, head_dim, dtype=torch.bfloat16, seed=0,
+                 device="cuda"):
+        g = torch.Generator(device=device).manual_seed(seed)
+        width = q_heads * head_dim
+
+        def w(*shape):
+            return (torch.randn(*shape, device=device, generator=g) * shape[0] ** -0.5).to(dtype)
+        self.heads = (q_heads, kv_heads, head_dim)
+        self.embed = torch.randn(V, width, device=device, generator=g).to(dtype)
+        self.qkv = [w(width, (q_heads + 2 * kv_heads) * head_dim) for _ in range(layers)]
+        self.proj = [w(width, width) for _ in range(layers)]
+
+    def forward(self, tokens, cache: PagedCache, stream=None):
+        """Logits [T, V] (fp32) of the planned step's tokens [T]."""
+        Hq, H, D = self.heads
+        x = self.embed[tokens]
+        for layer, (wqkv, wo) in enumerate(zip(self.qkv, self.proj)):
+            qkv = x @ wqkv
+            q, k, v = qkv.split((Hq * D, H * D, H * D), 1)
+            cache.append(layer, k.unflatten(1, (H, D)), v.unflatten(1, (H, D)), stream=stream)
+            out = torch.zeros(x.shape[0], Hq, D, dtype=x.dtype, device=x.device)
+            cache.attend(layer, q.unflatten(1, (Hq, D)), out, stream=stream)
+            x = x + out.flatten(1) @ wo
+        return (x @ self.embed.T).float()
+
+
+def speculative_loop(step, target: ToyTarget, cache: PagedCache, prompts, steps, draft_logits):
+    """``steps`` speculative steps after the prompts (a list of token lists, one for each
+    request of the DecodeStep ``step``). draft_logits(tokens) gives the drafter's base
+    logits [B, K, V] from the anchors [B]. Returns the emitted tokens (prompt excluded)
+    of each request."""
+    w = step.w
+    B, K, V = w.B, w.K, w.V
+    dev = step.device
+    lens = torch.tensor([len(p) for p in prompts], dtype=torch.int32, device=dev)
+    flat = torch.tensor([t for p in prompts for t in p], dtype=torch.int64, device=dev)
+    query_start, *_ = cache.plan(step.rsi, lens, flat.numel())
+    logits = target.forward(flat, cache)
+    # the prompts are in the cache; their last logits choose the first anchors
+    cache.cached_lens.index_add_(0, step.rsi, lens)
+    anchor = logits[query_start[1:].long() - 1].argmax(1)
+    emitted = [anchor[:, None]]
+    new = torch.full((B,), K + 1, dtype=torch.int32, device=dev)
+    accepted = None
+    for _ in range(steps):
+        step.base.copy_(draft_logits(anchor))
+        step.anchor.copy_(anchor)
+        query_start, seq_lens, positions, _ = cache.plan(step.rsi, new, B * (K + 1), accepted)
+        step.pos.copy_(positions[query_start[:-1].long()] + 1)  # of the first draft
+        step.markov()
+        tokens = torch.cat([anchor[:, None], step.draft.long()], 1).reshape(-1)
+        step.target.copy_(target.forward(tokens, cache).view(B, K + 1, V))
+        step.verify()
+        accepted = step.num_accepted
+        anchor = step.out.long().gather(1, accepted.long()[:, None])[:, 0]
+        emitted.append(step.out.long().clone())
+    out = torch.cat(emitted, 1).tolist()
+    return [[t for t in row if t >= 0] for row in out]
+
+
+def main(argv=None):
+    """Speculative decoding of a small random model on the paged cache:
+    python -m verify_dspark_markov_step_gb300.paged --batch 8 --steps 20"""
+    import argparse
+
+    from . import build, workloads
+    from .step import DecodeStep
+
+    ap = argparse.ArgumentParser()
+    ap.add_argument("--batch", type=int, default=8)
+    ap.add_argument("--drafts", type=int, default=7)
+    ap.add_argument("--prompt", type=int, default=500)
+    ap.add_argument("--steps", type=int, default=20)
+    ap.add_argument("--page", type=int, default=16)
+    ap.add_argument("--e4m3", action="store_true", help="8-bit cache")
+    args = ap.parse_args(argv)
+    build.build()
+    V, layers, heads = 4096, 2, (8, 2, 128)
+    w = workloads.custom(args.batch, args.drafts, V, 64, w_std=0.0)
+    step = DecodeStep(w)
+    target = ToyTarget(V, layers, *heads)
+    max_len = args.prompt + (args.steps + 1) * (args.drafts + 1)
+    ones = torch.full((layers, heads[1]), 0.02, device="cuda") if args.e4m3 else None
+    cache = PagedCache(layers=layers, slots=w.S, max_len=max_len,
+                       num_blocks=w.S * -(-max_len // args.page), page_size=args.page,
+                       q_heads=heads[0], kv_heads=heads[1], head_dim=heads[2],
+                       cache_dtype=torch.float8_e4m3fn if args.e4m3 else None, k_scale=ones,
+                       v_scale=ones)
+    g = torch.Generator().manual_seed(1)
+    prompts = [torch.randint(V, (args.prompt - 3 * b,), generator=g).tolist()
+               for b in range(args.batch)]
+    scores = (target.embed @ target.embed.T).float()
+
+    def draft_logits(anchor):  # a drafter that expects the anchor's neighbours
+        return scores[anchor][:, None].expand(-1, args.drafts, -1)
+    out = speculative_loop(step, target, cache, prompts, args.steps, draft_logits)
+    torch.cuda.synchronize()
+    made = sum(len(o) - 1 for o in out)
+    print(f"{args.batch} requests, {args.steps} steps: status {cache.status_code()} / "
+          f"{step.status_code()}, {made / args.steps / args.batch:.2f} tokens a step and request, "
+          f"{int(cache.pool[0])} blocks free")
+
+
+if __name__ == "__main__":
+    main()
