@@ -83,20 +83,16 @@ kv_append_kernel(KvAppendParams P, int width, int abreast) {
   for (int i = 0; i < kPer; ++i) {
     const int t = t0 + i * abreast;
     slot[i] = t < P.T ? P.slot_map[t] : -1;
-    if (slot[i] >= P.num_slots) {
-      report(P.status, DSPARK_ERR_BOUNDS);
-      slot[i] = -1;
-    }
   }
   const int cd = P.D / 8, chunks = P.H * cd;  // pieces of a head, of a token's keys
   for (int p = threadIdx.x - sub * width; p < 2 * chunks; p += width) {
     const int which = p >= chunks ? 1 : 0;  // keys, then values
     const int c = p - which * chunks, h = c / cd;
     const uint16_t* src = static_cast<const uint16_t*>(P.src[which]) + c * 8;
-    uint4 x[kPer];
+    uint4 x[kPer];  // (not waiting for the slots: rows without one are read for nothing)
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (slot[i] >= 0)
+      if (t0 + i * abreast < P.T)
         x[i] = *reinterpret_cast<const uint4*>(
             src + static_cast<int64_t>(t0 + i * abreast) * P.src_stride[which]);
     const int64_t head = h * P.head_stride[which] + (c - h * cd) * 8;
@@ -108,6 +104,10 @@ kv_append_kernel(KvAppendParams P, int width, int abreast) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       if (slot[i] < 0) continue;
+      if (slot[i] >= P.num_slots) {
+        report(P.status, DSPARK_ERR_BOUNDS);
+        continue;
+      }
       const int64_t at = (slot[i] >> P.page_shift) * P.block_stride[which] +
                          (slot[i] & ((1 << P.page_shift) - 1)) * P.token_stride[which] + head;
       if constexpr (kQuantise) {

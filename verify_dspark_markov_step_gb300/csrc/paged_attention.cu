@@ -64,6 +64,9 @@ constexpr int kMaxStages = 10;
 constexpr int kMaxRaw = 8;
 constexpr int kMaxCtas = 160;
 constexpr int kMinTiles = 2;  // key tiles a CTA takes at least
+// What a unit costs besides its key tiles, in tiles (its query rows, the first
+// scores, masks and the result overlap with little): the runs are of equal cost.
+constexpr int kUnitTiles = 3;
 // Units of at most this many key tiles are not split over CTAs: each part costs a
 // CTA a segment, and the launch that joins them 4 to 9 us (32 requests x 8 tokens
 // over 1400: 41 us whole, 50 split; one token over 600: 13 and 17). With units for
@@ -133,6 +136,7 @@ struct Misc {
   Seg seg[2];  // of the segment whose first row tile is in the slot
   uint32_t tmem;
   int fail;
+  uint32_t total;    // tiles that the producer has loaded, once it is done
   uint32_t filling;  // tiles of the MMA's ring whose stage is being filled, or was
   int bad[2];      // the last tile whose values were found non-finite, per warpgroup
   int skip_pv[2];  // the last item whose P V the warpgroup did itself
@@ -340,6 +344,25 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t phase, volatil
   return __all_sync(0xFFFFFFFFu, wait_on(bar, phase, fail, status));
 }
 
+// A converter warp's wait for the n-th tile; false after the last, too.
+__device__ __forceinline__ bool wait_raw(uint64_t* bar, uint32_t phase, Misc* m, uint32_t n,
+                                         int32_t* status) {
+  volatile int* fail = &m->fail;
+  bool there = mbar_try_wait(bar, phase);
+  if (!there) {
+    const unsigned long long t0 = globaltimer_ns();
+    while (!(there = mbar_try_wait_sleep(bar, phase, 500u))) {
+      if (n >= *const_cast<volatile uint32_t*>(&m->total) || *fail) break;
+      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        report(status, DSPARK_ERR_TIMEOUT);
+        *fail = 1;
+        break;
+      }
+    }
+  }
+  return __all_sync(0xFFFFFFFFu, there);
+}
+
 // Two barriers at once (their latencies overlap when both are through), and a
 // third one that is only looked at: `c_through` says whether to, and comes back
 // as whether it was through.
@@ -419,10 +442,11 @@ __device__ __forceinline__ void unit_tiles(const PagedAttentionParams& P, const 
   je = max(jb + 1, (hi + kKeys - 1) / kKeys);
 }
 
-// The segments of this CTA in order.
+// The segments of this CTA in order. Positions count the units' costs: the
+// first kUnitTiles places of a unit stand for no tile.
 struct Walk {
   const PagedAttentionParams& P;
-  int tp, b, h, u, jb, je, j, per;
+  int tp, b, h, u, jb, je, v, per;  // v: place within the unit
   long long pos, end;
   Request r;
   __device__ Walk(const PagedAttentionParams& P_, const Misc* m, int tp_)
@@ -433,19 +457,19 @@ struct Walk {
     long long rem = m->start_rem;
     for (;; ++u) {
       unit_tiles(P, r, tp, u, jb, je);
-      if (rem < je - jb) break;
-      rem -= je - jb;
+      if (rem < cost()) break;
+      rem -= cost();
     }
-    j = jb + static_cast<int>(rem);
-    if (P.whole && rem != 0) {  // the CTA before takes the unit to its end
-      pos += je - j;
-      j = je;
+    v = static_cast<int>(rem);
+    if (P.whole && v != 0) {  // the CTA before takes the unit to its end
+      pos += cost() - v;
       advance();
     }
   }
+  __device__ int cost() const { return je - jb + kUnitTiles; }
   // To the next unit, if the run goes on.
   __device__ void advance() {
-    if (j != je || pos >= end) return;
+    if (pos >= end) return;
     if (++u * 2 * tp >= r.n) {
       u = 0;
       if (++h == P.kv.kv_heads) {
@@ -456,25 +480,32 @@ struct Walk {
       }
     }
     unit_tiles(P, r, tp, u, jb, je);
-    j = jb;
+    v = 0;
   }
   __device__ bool next(Seg& s) {
-    if (pos >= end) return false;
-    s.r = r;
-    s.h = h;
-    s.t0 = u * 2 * tp;
-    s.t1 = min(r.n, s.t0 + 2 * tp);
-    s.pair = s.t1 - s.t0 > tp;
-    s.j0 = j;
-    s.j1 = P.whole ? je : static_cast<int>(min(static_cast<long long>(je), j + (end - pos)));
-    s.opens = j == jb;
-    s.closes = s.j1 == je;
-    s.c1 = static_cast<int>((pos + (je - j) - 1) / per);
-    s.end = false;
-    pos += s.j1 - s.j0;
-    j = s.j1;
-    advance();
-    return true;
+    while (pos < end) {
+      const int left = cost() - v;
+      const int take = P.whole ? left : static_cast<int>(min(static_cast<long long>(left), end - pos));
+      s.j0 = jb + max(0, v - kUnitTiles);
+      s.j1 = jb + max(0, v + take - kUnitTiles);
+      const bool some = s.j1 > s.j0;
+      if (some) {
+        s.r = r;
+        s.h = h;
+        s.t0 = u * 2 * tp;
+        s.t1 = min(r.n, s.t0 + 2 * tp);
+        s.pair = s.t1 - s.t0 > tp;
+        s.opens = s.j0 == jb;
+        s.closes = s.j1 == je;
+        s.c1 = static_cast<int>((pos + left - 1) / per);
+        s.end = false;
+      }
+      pos += take;
+      v += take;
+      if (take == left) advance();
+      if (some) return true;
+    }
+    return false;
   }
 };
 
@@ -500,7 +531,7 @@ __device__ void make_plan(const PagedAttentionParams& P, Misc* m, unsigned long 
       for (int u = 0; u < units; ++u) {
         int jb, je;
         unit_tiles(P, r, tp, u, jb, je);
-        cost += je - jb;
+        cost += je - jb + kUnitTiles;
       }
     unsigned int todo = __ballot_sync(0xFFFFFFFFu, big);
     while (todo) {
@@ -514,7 +545,7 @@ __device__ void make_plan(const PagedAttentionParams& P, Misc* m, unsigned long 
       for (int u = lane; u < ou; u += 32) {
         int jb, je;
         unit_tiles(P, o, tp, u, jb, je);
-        c += je - jb;
+        c += je - jb + kUnitTiles;
       }
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1) c += __shfl_xor_sync(0xFFFFFFFFu, c, s);
@@ -608,6 +639,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
       mbar_init(&m->merged, 8);
       mbar_init(&m->drain, 1);
       m->filling = 0;
+      m->total = 0xFFFFFFFFu;
       m->fail = 0;
     }
     fence_mbar_init();
@@ -655,6 +687,18 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
       // one thread of the warpgroup gives back what its MMAs have read: a tile
       // once, or twice where the other warpgroup has no use for it
       const bool giver = (warp & 3) == 0 && lane == 0;
+      // the query rows and the segment's description, of which every warp has its
+      // copy by now, after this warpgroup's last scores
+      auto give_queries = [&]() {
+        if (lane == 0) {
+          mbar_arrive(&m->q_empty[n_q & 1]);
+          if (s.pair) mbar_arrive(&m->q_empty[n_q1 & 1]);
+        }
+      };
+      if (items == 0) {
+        __syncwarp();
+        give_queries();
+      }
       auto give_tile = [&](uint32_t n) {
         if (s.pair)
           mbar_arrive(&m->kv_empty[n % C::kStages]);
@@ -683,6 +727,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
           give_tile(base + s.k_place(s.tile(w, k)));
           if (k > 0) give_tile(base + s.v_place(s.tile(w, k - 1)));
         }
+        if (k == items - 1) give_queries();
         __syncwarp();
         bool scan = false, tail = false;
         const bool masked = key0 < all_lo || key0 + kKeys > all_hi;
@@ -874,12 +919,6 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         if (giver) give_tile(base + s.v_place(s.tile(w, items - 1)));
       }
       base += 2 * s.tiles();
-      // the query rows and the segment's description (every warp has its copy)
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&m->q_empty[n_q & 1]);
-        if (s.pair) mbar_arrive(&m->q_empty[n_q1 & 1]);
-      }
       n_q += s.pair ? 2 : 1;
       // ---- the segment's result -----------------------------------------------------
       // A joined segment's is f0 O_0 + f1 O_1: the first warpgroup works out the
@@ -1081,6 +1120,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         }
         base += 2 * nt;
       }
+      if (kQuant && lane == 0) *const_cast<volatile uint32_t*>(&m->total) = base;
     } else if (warp == 11) {
       // ---- scout: segments and their query rows ---------------------------------------
       uint32_t n_q = 0;
@@ -1262,17 +1302,9 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
       if constexpr (kQuant) {
         const int ct = warp == 10 ? lane : tid - 12 * 32;  // 0..127: a key each
         constexpr int kChunks = D / 16;
-        Walk walk(P, m, tp);
-        Seg s;
-        uint32_t left = 0;  // tiles of the segment
-        for (uint32_t n = 0;; ++n, --left) {
-          if (left == 0) {
-            if (!walk.next(s)) break;
-            left = 2 * s.tiles();
-          }
+        for (uint32_t n = 0;; ++n) {
           const uint32_t rs = n % C::kRaw, st = n % C::kStages;
-          if (!wait_warp(&m->raw_full[rs], (n / C::kRaw) & 1, fail, P.status))
-            break;
+          if (!wait_raw(&m->raw_full[rs], (n / C::kRaw) & 1, m, n, P.status)) break;
           const unsigned char* src = smem + C::raw + rs * C::kRawBytes + ct * D;
           uint4 x[kChunks];
           // TMA swizzled the 16-byte pieces of a row by the row: 8 rows of 128
