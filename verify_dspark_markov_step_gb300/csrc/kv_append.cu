@@ -40,16 +40,8 @@ __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
   return r;
 }
 
-// x / scale of two values, rounded to 8 bits. With r = rn(1 / scale), q = rn(x r)
-// and the residual x - q scale (exact in an FMA), rn(q + (x - q scale) r) is the
-// correctly rounded quotient (Markstein's theorem, as for temp_div2) wherever
-// nothing over- or underflows. What underflows is far below the smallest 8-bit
-// value; overflow, infinities and NaN make the sum NaN, and those, and scales
-// outside [2^-30, 2^30] (`slow`), take the division itself.
 template <bool kF16>
-__device__ __forceinline__ uint32_t quantise_pair(uint32_t w, unsigned long long r2,
-                                                  unsigned long long nt2, bool slow) {
-  float a, b;
+__device__ __forceinline__ void unpack(uint32_t w, float& a, float& b) {
   if constexpr (kF16) {
     a = half_bits_to_float(w & 0xFFFFu);
     b = half_bits_to_float(w >> 16);
@@ -57,21 +49,54 @@ __device__ __forceinline__ uint32_t quantise_pair(uint32_t w, unsigned long long
     a = __uint_as_float(w << 16);
     b = __uint_as_float(w & 0xFFFF0000u);
   }
-  const unsigned long long z = f2_pack(a, b), q = f2_mul(z, r2);
-  float x0, x1;
-  f2_unpack(f2_fma(f2_fma(q, nt2, z), r2, q), x0, x1);
-  if (slow || !(x0 + x1 == x0 + x1)) {  // (no sum of two quotients overflows here)
-    float t0, t1;
-    f2_unpack(nt2, t0, t1);
-    x0 = __fdiv_rn(a, -t0);
-    x1 = __fdiv_rn(b, -t1);
+}
+
+// A piece by divisions (out of line: hardly ever called).
+template <bool kF16>
+__device__ __noinline__ uint2 quantise_by_division(uint4 x, float scale) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t y[4];
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    unpack<kF16>(w[i], a, b);
+    y[i] = e4m3_pair(__fdiv_rn(a, scale), __fdiv_rn(b, scale));
   }
-  return e4m3_pair(x0, x1);
+  return make_uint2(y[0] | (y[1] << 16), y[2] | (y[3] << 16));
+}
+
+// The 8 values of a piece over the scale, rounded to 8 bits. With r = rn(1 /
+// scale), q = rn(x r) and the residual x - q scale (exact in an FMA),
+// rn(q + (x - q scale) r) is the correctly rounded quotient (Markstein's
+// theorem, as for temp_div2) wherever nothing over- or underflows. What
+// underflows is far below the smallest 8-bit value; overflow, infinities and
+// NaN make the quotient and so the piece's sum NaN, and such pieces, and scales
+// outside [2^-30, 2^30] (`slow`), take the division itself.
+template <bool kF16>
+__device__ __forceinline__ uint2 quantise(uint4 x, unsigned long long r2, unsigned long long nt2,
+                                          float scale, bool slow) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t y[4];
+  unsigned long long sum = 0ull;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    unpack<kF16>(w[i], a, b);
+    const unsigned long long z = f2_pack(a, b), q = f2_mul(z, r2);
+    const unsigned long long v = f2_fma(f2_fma(q, nt2, z), r2, q);
+    sum = i ? f2_add(sum, v) : v;
+    f2_unpack(v, a, b);
+    y[i] = e4m3_pair(a, b);
+  }
+  float s0, s1;
+  f2_unpack(sum, s0, s1);
+  s0 += s1;
+  if (slow || s0 != s0) return quantise_by_division<kF16>(x, scale);
+  return make_uint2(y[0] | (y[1] << 16), y[2] | (y[3] << 16));
 }
 
 // `width` threads share a token, `abreast` tokens are taken at a time.
 template <bool kQuantise, bool kF16, int kPer>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 5)
 kv_append_kernel(KvAppendParams P, int width, int abreast) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -108,14 +133,12 @@ kv_append_kernel(KvAppendParams P, int width, int abreast) {
         report(P.status, DSPARK_ERR_BOUNDS);
         continue;
       }
-      const int64_t at = (slot[i] >> P.page_shift) * P.block_stride[which] +
-                         (slot[i] & ((1 << P.page_shift) - 1)) * P.token_stride[which] + head;
+      const int block = static_cast<int>(slot[i] >> P.page_shift);
+      const int off = static_cast<int>(slot[i]) & ((1 << P.page_shift) - 1);
+      const int64_t at = block * P.block_stride[which] + off * P.token_stride[which] + head;
       if constexpr (kQuantise) {
-        const uint32_t lo = quantise_pair<kF16>(x[i].x, r2, nt2, slow) |
-                            (quantise_pair<kF16>(x[i].y, r2, nt2, slow) << 16);
-        const uint32_t hi = quantise_pair<kF16>(x[i].z, r2, nt2, slow) |
-                            (quantise_pair<kF16>(x[i].w, r2, nt2, slow) << 16);
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(P.dst[which]) + at) = make_uint2(lo, hi);
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(P.dst[which]) + at) =
+            quantise<kF16>(x[i], r2, nt2, scale, slow);
       } else {
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.dst[which]) + at) = x[i];
       }

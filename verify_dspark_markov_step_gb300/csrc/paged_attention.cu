@@ -725,7 +725,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         tc::fence_after_thread_sync();
         if (giver) {  // these scores are there: the keys, and the values before
           give_tile(base + s.k_place(s.tile(w, k)));
-          if (k > 0) give_tile(base + s.v_place(s.tile(w, k - 1)));
+          if (!kQuant && k > 0) give_tile(base + s.v_place(s.tile(w, k - 1)));
         }
         if (k == items - 1) give_queries();
         __syncwarp();
@@ -916,7 +916,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         if (!(ok = wait_warp(&m->o_full[w], n_seg & 1, fail, P.status))) break;
         tc::fence_after_thread_sync();
         ++n_seg;
-        if (giver) give_tile(base + s.v_place(s.tile(w, items - 1)));
+        if (!kQuant && giver) give_tile(base + s.v_place(s.tile(w, items - 1)));
       }
       base += 2 * s.tiles();
       n_q += s.pair ? 2 : 1;
@@ -1274,6 +1274,10 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
 #pragma unroll
               for (int c = 0; c < kKeys / 16; ++c)
                 mma_ts(o_d, p_d + c * 8, vd + ((c * 2048) >> 4), id_pv, i >= 2 || c != 0);
+            }
+            if constexpr (kQuant) {  // few stages: values are given back at once
+              tc::mma_commit(&m->kv_empty[vi % C::kStages]);
+              if (!s.pair) tc::mma_commit(&m->kv_empty[vi % C::kStages]);
             }
             if (!more) tc::mma_commit(&m->o_full[w]);
             if (keys) scores(i + 2, ki);
