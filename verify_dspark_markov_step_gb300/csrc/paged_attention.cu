@@ -29,16 +29,17 @@
 //
 // Warps: 0-3 and 4-7 softmax (thread = row = lane of tensor memory), 9 issues
 // the MMAs (the warpgroups' in turn, which keeps one's softmax beside the other's
-// products; waits and commits cost it time that the tensor core then idles, so
-// an item has two waits and one commit, and the softmax warps release what the
-// committed MMAs have read), 8 and 10
-// are the TMA producers (keys and values go through one ring; each issues half of
-// a tile's boxes), 11 the scout: it walks the units ahead of the others, loads
-// their query rows (a ring of two row tiles) and publishes what the others need
-// to know of them. With an 8-bit cache 8 loads alone, the scout brings query rows to fp16 by a power of two per row, and
-// 12-15 convert e4m3 tiles to fp16 in shared memory (the 8-bit values are exact
-// in fp16; an 8-bit MMA would want the queries and p in 8 bits too). Pages: a
-// 128-key tile is 128 / page_size TMA boxes.
+// products; what the issuer spends on waits and commits the tensor core idles, so
+// an item has one wait and one commit, and the softmax warps give back the tiles
+// that committed MMAs have read), 8 and 10 are the TMA producers (keys and values
+// go through one ring in the order of their use; each issues half of a tile's
+// boxes), 11 the scout: it walks the units ahead of the others, loads their query
+// rows (a ring of two row tiles) and publishes what the others need to know of
+// them. With an 8-bit cache 8 loads alone, 10 and 13-15 convert e4m3 tiles to fp16
+// in shared memory (the 8-bit values are exact in fp16; an 8-bit MMA would want
+// the queries and p in 8 bits too), and the softmax warps bring the query rows to
+// fp16 by a power of two per row. Pages: a 128-key tile is 128 / page_size TMA
+// boxes.
 //
 // What a row does not see must not reach it: masked scores are replaced (not
 // added to), value rows past the request's last token are zeroed in shared
@@ -130,7 +131,7 @@ struct Seg {
 struct Misc {
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
   uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];
-  uint64_t q_full[2], q_empty[2];
+  uint64_t q_full[2], q_ready[2], q_empty[2];
   uint64_t s_full[2], p_ready[2], o_full[2], scanned[2];
   uint64_t merge[2], merged, drain;
   Seg seg[2];  // of the segment whose first row tile is in the slot
@@ -627,6 +628,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     }
     if (lane < 2) {
       mbar_init(&m->q_full[lane], 1);
+      mbar_init(&m->q_ready[lane], 4);
       mbar_init(&m->q_empty[lane], 8);  // the softmax warps
       mbar_init(&m->s_full[lane], 1);
       mbar_init(&m->p_ready[lane], 4);
@@ -645,7 +647,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     fence_mbar_init();
   }
   if (tid == 0) {
-    if (!kQuant) tc::prefetch_tensormap(&tmap_q);
+    tc::prefetch_tensormap(&tmap_q);
     tc::prefetch_tensormap(&tmap_k);
     tc::prefetch_tensormap(&tmap_v);
   }
@@ -682,7 +684,6 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
       const uint32_t n_q1 = n_q + 1;
       if (s.pair && !(ok = wait_warp(&m->q_full[n_q1 & 1], (n_q1 >> 1) & 1, fail, P.status))) break;
       float sl = sl0 * (P.kv.k_scale ? P.kv.k_scale[s.h] : 1.f);
-      if constexpr (kQuant) sl *= row_scale[((n_q + (s.pair ? w : 0)) & 1) * kRows + row];
       const int items = s.items(w);
       // one thread of the warpgroup gives back what its MMAs have read: a tile
       // once, or twice where the other warpgroup has no use for it
@@ -718,6 +719,49 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
       int all_lo, all_hi, unused;
       key_range(P, s.r.n, s.r.len, first, first + 1, unused, all_hi);
       key_range(P, s.r.n, s.r.len, first + ntok - 1, first + ntok, all_lo, unused);
+      if constexpr (kQuant) {
+        // The row tile to fp16, in place, each row's largest value brought to 2^14
+        // by a power of two: exact but for values 2^-28 below it. D / 8
+        // neighbouring lanes hold a row.
+        const uint32_t mine = n_q + (s.pair ? w : 0);
+        float* scales = row_scale + (mine & 1) * kRows;
+        if (s.pair || w == 0) {
+          unsigned char* q_s = smem + C::q + (mine & 1) * C::kTileBytes;
+#pragma unroll 2
+          for (int i = row; i < nrow * (D / 8); i += kRows) {
+            const int rr = i / (D / 8), c = i % (D / 8);
+            uint4* at = reinterpret_cast<uint4*>(q_s + (c >> 3) * (kRows * 128) + rr * 128 +
+                                                 (((c & 7) ^ (rr & 7)) << 4));
+            const uint4 x = *at;
+            uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+            float v[8];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              if (P.dtype == DSPARK_F16)
+                unpack_f16(xw[y], v[2 * y], v[2 * y + 1]);
+              else
+                unpack_bf16(xw[y], v[2 * y], v[2 * y + 1]);
+            }
+            uint32_t big = 0;
+#pragma unroll
+            for (int y = 0; y < 8; ++y) big = max(big, __float_as_uint(v[y]) & 0x7FFFFFFFu);
+            const unsigned int who = ((1u << (D / 8)) - 1u) << (lane & ~(D / 8 - 1));
+#pragma unroll
+            for (int o = D / 16; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(who, big, o));
+            const int ex = big == 0u ? 14 : max(static_cast<int>(big >> 23) - 127, -112);
+            const float up = __uint_as_float(static_cast<uint32_t>(14 - ex + 127) << 23);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) xw[y] = pack_f16(v[2 * y] * up, v[2 * y + 1] * up);
+            if (c == 0) scales[rr] = __uint_as_float(static_cast<uint32_t>(ex - 14 + 127) << 23);
+            *at = make_uint4(xw[0], xw[1], xw[2], xw[3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&m->q_ready[mine & 1]);
+        }
+        if (!(ok = wait_warp(&m->q_ready[mine & 1], (mine >> 1) & 1, fail, P.status))) break;
+        sl *= scales[row];
+      }
       float r = -INFINITY, l = 0.f;  // reference (scaled), sum
       for (int k = 0; k < items; ++k, ++n_item) {
         const int key0 = s.tile(w, k) * kKeys;
@@ -1136,72 +1180,16 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
           if (!(ok = wait_warp(&m->q_empty[sl], ((n_q >> 1) & 1) ^ 1, fail, P.status))) break;
           if (f == 0 && lane == 0) m->seg[sl] = s;
           const int tok0 = s.r.q0 + s.t0 + f * tp;
-          if constexpr (!kQuant) {
-            if (lane == 0) {
-              if (more) {
-                mbar_arrive_expect_tx(&m->q_full[sl], C::kHalves * 128 * G * tp);
+          if (lane == 0) {
+            if (more) {
+              mbar_arrive_expect_tx(&m->q_full[sl], C::kHalves * 128 * G * tp);
 #pragma unroll
-                for (int c = 0; c < C::kHalves; ++c)
-                  tc::tma_load_3d(smem + C::q + sl * C::kTileBytes + c * (kRows * 128), &tmap_q,
-                                  c * 64, s.h * G, tok0, &m->q_full[sl], policy_evict_normal());
-              } else {
-                mbar_arrive(&m->q_full[sl]);
-              }
+              for (int c = 0; c < C::kHalves; ++c)
+                tc::tma_load_3d(smem + C::q + sl * C::kTileBytes + c * (kRows * 128), &tmap_q,
+                                c * 64, s.h * G, tok0, &m->q_full[sl], policy_evict_normal());
+            } else {
+              mbar_arrive(&m->q_full[sl]);
             }
-          } else {
-            // to fp16 with each row's largest value brought to 2^14: exact but for
-            // values 2^-28 below it. D / 8 neighbouring lanes hold a row.
-            const int nrow = more ? min(tp, s.t1 - s.t0 - f * tp) * G : 0;
-            unsigned char* q_s = smem + C::q + sl * C::kTileBytes;
-            const uint16_t* src = static_cast<const uint16_t*>(P.q);
-            const uint32_t flip = P.scale < 0.f ? 0x80008000u : 0u;
-            constexpr int kBatch = 4;
-            const int total = nrow * (D / 8);
-            for (int i0 = lane; i0 < total; i0 += 32 * kBatch) {
-              uint4 x[kBatch];
-#pragma unroll
-              for (int e = 0; e < kBatch; ++e) {
-                const int i = i0 + 32 * e, rr = i / (D / 8), c = i % (D / 8);
-                const int tk = rr / G, g = rr - tk * G;
-                if (i < total)
-                  x[e] = __ldg(reinterpret_cast<const uint4*>(
-                      src + static_cast<int64_t>(tok0 + tk) * P.q_stride +
-                      static_cast<int64_t>(s.h * G + g) * D + c * 8));
-              }
-#pragma unroll
-              for (int e = 0; e < kBatch; ++e) {
-                const int i = i0 + 32 * e, rr = i / (D / 8), c = i % (D / 8);
-                if (i >= total) break;
-                uint32_t xw[4] = {x[e].x ^ flip, x[e].y ^ flip, x[e].z ^ flip, x[e].w ^ flip};
-                float v[8];
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                  if (P.dtype == DSPARK_F16)
-                    unpack_f16(xw[y], v[2 * y], v[2 * y + 1]);
-                  else
-                    unpack_bf16(xw[y], v[2 * y], v[2 * y + 1]);
-                }
-                uint32_t big = 0;
-#pragma unroll
-                for (int y = 0; y < 8; ++y) big = max(big, __float_as_uint(v[y]) & 0x7FFFFFFFu);
-                const unsigned int who = ((1u << (D / 8)) - 1u) << (lane & ~(D / 8 - 1));
-#pragma unroll
-                for (int o = D / 16; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(who, big, o));
-                const int ex = big == 0u ? 14 : max(static_cast<int>(big >> 23) - 127, -112);
-                const float up = __uint_as_float(static_cast<uint32_t>(14 - ex + 127) << 23);
-#pragma unroll
-                for (int y = 0; y < 4; ++y) xw[y] = pack_f16(v[2 * y] * up, v[2 * y + 1] * up);
-                if (c == 0)
-                  row_scale[sl * kRows + rr] =
-                      __uint_as_float(static_cast<uint32_t>(ex - 14 + 127) << 23);
-                *reinterpret_cast<uint4*>(q_s + (c >> 3) * (kRows * 128) + rr * 128 +
-                                          (((c & 7) ^ (rr & 7)) << 4)) =
-                    make_uint4(xw[0], xw[1], xw[2], xw[3]);
-              }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&m->q_full[sl]);
           }
         }
         if (!more || !ok) break;
@@ -1211,9 +1199,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
       // The whole warp runs the loop, so that descriptors stay in uniform
       // registers; one elected lane issues.
       constexpr uint32_t id_pv = idesc_of(!kF16, true, D);
-      // (a negative scale is a negated A; the scout of an 8-bit cache sees to it)
-      const uint32_t id_qk = idesc_of(!kF16, false, kKeys) |
-                             (!kQuant && P.scale < 0.f ? 1u << 13 : 0u);
+      // (a negative scale is a negated A)
+      const uint32_t id_qk = idesc_of(!kF16, false, kKeys) | (P.scale < 0.f ? 1u << 13 : 0u);
       const bool leader = elect_one();
       const uint64_t q_desc = tc::sw128_kmajor_desc(smem_addr(smem + C::q));
       const uint64_t k_desc = tc::sw128_kmajor_desc(smem_addr(smem + C::kv));
@@ -1225,7 +1212,9 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         const Seg s = m->seg[n_q & 1];
         if (s.end) break;
         const uint32_t n_q1 = n_q + 1;
-        if (s.pair && !wait_warp(&m->q_full[n_q1 & 1], (n_q1 >> 1) & 1, fail, P.status)) break;
+        uint64_t* there = kQuant ? m->q_ready : m->q_full;
+        if (kQuant && !wait_warp(&there[n_q & 1], (n_q >> 1) & 1, fail, P.status)) break;
+        if (s.pair && !wait_warp(&there[n_q1 & 1], (n_q1 >> 1) & 1, fail, P.status)) break;
         tc::fence_after_thread_sync();
         const int nt = s.tiles(), ni = s.pair ? 2 * nt : nt;
         auto keys_of = [&](int i) { return base + s.k_place(s.j0 + (s.pair ? i >> 1 : i)); };
@@ -1560,7 +1549,7 @@ cudaError_t launch_paged_attention(PagedAttentionParams p, cudaStream_t stream) 
   if (!make_map(&mk, kv.k, kv, kv.k_block_stride, kv.k_head_stride, kv.k_token_stride) ||
       !make_map(&mv, kv.v, kv, kv.v_block_stride, kv.v_head_stride, kv.v_token_stride))
     return cudaErrorInvalidValue;
-  if (kv.dtype != DSPARK_E4M3 && !make_q_map(&mq, p)) return cudaErrorInvalidValue;
+  if (!make_q_map(&mq, p)) return cudaErrorInvalidValue;
   return kv.head_dim == 64 ? launch_dim<64>(p, mq, mk, mv, sms, stream)
                            : launch_dim<128>(p, mq, mk, mv, sms, stream);
 }
