@@ -365,6 +365,34 @@ CASES = [
 ]
 
 
+def _ragged(B, lo, hi, new, seed):
+    r = np.random.RandomState(seed)
+    news = [int(x) for x in r.randint(1, new + 1, B)]
+    return dict(lens=[n + int(x) for n, x in zip(news, r.randint(lo, hi + 1, B))], news=news)
+
+
+# more requests than CTAs, more than threads of a CTA, units that end anywhere in a
+# CTA's run, units of single and of two row tiles beside each other
+MANY = [
+    dict(**_ragged(40, 100, 3000, 9, 1), Hq=16, H=4, D=128, page=32),
+    dict(**_ragged(40, 100, 3000, 9, 2), Hq=24, H=4, D=64, page=16, cache="float8_e4m3fn"),
+    dict(**_ragged(60, 0, 2500, 3, 3), Hq=8, H=2, D=128, page=64, dtype="float16",
+         cache="float8_e4m3fn", fused=True),
+    dict(**_ragged(12, 0, 900, 700, 4), Hq=12, H=2, D=128, page=16, layout="tokens"),
+    dict(**_ragged(9, 0, 500, 600, 5), Hq=5, H=1, D=64, page=128, cache="float8_e4m3fn"),
+    dict(**_ragged(300, 0, 300, 2, 6), Hq=4, H=2, D=64, page=16),
+    dict(**_ragged(1024, 0, 60, 1, 7), Hq=2, H=1, D=64, page=16),
+    dict(**_ragged(500, 0, 1700, 1, 8), Hq=3, H=1, D=128, page=16, dtype="float16"),
+]
+
+
+@pytest.mark.parametrize("window", [0, 333])
+@pytest.mark.parametrize("case", range(len(MANY)))
+def test_attention_of_many_requests(case, window):
+    torch = require_gpu()
+    Attend(torch, seed=100 + case, **MANY[case]).check(True, window)
+
+
 @pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 37), (False, 130)])
 @pytest.mark.parametrize("case", range(len(CASES)))
 def test_attention_follows_the_definition(case, causal, window):

@@ -82,6 +82,7 @@ struct Cfg {
   static constexpr int kHalves = D / 64;
   static constexpr int kTileBytes = kHalves * kRows * 128;  // 128 x D in 16 bits
   static constexpr int kRawBytes = kKeys * D;               // 128 x D in 8 bits
+  // (3 + 3 stages beside an 8-bit cache: 4 + 2 took 302 us for 277, 3 + 4 280)
   static constexpr int kStages = kQuant ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 10);
   static constexpr int kRaw = kQuant ? (D == 128 ? 3 : 6) : 0;
   static constexpr int kThreads = kQuant ? 512 : 384;
@@ -94,8 +95,7 @@ struct Cfg {
   static constexpr int kv = q + 2 * kTileBytes;
   static constexpr int raw = kv + kStages * kTileBytes;
   static constexpr int misc = raw + kRaw * kRawBytes;
-  static constexpr int row_scale = misc + 2048;             // 8-bit cache: [2][kRows]
-  static constexpr int kBytes = row_scale + (kQuant ? 1024 : 0) + 1024;
+  static constexpr int kBytes = misc + 2048 + 1024;
   static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
 };
 
@@ -146,7 +146,12 @@ struct Misc {
   int start_h;
   long long start_rem, pos, end;
   unsigned long long warp_sum[17];
-  float2 x[kRows];  // joined unit: r, l of the second warpgroup, then f0, f1
+  union {
+    float2 x[kRows];  // joined unit: r, l of the second warpgroup, then f0, f1
+    // 8-bit cache: of the query rows in a slot; all read before the first items
+    // end, and so before x is written
+    float row_scale[2][kRows];
+  };
 };
 static_assert(sizeof(Misc) <= 2048, "Misc fits its place");
 
@@ -607,7 +612,6 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   Misc* m = reinterpret_cast<Misc*>(smem + C::misc);
-  float* row_scale = reinterpret_cast<float*>(smem + C::row_scale);
   volatile int* fail = &m->fail;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = P.Hq / P.kv.kv_heads;
@@ -724,7 +728,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         // by a power of two: exact but for values 2^-28 below it. D / 8
         // neighbouring lanes hold a row.
         const uint32_t mine = n_q + (s.pair ? w : 0);
-        float* scales = row_scale + (mine & 1) * kRows;
+        float* scales = m->row_scale[mine & 1];
         if (s.pair || w == 0) {
           unsigned char* q_s = smem + C::q + (mine & 1) * C::kTileBytes;
 #pragma unroll 2
