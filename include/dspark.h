@@ -1,6 +1,7 @@
 /*
- * dspark.h -- C ABI of the DSpark Markov drafting step and rejection-sampling
- * verifier for one NVIDIA GB300 (sm_103a).
+ * dspark.h -- C ABI of the DSpark Markov drafting step, the rejection-sampling
+ * verifier and the paged key/value cache of the verification pass for one
+ * NVIDIA GB300 (sm_103a).
  *
  * The operations follow these pages (cited by title and section):
  *   - "DSparkSpeculator" API page (vllm/v1/worker/gpu/spec_decode/dspark/
@@ -451,7 +452,7 @@ dspark_status dspark_kv_append(const void* k, const void* v, dspark_dtype dtype,
  *
  * Arguments
  *   q             [T, q_heads, head_dim] dtype, tokens q_stride elements apart
- *   out           [T, q_heads, head_dim] dtype, contiguous
+ *   out           [T, q_heads, head_dim] dtype, contiguous, apart from q
  *   lse           [T, q_heads] fp32, or NULL
  *   dtype         DSPARK_BF16 or DSPARK_F16, the cache's unless that is 8-bit
  *   block_table   [S, M] int32
@@ -460,8 +461,9 @@ dspark_status dspark_kv_append(const void* k, const void* v, dspark_dtype dtype,
  *   q_heads       a multiple of kv_heads, at most 128 * kv_heads
  *   causal 0 or 1; window >= 0, 0 = none; scale finite
  *   B in [0, 1024], S >= 1, M in [1, 2^20], T in [0, 2^24).
- *   workspace     at least dspark_paged_attention_workspace_bytes() bytes,
- *                 256-byte aligned, no initial contents required.
+ *   workspace     at least dspark_paged_attention_workspace_bytes() bytes
+ *                 (43 MB for head_dim 128, 22 MB for 64), 256-byte aligned, no
+ *                 initial contents required.
  * Alignment: q, out, the caches and all strides (in bytes): 16.
  * ------------------------------------------------------------------------ */
 size_t dspark_paged_attention_workspace_bytes(int B, int q_heads, int kv_heads,
