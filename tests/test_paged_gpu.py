@@ -393,6 +393,54 @@ def test_attention_of_many_requests(case, window):
     Attend(torch, seed=100 + case, **MANY[case]).check(True, window)
 
 
+# many short requests of several key heads, an odd number of heads, heads that end a
+# CTA's run, tables that can hold long requests (units may be cut) or cannot
+HEADS = [
+    dict(**_ragged(200, 0, 700, 1, 9), Hq=8, H=8, D=64, page=16, dtype="float16"),
+    dict(**_ragged(200, 0, 700, 1, 10), Hq=8, H=8, D=64, page=64, dtype="float16",
+         cache="float8_e4m3fn", fused=True),
+    dict(**_ragged(150, 0, 500, 8, 11), Hq=20, H=5, D=128, page=32),
+    dict(**_ragged(150, 0, 500, 8, 12), Hq=12, H=3, D=128, page=16, cache="float8_e4m3fn"),
+    dict(**_ragged(90, 300, 2600, 4, 13), Hq=35, H=7, D=128, page=16, dtype="float16"),
+    dict(**_ragged(90, 300, 2600, 4, 14), Hq=14, H=7, D=64, page=128, cache="float8_e4m3fn"),
+    # one token tile, two of them and prompts beside each other
+    dict(**_ragged(60, 0, 900, 90, 15), Hq=32, H=8, D=64, page=16),
+]
+
+
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 150)])
+@pytest.mark.parametrize("case", range(len(HEADS)))
+def test_attention_of_short_requests_and_many_heads(case, causal, window):
+    torch = require_gpu()
+    Attend(torch, seed=200 + case, **HEADS[case]).check(causal, window)
+
+
+@pytest.mark.parametrize("cache", [None, "float8_e4m3fn"])
+def test_a_value_that_one_head_does_not_see_stays_out_of_all(cache):
+    """A NaN in one key head's values, at the last token of every third request:
+    earlier rows of that head and all rows of the others keep their results."""
+    torch = require_gpu()
+    a = Attend(torch, seed=31, cache=cache, **_ragged(120, 0, 400, 6, 16), Hq=12, H=6, D=64,
+               page=16)
+    a.check()
+    clean = a.out.clone()
+    for b in range(0, a.B, 3):
+        last = a.lens[b] - 1
+        a.vc[int(a.table[a.slots[b], last // 16]), b % 6, last % 16, 11] = math.nan
+    a.call()
+    torch.cuda.synchronize()
+    for b in range(a.B):
+        rows, h = slice(a.starts[b], a.starts[b + 1]), b % 6
+        got, was = a.out[rows].clone(), clean[rows].clone()
+        if b % 3 == 0:
+            assert got[-1, 2 * h:2 * h + 2, 11].isnan().all()
+            got[-1, 2 * h:2 * h + 2, 11] = was[-1, 2 * h:2 * h + 2, 11]
+            # (that head's products may be summed in another order: compared below)
+            got[:, 2 * h:2 * h + 2] = was[:, 2 * h:2 * h + 2]
+        assert torch.equal(got, was)
+    a.compare()
+
+
 @pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 37), (False, 130)])
 @pytest.mark.parametrize("case", range(len(CASES)))
 def test_attention_follows_the_definition(case, causal, window):

@@ -18,8 +18,12 @@
 // work is two such row tiles of one request and key head ("pair": each of the
 // two softmax warpgroups owns a row tile, and every key tile is used twice), or
 // a single one ("single": the two warpgroups take key tiles in turn, and their
-// results are joined at the end). Either way the tensor core works on one
-// warpgroup's scores while the other's are being exponentiated.
+// results are joined at the end). Two single units of neighbouring key heads have
+// the same lengths and masks; where a run has both whole, they are done side by
+// side ("twin": a warpgroup each, nothing to join, one end for two units: 177
+// requests of one token over 279 keys, 8 heads of 64, fp16: 49 us for 64). In all
+// three the tensor core works on one warpgroup's scores while the other's are being
+// exponentiated.
 //
 // Split. Lengths live on the device and are ragged. Every CTA sums up the costs
 // of all units (key tiles and a constant) and takes a run of equal cost, so a long
@@ -55,7 +59,7 @@
 // cores; 4096 tokens over 12288: 1.21 ms, 1.58 PFLOP/s at full clocks, the tensor
 // pipe active 68%. An 8-bit cache: shared memory, through which a tile passes
 // three times (raw, converted, operands): about 1800 clocks a tile of K and V at
-// 128 bytes a clock, 1930 taken; 256 x 4 tokens over 2-6k, 32/4 heads: 278 us.
+// 128 bytes a clock, 1890 taken; 256 x 4 tokens over 2-6k, 32/4 heads: 272 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -122,21 +126,26 @@ struct Seg {
   int j0, j1;   // key tiles
   int c1;       // the last CTA that works on the unit
   bool pair, opens, closes;  // two row tiles; starts / ends with the unit
+  bool twin;    // the whole units of key heads h and h + 1
   bool end;     // no segment, the walk is over
   __device__ int tiles() const { return j1 - j0; }
+  __device__ bool two() const { return pair || twin; }  // a row tile each
   // items (key tiles) of warpgroup w and the k-th one's tile
-  __device__ int items(int w) const { return pair ? tiles() : (tiles() + 1 - w) / 2; }
-  __device__ int tile(int w, int k) const { return pair ? j0 + k : j0 + 2 * k + w; }
+  __device__ int items(int w) const { return two() ? tiles() : (tiles() + 1 - w) / 2; }
+  __device__ int tile(int w, int k) const { return two() ? j0 + k : j0 + 2 * k + w; }
+  // The tiles in the order of their loading (a twin's heads in turn): how many,
+  // which one is item k of warpgroup w, the i-th one's key tile and head.
+  __device__ int loads() const { return twin ? 2 * tiles() : tiles(); }
+  __device__ int load_of(int w, int k) const { return pair ? k : 2 * k + w; }
+  __device__ int load_tile(int i) const { return j0 + (twin ? i >> 1 : i); }
+  __device__ int load_head(int i) const { return twin ? h + (i & 1) : h; }
   __device__ int ahead() const { return pair ? 1 : 2; }  // key tiles loaded before the first values
-  // place of a tile's keys / values in the order in which the segment loads them
-  __device__ int k_place(int j) const {
-    const int i = j - j0, a = ahead();
+  // place of the i-th tile's keys / values among all loads of the segment
+  __device__ int k_place(int i) const {
+    const int a = ahead();
     return i < a ? i : 2 * i - a + 1;
   }
-  __device__ int v_place(int j) const {
-    const int i = j - j0;
-    return i + min(tiles(), ahead() + i);
-  }
+  __device__ int v_place(int i) const { return i + min(loads(), ahead() + i); }
 };
 
 struct Misc {
@@ -506,6 +515,7 @@ struct Walk {
       s.j0 = jb + max(0, v - kUnitTiles);
       s.j1 = jb + max(0, v + take - kUnitTiles);
       const bool some = s.j1 > s.j0;
+      bool twin = false;
       if (some) {
         s.r = r;
         s.h = h;
@@ -516,9 +526,17 @@ struct Walk {
         s.closes = s.j1 == je;
         s.c1 = static_cast<int>((pos + left - 1) / per);
         s.end = false;
+        // the next unit is the next head's, of the same cost: all of it in this run?
+        twin = s.opens && s.closes && r.n <= tp && h + 1 < P.kv.kv_heads &&
+               (P.whole ? pos + left < end : pos + left + cost() <= end);
+        s.twin = twin;
       }
       pos += take;
       v += take;
+      if (twin) {
+        pos += cost();
+        ++h;
+      }
       if (take == left) advance();
       if (some) return true;
     }
@@ -694,10 +712,11 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     bool ok = true;
     for (;;) {
       if (!(ok = wait_warp(&m->q_full[n_q & 1], (n_q >> 1) & 1, fail, P.status))) break;
-      const Seg s = m->seg[n_q & 1];
+      Seg s = m->seg[n_q & 1];
       if (s.end) break;
       const uint32_t n_q1 = n_q + 1;
-      if (s.pair && !(ok = wait_warp(&m->q_full[n_q1 & 1], (n_q1 >> 1) & 1, fail, P.status))) break;
+      if (s.two() && !(ok = wait_warp(&m->q_full[n_q1 & 1], (n_q1 >> 1) & 1, fail, P.status))) break;
+      if (s.twin) s.h += w;  // this warpgroup's head
       float sl = sl0 * (P.kv.k_scale ? P.kv.k_scale[s.h] : 1.f);
       const int items = s.items(w);
       // one thread of the warpgroup gives back what its MMAs have read: a tile
@@ -708,7 +727,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
       auto give_queries = [&]() {
         if (lane == 0) {
           mbar_arrive(&m->q_empty[n_q & 1]);
-          if (s.pair) mbar_arrive(&m->q_empty[n_q1 & 1]);
+          if (s.two()) mbar_arrive(&m->q_empty[n_q1 & 1]);
         }
       };
       if (items == 0) {
@@ -738,11 +757,12 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         // The row tile to fp16, in place, each row's largest value brought to 2^14
         // by a power of two: exact but for values 2^-28 below it. D / 8
         // neighbouring lanes hold a row.
-        const uint32_t mine = n_q + (s.pair ? w : 0);
+        const uint32_t mine = n_q + (s.two() ? w : 0);
         float* scales = m->row_scale[mine & 1];
-        if (s.pair || w == 0) {
+        if (s.two() || w == 0) {
           unsigned char* q_s = smem + C::q + (mine & 1) * C::kTileBytes;
-#pragma unroll 2
+          // (two rounds at once spill: 276 us for 272 with 256 x 4 tokens over 2-6k)
+#pragma unroll 1
           for (int i = row; i < nrow * (D / 8); i += kRows) {
             const int rr = i / (D / 8), c = i % (D / 8);
             uint4* at = reinterpret_cast<uint4*>(q_s + (c >> 3) * (kRows * 128) + rr * 128 +
@@ -783,8 +803,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         if (!(ok = wait_warp(&m->s_full[w], n_item & 1, fail, P.status))) break;
         tc::fence_after_thread_sync();
         if (giver) {  // these scores are there: the keys, and the values before
-          give_tile(base + s.k_place(s.tile(w, k)));
-          if (!kQuant && k > 0) give_tile(base + s.v_place(s.tile(w, k - 1)));
+          give_tile(base + s.k_place(s.load_of(w, k)));
+          if (!kQuant && k > 0) give_tile(base + s.v_place(s.load_of(w, k - 1)));
         }
         if (k == items - 1) give_queries();
         __syncwarp();
@@ -882,7 +902,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         if (tail || scan) {
           // the tile's values: rows past the end become zero; a non-finite one
           // that some row does not see takes P V off the tensor core
-          const uint32_t vi = base + s.v_place(s.tile(w, k));
+          const uint32_t vi = base + s.v_place(s.load_of(w, k));
           unsigned char* v_s = smem + C::kv + (vi % C::kStages) * C::kTileBytes;
           if (!(ok = wait_tile<C::kStages>(m, vi, P.status))) break;
           const int key = key0 + row;
@@ -975,15 +995,15 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         if (!(ok = wait_warp(&m->o_full[w], n_seg & 1, fail, P.status))) break;
         tc::fence_after_thread_sync();
         ++n_seg;
-        if (!kQuant && giver) give_tile(base + s.v_place(s.tile(w, items - 1)));
+        if (!kQuant && giver) give_tile(base + s.v_place(s.load_of(w, items - 1)));
       }
-      base += 2 * s.tiles();
-      n_q += s.pair ? 2 : 1;
+      base += 2 * s.loads();
+      n_q += s.two() ? 2 : 1;
       // ---- the segment's result -----------------------------------------------------
       // A joined segment's is f0 O_0 + f1 O_1: the first warpgroup works out the
       // factors, and each writes half of the columns.
-      const bool joined = !s.pair && s.items(1) > 0;
-      if (!s.pair && w == 1 && !joined) continue;
+      const bool joined = !s.two() && s.items(1) > 0;
+      if (!s.two() && w == 1 && !joined) continue;
       float f0 = 1.f, f1 = 0.f;
       if (joined && w == 1) {
         m->x[row] = make_float2(r, l);
@@ -1148,7 +1168,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
           report(P.status, DSPARK_ERR_BOUNDS);
           return P.kv.num_blocks;
         };
-        auto load = [&](const CUtensorMap* map, int j, int id, int place) -> bool {
+        auto load = [&](const CUtensorMap* map, int i, int id, int place) -> bool {
           const uint32_t n = base + place, st = n % kRing, ph = (n / kRing) & 1;
           if (!wait_warp(&empty[st], ph ^ 1, fail, P.status)) return false;
           if (lane == 0) {
@@ -1160,20 +1180,21 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
           }
           __syncwarp();
           if (bi < nb) {
-            const int y = (j * kKeys + bk) & (page - 1);
+            const int y = (s.load_tile(i) * kKeys + bk) & (page - 1);
             unsigned char* dst = ring + st * kBytes + bk * (kQuant ? D : 128);
-            tma_load_4d(dst + bc * (kKeys * 128), map, bc * 64, y, s.h, id, &full[st], pol);
+            tma_load_4d(dst + bc * (kKeys * 128), map, bc * 64, y, s.load_head(i), id, &full[st],
+                        pol);
           }
           return true;
         };
         // the pages of a tile are looked up a tile before it is due
-        const int nt = s.tiles(), a = s.ahead();  // keys `a` tiles ahead of the values
+        const int nt = s.loads(), a = s.ahead();  // keys `a` tiles ahead of the values
         int id_next = page_of(s.j0), id_v0 = 0, id_v1 = 0;  // of the tiles one and two before
         for (int i = 0; i < nt + a && ok; ++i) {
-          const int j = s.j0 + i, id_k = id_next;
-          if (i + 1 < nt) id_next = page_of(j + 1);
-          if (i >= a) ok = load(&tmap_v, j - a, a == 2 ? id_v1 : id_v0, s.v_place(j - a));
-          if (ok && i < nt) ok = load(&tmap_k, j, id_k, s.k_place(j));
+          const int id_k = id_next;
+          if (i + 1 < nt) id_next = page_of(s.load_tile(i + 1));
+          if (i >= a) ok = load(&tmap_v, i - a, a == 2 ? id_v1 : id_v0, s.v_place(i - a));
+          if (ok && i < nt) ok = load(&tmap_k, i, id_k, s.k_place(i));
           id_v1 = id_v0;
           id_v0 = id_k;
         }
@@ -1189,19 +1210,20 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
       for (;;) {
         const bool more = walk.next(s);
         s.end = !more;
-        const int fills = more && s.pair ? 2 : 1;
+        const int fills = more && s.two() ? 2 : 1;
         for (int f = 0; f < fills && ok; ++f, ++n_q) {
           const uint32_t sl = n_q & 1;
           if (!(ok = wait_warp(&m->q_empty[sl], ((n_q >> 1) & 1) ^ 1, fail, P.status))) break;
           if (f == 0 && lane == 0) m->seg[sl] = s;
-          const int tok0 = s.r.q0 + s.t0 + f * tp;
+          const int tok0 = s.r.q0 + s.t0 + (s.pair ? f * tp : 0);
+          const int head = s.h + (s.twin ? f : 0);
           if (lane == 0) {
             if (more) {
               mbar_arrive_expect_tx(&m->q_full[sl], C::kHalves * 128 * G * tp);
 #pragma unroll
               for (int c = 0; c < C::kHalves; ++c)
                 tc::tma_load_3d(smem + C::q + sl * C::kTileBytes + c * (kRows * 128), &tmap_q,
-                                c * 64, s.h * G, tok0, &m->q_full[sl], policy_evict_normal());
+                                c * 64, head * G, tok0, &m->q_full[sl], policy_evict_normal());
             } else {
               mbar_arrive(&m->q_full[sl]);
             }
@@ -1229,13 +1251,13 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         const uint32_t n_q1 = n_q + 1;
         uint64_t* there = kQuant ? m->q_ready : m->q_full;
         if (kQuant && !wait_warp(&there[n_q & 1], (n_q >> 1) & 1, fail, P.status)) break;
-        if (s.pair && !wait_warp(&there[n_q1 & 1], (n_q1 >> 1) & 1, fail, P.status)) break;
+        if (s.two() && !wait_warp(&there[n_q1 & 1], (n_q1 >> 1) & 1, fail, P.status)) break;
         tc::fence_after_thread_sync();
-        const int nt = s.tiles(), ni = s.pair ? 2 * nt : nt;
-        auto keys_of = [&](int i) { return base + s.k_place(s.j0 + (s.pair ? i >> 1 : i)); };
+        const int nt = s.loads(), ni = s.pair ? 2 * nt : nt;
+        auto keys_of = [&](int i) { return base + s.k_place(s.pair ? i >> 1 : i); };
         auto scores = [&](int i, uint32_t ki) {  // S_w = Q K^T of item i
           const int w = i & 1;
-          const uint32_t sl = (n_q + (s.pair ? w : 0)) & 1;
+          const uint32_t sl = (n_q + (s.two() ? w : 0)) & 1;
           const uint64_t qd = q_desc + static_cast<uint32_t>((sl * C::kTileBytes) >> 4);
           const uint64_t kd =
               k_desc + static_cast<uint32_t>(((ki % C::kStages) * C::kTileBytes) >> 4);
@@ -1257,7 +1279,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         }
         for (int i = 0; i < ni && ok; ++i) {  // O_w += P_w V of item i, S_w of item i + 2
           const int w = i & 1;
-          const uint32_t vi = base + s.v_place(s.j0 + (s.pair ? i >> 1 : i));
+          const uint32_t vi = base + s.v_place(s.pair ? i >> 1 : i);
           const uint32_t n = w ? n_item1 : n_item0;
           const bool more = i + 2 < ni;
           const uint32_t ki = keys_of(more ? i + 2 : i);
@@ -1299,7 +1321,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
           n_item1 += w == 1;
         }
         base += 2 * nt;
-        n_q += s.pair ? 2 : 1;
+        n_q += s.two() ? 2 : 1;
       }
       if (leader) {
         tc::mma_commit(&m->drain);
