@@ -415,6 +415,20 @@ def test_attention_of_short_requests_and_many_heads(case, causal, window):
     Attend(torch, seed=200 + case, **HEADS[case]).check(causal, window)
 
 
+@pytest.mark.parametrize("table", [40, 4000])
+@pytest.mark.parametrize("B,ctx,new,H", [(28, 900, 32, 4), (28, 1900, 16, 4), (3, 500, 300, 2),
+                                         (1, 2, 700, 2), (150, 1500, 4, 4), (14, 2500, 8, 4)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 205)])
+def test_attention_whether_units_are_split_or_not(B, ctx, new, H, causal, window, table):
+    """Equal requests, for which units are kept whole or cut by how they fill the
+    SMs, under tables that can hold short or long requests."""
+    torch = require_gpu()
+    a = Attend(torch, [ctx + new] * B, [new] * B, Hq=2 * H, H=H, D=64, page=64, seed=B)
+    if table * 64 > ctx + new:
+        a.dev[0] = torch.nn.functional.pad(a.dev[0], (0, table - a.dev[0].shape[1]), value=-1)
+    a.check(causal, window)
+
+
 @pytest.mark.parametrize("cache", [None, "float8_e4m3fn"])
 def test_a_value_that_one_head_does_not_see_stays_out_of_all(cache):
     """A NaN in one key head's values, at the last token of every third request:

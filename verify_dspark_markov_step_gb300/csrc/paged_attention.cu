@@ -29,8 +29,9 @@
 // of all units (key tiles and a constant) and takes a run of equal cost, so a long
 // request is spread over many CTAs and short ones share a CTA, without the host
 // and without atomics. A unit that a run's ends cut is written as partial
-// (O, r, l) per CTA and joined by paged_join_kernel in a fixed order; where the
-// table can only hold short requests, units stay whole and nothing is joined.
+// (O, r, l) per CTA and joined by paged_join_kernel in a fixed order; where even
+// runs gain less than that costs, a CTA takes the units that start in its run to
+// their ends and nothing is joined.
 //
 // Warps: 0-3 and 4-7 softmax (thread = row = lane of tensor memory), 9 issues
 // the MMAs (the warpgroups' in turn, which keeps one's softmax beside the other's
@@ -59,7 +60,7 @@
 // cores; 4096 tokens over 12288: 1.21 ms, 1.58 PFLOP/s at full clocks, the tensor
 // pipe active 68%. An 8-bit cache: shared memory, through which a tile passes
 // three times (raw, converted, operands): about 1800 clocks a tile of K and V at
-// 128 bytes a clock, 1890 taken; 256 x 4 tokens over 2-6k, 32/4 heads: 272 us.
+// 128 bytes a clock, 1870 taken; 256 x 4 tokens over 2-6k, 32/4 heads: 268 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -82,11 +83,22 @@ constexpr int kMinTiles = 2;  // key tiles a CTA takes at least
 // What a unit costs besides its key tiles, in tiles (its query rows, the first
 // scores, masks and the result overlap with little): the runs are of equal cost.
 constexpr int kUnitTiles = 3;
-// Units of at most this many key tiles are not split over CTAs: each part costs a
-// CTA a segment, and the launch that joins them 4 to 9 us (32 requests x 8 tokens
-// over 1400: 41 us whole, 50 split; one token over 600: 13 and 17). With units for
-// few of the SMs long ones gain more from more SMs (one token over 1400: 20 and 18).
+// Where the table can only hold units of at most this many key tiles, none is split
+// over CTAs and the join is not launched: each part costs a CTA a segment, and the
+// join 4 to 12 us (32 requests x 8 tokens over 1400: 41 us whole, 50 split; one
+// token over 600: 13 and 17). With units for few of the SMs long ones gain more from
+// more SMs (one token over 1400: 20 and 18).
 constexpr int kWholeTiles = 12, kWholeTilesFewUnits = 8;
+// Else the plan decides by the lengths: units stay whole where the longest run of
+// whole units is at most this many tiles longer than an even split's (8, and 2 for
+// each unit an SM up to two: with more units a CTA has more parts). Measured, split
+// and whole, units of 256 rows, bf16, heads of 128: 112 units of 8 tiles 40.0 and
+// 22.5 us, of 24 tiles 64.3 and 48.7; 56 of 12 tiles 30.3 and 27.8, of 24 tiles
+// 41.2 and 46.4; 8 of 8 tiles 19.3 and 20.8; 480 of 12 tiles 106 and 104, of 24
+// tiles 170 and 178. Units of 8 rows, fp16 heads of 64 and an 8-bit cache change
+// sides within two tiles of these.
+constexpr int kSplitGain = 8, kSplitGainUnits = 2;
+constexpr int kMaxRun = 0x3FFFFFFF;
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kGrow = 8.0f;  // the reference moves when the maximum passes it by 2^8
@@ -124,7 +136,7 @@ struct Seg {
   int h;
   int t0, t1;   // tokens of the unit within the request
   int j0, j1;   // key tiles
-  int c1;       // the last CTA that works on the unit
+  int after;    // CTAs after this one that work on the unit
   bool pair, opens, closes;  // two row tiles; starts / ends with the unit
   bool twin;    // the whole units of key heads h and h + 1
   bool end;     // no segment, the walk is over
@@ -161,11 +173,14 @@ struct Misc {
   uint32_t filling;  // tiles of the MMA's ring whose stage is being filled, or was
   int bad[2];      // the last tile whose values were found non-finite, per warpgroup
   int skip_pv[2];  // the last item whose P V the warpgroup did itself
-  int start_b, per;
+  int start_b;
+  int per;         // places of a run
+  int end, limit;  // as in Walk
   Request start_r;
   int start_h;
-  long long start_rem, pos, end;
+  long long start_rem;
   unsigned long long warp_sum[16];
+  unsigned int warp_units[16], warp_lo[16], warp_hi[16];  // units, their least and largest cost
   union {
     float2 x[kRows];  // joined unit: r, l of the second warpgroup, then f0, f1
     // 8-bit cache: of the query rows in a slot; all read before the first items
@@ -468,15 +483,18 @@ __device__ __forceinline__ void unit_tiles(const PagedAttentionParams& P, const 
   je = max(jb + 1, (hi + kKeys - 1) / kKeys);
 }
 
-// The segments of this CTA in order. Positions count the units' costs: the
-// first kUnitTiles places of a unit stand for no tile.
+// The segments of this CTA in order. Positions count the units' costs from the
+// run's start: the first kUnitTiles places of a unit stand for no tile. Units that
+// start before `end` are this CTA's, up to `limit`.
 struct Walk {
   const PagedAttentionParams& P;
-  int tp, b, h, u, jb, je, v, per;  // v: place within the unit
-  long long pos, end;
+  int tp, b, h, u, jb, je;
+  int v;  // place within the unit
+  int pos, end, limit, per;
   Request r;
   __device__ Walk(const PagedAttentionParams& P_, const Misc* m, int tp_)
-      : P(P_), tp(tp_), b(m->start_b), h(0), u(0), per(m->per), pos(m->pos), end(m->end) {
+      : P(P_), tp(tp_), b(m->start_b), h(0), u(0), pos(0), end(m->end), limit(m->limit),
+        per(m->per) {
     if (pos >= end) return;
     r = m->start_r;
     h = m->start_h;
@@ -487,7 +505,7 @@ struct Walk {
       rem -= cost();
     }
     v = static_cast<int>(rem);
-    if (P.whole && v != 0) {  // the CTA before takes the unit to its end
+    if (limit > end && v != 0) {  // the CTA before takes the unit to its end
       pos += cost() - v;
       advance();
     }
@@ -511,11 +529,11 @@ struct Walk {
   __device__ bool next(Seg& s) {
     while (pos < end) {
       const int left = cost() - v;
-      const int take = P.whole ? left : static_cast<int>(min(static_cast<long long>(left), end - pos));
+      const int take = min(left, limit - pos);
       s.j0 = jb + max(0, v - kUnitTiles);
       s.j1 = jb + max(0, v + take - kUnitTiles);
       const bool some = s.j1 > s.j0;
-      bool twin = false;
+      s.twin = false;
       if (some) {
         s.r = r;
         s.h = h;
@@ -524,16 +542,15 @@ struct Walk {
         s.pair = s.t1 - s.t0 > tp;
         s.opens = s.j0 == jb;
         s.closes = s.j1 == je;
-        s.c1 = static_cast<int>((pos + left - 1) / per);
+        s.after = static_cast<unsigned int>(pos + left - 1) / static_cast<unsigned int>(per);
         s.end = false;
         // the next unit is the next head's, of the same cost: all of it in this run?
-        twin = s.opens && s.closes && r.n <= tp && h + 1 < P.kv.kv_heads &&
-               (P.whole ? pos + left < end : pos + left + cost() <= end);
-        s.twin = twin;
+        s.twin = s.opens && s.closes && r.n <= tp && h + 1 < P.kv.kv_heads &&
+               pos + left < end && pos + left + cost() <= limit;
       }
       pos += take;
       v += take;
-      if (twin) {
+      if (s.twin) {
         pos += cost();
         ++h;
       }
@@ -551,6 +568,15 @@ __device__ void make_plan(const PagedAttentionParams& P, Misc* m, unsigned long 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int B = P.B;
   unsigned long long sum = 0;
+  unsigned int n_units = 0, least = 0xFFFFFFFFu, largest = 0;  // of units' costs
+  auto count = [&](const Request& o, int u) -> unsigned int {
+    int jb, je;
+    unit_tiles(P, o, tp, u, jb, je);
+    const unsigned int c = je - jb + kUnitTiles;
+    least = min(least, c);
+    largest = max(largest, c);
+    return c;
+  };
   // each thread takes `each` consecutive requests, so that a scan of the
   // threads' sums gives the prefix
   const int each = (B + kThreads - 1) / kThreads;
@@ -562,12 +588,9 @@ __device__ void make_plan(const PagedAttentionParams& P, Misc* m, unsigned long 
     const int units = (r.n + 2 * tp - 1) / (2 * tp);
     unsigned long long cost = 0;
     const bool big = units > 4;
+    n_units += min(units, 1 << 16);
     if (!big)
-      for (int u = 0; u < units; ++u) {
-        int jb, je;
-        unit_tiles(P, r, tp, u, jb, je);
-        cost += je - jb + kUnitTiles;
-      }
+      for (int u = 0; u < units; ++u) cost += count(r, u);
     unsigned int todo = __ballot_sync(0xFFFFFFFFu, big);
     while (todo) {
       const int src = __ffs(todo) - 1;
@@ -577,11 +600,7 @@ __device__ void make_plan(const PagedAttentionParams& P, Misc* m, unsigned long 
       o.len = __shfl_sync(0xFFFFFFFFu, r.len, src);
       const int ou = (o.n + 2 * tp - 1) / (2 * tp);
       unsigned long long c = 0;
-      for (int u = lane; u < ou; u += 32) {
-        int jb, je;
-        unit_tiles(P, o, tp, u, jb, je);
-        c += je - jb + kUnitTiles;
-      }
+      for (int u = lane; u < ou; u += 32) c += count(o, u);
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1) c += __shfl_xor_sync(0xFFFFFFFFu, c, s);
       if (lane == src) cost = c;
@@ -596,7 +615,15 @@ __device__ void make_plan(const PagedAttentionParams& P, Misc* m, unsigned long 
     const unsigned long long u = __shfl_up_sync(0xFFFFFFFFu, v, o);
     if (lane >= o) v += u;
   }
-  if (lane == 31) m->warp_sum[warp] = v;
+  n_units = __reduce_add_sync(0xFFFFFFFFu, n_units);
+  least = __reduce_min_sync(0xFFFFFFFFu, least);
+  largest = __reduce_max_sync(0xFFFFFFFFu, largest);
+  if (lane == 31) {
+    m->warp_sum[warp] = v;
+    m->warp_units[warp] = n_units;
+    m->warp_lo[warp] = least;
+    m->warp_hi[warp] = largest;
+  }
   __syncthreads();
   unsigned long long base = v - sum, total = 0;
   const int used = (B + 32 * each - 1) / (32 * each);  // warps that have requests
@@ -604,14 +631,37 @@ __device__ void make_plan(const PagedAttentionParams& P, Misc* m, unsigned long 
     if (w < warp) base += m->warp_sum[w];
     total += m->warp_sum[w];
   }
-  unsigned long long per = total >> 31 ? (total + gridDim.x - 1) / gridDim.x
-                                       : (static_cast<unsigned int>(total) + gridDim.x - 1) / gridDim.x;
-  if (per < kMinTiles) per = kMinTiles;
+  unsigned long long per =
+      total >> 31 ? (total + gridDim.x - 1) / gridDim.x
+                  : (static_cast<unsigned int>(total) + gridDim.x - 1) / gridDim.x;
+  per = min(max(per, static_cast<unsigned long long>(kMinTiles)),
+            static_cast<unsigned long long>(kMaxRun));
   const unsigned long long pos = per * blockIdx.x;
-  if (tid == 0) {
-    m->per = static_cast<int>(per > 0x7FFFFFFF ? 0x7FFFFFFF : per);
-    m->pos = static_cast<long long>(pos);
-    m->end = static_cast<long long>(pos + per < total ? pos + per : total);
+  if (tid == kThreads - 32) {  // (a warp that mostly has no request's start to find)
+    // a run of whole units starts at most ceil(per / least) of them, and ends less
+    // than one past its end
+    unsigned int units = 0;
+    least = 0xFFFFFFFFu, largest = 0;
+    for (int w = 0; w < used; ++w) {
+      units += m->warp_units[w];
+      least = min(least, m->warp_lo[w]);
+      largest = max(largest, m->warp_hi[w]);
+    }
+    units = min(units, 2 * gridDim.x) * P.kv.kv_heads;
+    units = min(units, 2 * gridDim.x);
+    // (32 bits: a run too long for them gains nothing from whole units)
+    const unsigned int run = static_cast<unsigned int>(per);
+    bool whole = P.whole;
+    if (per < 0x1000000u && largest < 0x1000000u) {
+      const unsigned long long most =
+          static_cast<unsigned long long>((run + least - 1) / least) * largest;
+      const unsigned int past =  // the longest run beyond an even one
+          most - run < largest ? static_cast<unsigned int>(most - run) : largest;
+      whole |= past * gridDim.x <= kSplitGain * gridDim.x + kSplitGainUnits * units;
+    }
+    m->per = static_cast<int>(per);
+    m->end = total <= pos ? 0 : static_cast<int>(min(per, total - pos));
+    m->limit = whole ? 0x7FFFFFFF : m->end;
   }
   for (int i = 0; i < each; ++i) {
     const int b = tid * each + i;
@@ -1121,7 +1171,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         tail_split = true;
         if (tid == 0) {
           JoinDesc d;
-          d.parts = s.c1 - static_cast<int>(blockIdx.x) + 1;
+          d.parts = s.after + 1;
           d.token0 = s.r.q0 + s.t0;
           d.tokens = s.t1 - s.t0;
           d.h = s.h;
@@ -1580,7 +1630,11 @@ cudaError_t launch_paged_attention(PagedAttentionParams p, cudaStream_t stream) 
   const dspark_paged_kv& kv = p.kv;
   // the most key tiles a unit can have
   int64_t keys = static_cast<int64_t>(p.M) << p.page_shift;
-  if (p.window > 0 && p.window + 2 * kRows < keys) keys = p.window + 2 * kRows;
+  if (p.window > 0) {
+    // (without a causal mask a unit sees from its first token's window to the end)
+    const int64_t tokens = p.causal ? 2 * (kRows / (p.Hq / kv.kv_heads)) : p.T;
+    keys = min(keys, p.window + tokens);
+  }
   p.whole = (keys + kKeys - 1) / kKeys + (p.window > 0 ? 1 : 0) <=
             (3 * p.B * kv.kv_heads >= sms ? kWholeTiles : kWholeTilesFewUnits);
   if (!make_map(&mk, kv.k, kv, kv.k_block_stride, kv.k_head_stride, kv.k_token_stride) ||
