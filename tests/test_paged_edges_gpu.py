@@ -1,0 +1,29 @@
+"""Edges of the paged attention and append on the GPU. Bounds are those of
+test_paged_gpu.py, whose ragged batches (``Attend``) these tests use."""
+import math
+
+import pytest
+
+import paged_oracle as po
+from gpu_util import require_gpu
+from test_paged_gpu import Attend, _half_eps, _ragged
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("D,dtype", [(64, "bfloat16"), (128, "float16")])
+def test_requests_of_one_key_tile_over_an_8_bit_cache(D, dtype):
+    """Units of one key tile, several to a CTA (of one key head: each alone), of
+    which a warpgroup has nothing to do, and longer ones between them: every call
+    of many in a row gives the definition's result, the same bits each time."""
+    torch = require_gpu()
+    for seed, case in enumerate((_ragged(1000, 0, 120, 1, 21), _ragged(700, 0, 300, 3, 22))):
+        a = Attend(torch, seed=seed, **case, Hq=4, H=1, D=D, page=16, dtype=dtype,
+                   cache="float8_e4m3fn")
+        a.check()
+        want, want_lse = a.out.clone(), a.lse.clone()
+        for _ in range(60):
+            a.call()
+        torch.cuda.synchronize()
+        assert a.status.item() == 0
+        assert torch.equal(a.out, want) and torch.equal(a.lse, want_lse)

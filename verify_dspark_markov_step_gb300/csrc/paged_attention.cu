@@ -844,8 +844,12 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
           __syncwarp();
           if (lane == 0) mbar_arrive(&m->q_ready[mine & 1]);
         }
-        if (!(ok = wait_warp(&m->q_ready[mine & 1], (mine >> 1) & 1, fail, P.status))) break;
-        sl *= scales[row];
+        // (A warpgroup without items has given the slot back: nothing keeps its next
+        // phases from passing, so it neither waits for the rows nor reads their scales.)
+        if (items > 0) {
+          if (!(ok = wait_warp(&m->q_ready[mine & 1], (mine >> 1) & 1, fail, P.status))) break;
+          sl *= scales[row];
+        }
       }
       float r = -INFINITY, l = 0.f;  // reference (scaled), sum
       for (int k = 0; k < items; ++k, ++n_item) {
