@@ -27,3 +27,16 @@ def test_requests_of_one_key_tile_over_an_8_bit_cache(D, dtype):
         torch.cuda.synchronize()
         assert a.status.item() == 0
         assert torch.equal(a.out, want) and torch.equal(a.lse, want_lse)
+
+
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 70), (False, 0)])
+@pytest.mark.parametrize("small", [2.0 ** -10, 2.0 ** -40])
+def test_a_zero_softmax_scale_over_an_8_bit_cache(small, causal, window):
+    """Every visible key weighs the same, whatever the size of the query rows,
+    the scales of the cache's heads and what is masked."""
+    torch = require_gpu()
+    a = Attend(torch, [400, 260, 0, 7], [5, 200, 0, 2], Hq=4, H=2, D=64, page=16, seed=8,
+               cache="float8_e4m3fn")
+    a.q.copy_((a.q.float() * small).to(a.q.dtype))
+    a.scale = 0.0
+    a.check(causal, window)

@@ -757,7 +757,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     uint32_t n_q = 0, n_seg = 0, n_item = 0, n_scan = 0, n_merge = 0;
     uint32_t base = 0;  // tiles loaded before this segment
     bool tail_split = false;
-    const float sl0 = fminf(fmaxf(fabsf(P.scale) * kLog2e, 1e-37f), 3e38f);
+    const float sl0 = fabsf(P.scale) * kLog2e;
     const int tok = row / G;  // token within the row tile
     bool ok = true;
     for (;;) {
@@ -848,9 +848,13 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         // phases from passing, so it neither waits for the rows nor reads their scales.)
         if (items > 0) {
           if (!(ok = wait_warp(&m->q_ready[mine & 1], (mine >> 1) & 1, fail, P.status))) break;
-          sl *= scales[row];
+          if (live) sl *= scales[row];
         }
       }
+      // A product with the scores of what is masked, which are -inf, has to stay
+      // -inf: not below the least positive number, whose products with finite
+      // scores are 2^-21 at most.
+      sl = fminf(fmaxf(sl, 0x1p-149f), 3e38f);
       float r = -INFINITY, l = 0.f;  // reference (scaled), sum
       for (int k = 0; k < items; ++k, ++n_item) {
         const int key0 = s.tile(w, k) * kKeys;
