@@ -349,8 +349,8 @@ dspark_status dspark_noise(const uint64_t* seed, const int64_t* pos,
 typedef struct {
   void* k;                  /* DEVICE memory, as every pointer below          */
   void* v;
-  const float* k_scale;     /* [kv_heads] or NULL (= 1): a stored value x     */
-  const float* v_scale;     /*   stands for x * scale[head]                   */
+  const float* k_scale;     /* [kv_heads] or NULL (= 1), finite: a stored     */
+  const float* v_scale;     /*   value x stands for x * scale[head]           */
   int64_t k_block_stride, k_head_stride, k_token_stride; /* elements */
   int64_t v_block_stride, v_head_stride, v_token_stride;
   dspark_dtype dtype;       /* DSPARK_BF16, DSPARK_F16 or DSPARK_E4M3         */

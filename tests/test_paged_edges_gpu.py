@@ -40,3 +40,19 @@ def test_a_zero_softmax_scale_over_an_8_bit_cache(small, causal, window):
     a.q.copy_((a.q.float() * small).to(a.q.dtype))
     a.scale = 0.0
     a.check(causal, window)
+
+
+@pytest.mark.parametrize("cache", [None, "float8_e4m3fn"])
+@pytest.mark.parametrize("H,D,news,lens", [
+    (5, 64, [1] * 40, list(range(90, 490, 10))),       # heads side by side
+    (5, 128, [3, 40, 1], [300, 90, 1300]),             # one row tile, cut units
+    (5, 128, [200, 333], [200, 700])])                 # two row tiles
+def test_scales_of_zero_and_below(cache, H, D, news, lens):
+    """A head's scale multiplies what the cache stores, of either sign or zero."""
+    torch = require_gpu()
+    a = Attend(torch, lens, news, Hq=2 * H, H=H, D=D, page=32, cache=cache, seed=11)
+    size = 0.01 if cache else 1.0
+    a.ks = size * torch.tensor([1.25, -1.5, 0.0, -0.75, 1.0], device="cuda")
+    a.vs = size * torch.tensor([-1.0, 1.5, 0.5, 0.0, -2.0], device="cuda")
+    a.check()
+    a.check(True, 100)

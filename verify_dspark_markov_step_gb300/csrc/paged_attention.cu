@@ -767,7 +767,10 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
       const uint32_t n_q1 = n_q + 1;
       if (s.two() && !(ok = wait_warp(&m->q_full[n_q1 & 1], (n_q1 >> 1) & 1, fail, P.status))) break;
       if (s.twin) s.h += w;  // this warpgroup's head
-      float sl = sl0 * (P.kv.k_scale ? P.kv.k_scale[s.h] : 1.f);
+      // (the scales' signs are the queries', here or in the product: a masked
+      // score is -inf and the largest score the largest exponent)
+      const float k_scale = P.kv.k_scale ? P.kv.k_scale[s.h] : 1.f;
+      float sl = sl0 * fabsf(k_scale);
       const int items = s.items(w);
       // one thread of the warpgroup gives back what its MMAs have read: a tile
       // once, or twice where the other warpgroup has no use for it
@@ -834,7 +837,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
 #pragma unroll
             for (int o = D / 16; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(who, big, o));
             const int ex = big == 0u ? 14 : max(static_cast<int>(big >> 23) - 127, -112);
-            const float up = __uint_as_float(static_cast<uint32_t>(14 - ex + 127) << 23);
+            const float up =
+                copysignf(__uint_as_float(static_cast<uint32_t>(14 - ex + 127) << 23), k_scale);
 #pragma unroll
             for (int y = 0; y < 4; ++y) xw[y] = pack_f16(v[2 * y] * up, v[2 * y + 1] * up);
             if (c == 0) scales[rr] = __uint_as_float(static_cast<uint32_t>(ex - 14 + 127) << 23);
@@ -1294,8 +1298,14 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
       // The whole warp runs the loop, so that descriptors stay in uniform
       // registers; one elected lane issues.
       constexpr uint32_t id_pv = idesc_of(!kF16, true, D);
-      // (a negative scale is a negated A)
+      // (a negative scale is a negated A; the rows beside an 8-bit cache come with
+      // their head's sign)
       const uint32_t id_qk = idesc_of(!kF16, false, kKeys) | (P.scale < 0.f ? 1u << 13 : 0u);
+      // (a vote, so that the descriptor stays in a uniform register)
+      auto id_of = [&](int h) {
+        const bool flip = !kQuant && P.kv.k_scale && P.kv.k_scale[h] < 0.f;
+        return id_qk ^ (__any_sync(0xFFFFFFFFu, flip) ? 1u << 13 : 0u);
+      };
       const bool leader = elect_one();
       const uint64_t q_desc = tc::sw128_kmajor_desc(smem_addr(smem + C::q));
       const uint64_t k_desc = tc::sw128_kmajor_desc(smem_addr(smem + C::kv));
@@ -1312,6 +1322,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         if (s.two() && !wait_warp(&there[n_q1 & 1], (n_q1 >> 1) & 1, fail, P.status)) break;
         tc::fence_after_thread_sync();
         const int nt = s.loads(), ni = s.pair ? 2 * nt : nt;
+        const uint32_t id0 = id_of(s.h), id1 = s.twin ? id_of(s.h + 1) : id0;
         auto keys_of = [&](int i) { return base + s.k_place(s.pair ? i >> 1 : i); };
         auto scores = [&](int i, uint32_t ki) {  // S_w = Q K^T of item i
           const int w = i & 1;
@@ -1322,7 +1333,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) {
             const uint32_t off = ((c >> 2) * (kRows * 128) + (c & 3) * 32) >> 4;
-            mma_ss(tmem + w * kKeys, qd + off, kd + off, id_qk, c != 0);
+            mma_ss(tmem + w * kKeys, qd + off, kd + off, w ? id1 : id0, c != 0);
           }
           tc::mma_commit(&m->s_full[w]);
         };
