@@ -56,3 +56,53 @@ def test_scales_of_zero_and_below(cache, H, D, news, lens):
     a.vs = size * torch.tensor([-1.0, 1.5, 0.5, 0.0, -2.0], device="cuda")
     a.check()
     a.check(True, 100)
+
+
+@pytest.mark.parametrize("dtype,cache", [("float16", None), ("float16", "float8_e4m3fn"),
+                                         ("bfloat16", "float8_e4m3fn"), ("bfloat16", None)])
+@pytest.mark.parametrize("lens,news", [([400, 700], [2, 5]), ([9000], [1]), ([300], [260])])
+def test_scores_whose_fp32_steps_are_large(dtype, cache, lens, news):
+    """Large queries and large keys, scores past 2^29: a key that fits a row takes
+    all of it, every row is an average of its values, nothing overflows."""
+    torch = require_gpu()
+    H, G, D, page = 2, 2, 128, 16
+    a = Attend(torch, lens, news, Hq=G * H, H=H, D=D, page=page, dtype=dtype, cache=cache, seed=12)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    a.q.copy_(torch.randn(a.q.shape, device="cuda", generator=g) * 8000)
+    if cache:
+        a.ks = torch.full((H,), 50.0, device="cuda")
+        fit = lambda row: 448.0 * row.sign()  # noqa: E731
+    else:
+        a.kc.copy_(torch.randn(a.kc.shape, device="cuda", generator=g) * 8000)
+        fit = lambda row: row  # noqa: E731
+    spots = {}  # (row, key head): the position of the key that fits the head's first query head
+    for b in range(a.B):
+        n, L, s = a.news[b], a.lens[b], a.slots[b]
+        for i in range(min(n, 40)):
+            for h in range(H):
+                at = (37 * i + 211 * h + 5) % (L - n)
+                t = a.starts[b] + i
+                spots[t, h] = (int(a.table[s, at // page]), at % page)
+    assert len(set((h, *p) for (t, h), p in spots.items())) == len(spots)
+    for (t, h), (block, off) in spots.items():
+        a.kc[block, h, off] = fit(a.q[t, h * G].float()).to(a.kc.dtype)
+    a.call()
+    torch.cuda.synchronize()
+    assert a.status.item() == 0
+    n = a.starts[-1]
+    out, lse, mass, slack = po.attention(a.q, a.kc, a.vc, a.table.tolist(), a.slots, a.starts,
+                                         a.lens, a.scale, True, 0, a.ks, a.vs)
+    assert slack[:n].max() > 2.0 ** 29
+    got = a.out[:n].double()
+    assert got.isfinite().all() and a.lse[:n].isfinite().all()
+    u_p = 2.0 ** -11 if dtype == "float16" or cache else 2.0 ** -8
+    u = _half_eps(torch, a.q.dtype)
+    top = max(a.vc[int(i), :, :min(page, a.lens[b] - j * page)].double().abs().max().item()
+              for b in range(a.B) for j, i in enumerate(a.table[a.slots[b]]) if j * page < a.lens[b])
+    top *= 1.0 if a.vs is None else a.vs.max().item()
+    assert (got.abs() <= top * (1 + u_p + 2 * u)).all()
+    for (t, h), (block, off) in spots.items():
+        v = a.vc[block, h, off].double() * (1.0 if a.vs is None else a.vs[h].double())
+        assert ((got[t, h * G] - v).abs() <= (u_p + u + 2.0 ** -20) * v.abs() + 2.0 ** -24).all()
+    e_x = 2 * (D + 8) * 2.0 ** -24 * slack[:n] + 2.0 ** -18
+    assert ((a.lse[:n].double() - lse[:n]).abs() <= e_x + lse[:n].abs() * 2.0 ** -22).all()

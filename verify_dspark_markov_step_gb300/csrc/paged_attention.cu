@@ -11,7 +11,10 @@
 // lives in tensor memory, is hardly ever touched by the softmax. Scores, l and
 // O are fp32; the p_j are rounded to the MMA's 16-bit type (bf16 keeps its
 // range; fp16 gets 2^7 on top, so that a p 2^-31 below the maximum is still
-// nonzero), which costs as much accuracy as the output's own rounding.
+// nonzero), which costs as much accuracy as the output's own rounding. x_j - r is
+// one FMA of the unscaled score and the rounded r; where r is so large that its
+// rounding shows, the row's reference is first taken off its scores, which is
+// exact near the maximum (p keeps its bound whatever the scores' size).
 //
 // Rows. The query heads of a key head read the same keys, so a tile's 128 rows
 // are (token, head of the group) pairs: floor(128 / group) tokens. A unit of
@@ -102,6 +105,12 @@ constexpr int kMaxRun = 0x3FFFFFFF;
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kGrow = 8.0f;  // the reference moves when the maximum passes it by 2^8
+// A reference beyond this (in powers of two) is taken off the scores before they
+// are scaled: a rounded 2^29 is off by enough to bring a p past fp16's range, or
+// to zero. Done where a maximum moves, beside the branch that every tile has for
+// that: a branch of its own in every tile took 1344 us for 1318 (4096 tokens over
+// 12288).
+constexpr float kFar = 1024.f;
 
 template <int D, bool kQuant>
 struct Cfg {
@@ -859,7 +868,9 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
       // -inf: not below the least positive number, whose products with finite
       // scores are 2^-21 at most.
       sl = fminf(fmaxf(sl, 0x1p-149f), 3e38f);
-      float r = -INFINITY, l = 0.f;  // reference (scaled), sum
+      float r = -INFINITY, l = 0.f;  // reference (a score, not scaled), sum
+      float neg = kOff;              // what is added to the scaled scores
+      bool any_far = false;          // a row of the warp has a reference beyond kFar
       for (int k = 0; k < items; ++k, ++n_item) {
         const int key0 = s.tile(w, k) * kKeys;
         if (!(ok = wait_warp(&m->s_full[w], n_item & 1, fail, P.status))) break;
@@ -911,26 +922,54 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
             }
             mx = fmaxf(mx, fmaxf(mx0, mx1));
           }
-          mx *= sl;
-          float keep = 1.f;
-          const bool move = mx > r + kGrow;  // also the first finite maximum
-          if (move) {
-            keep = ex2_approx(r - mx);  // 0 the first time
-            r = mx;
-          }
-          if (k > 0 && __any_sync(0xFFFFFFFFu, move)) {
-            l *= keep;
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              uint32_t o[32];
-              tmem_ld32(o_t + c, o);
-              tc::tmem_wait_ld();
+          const float grown = (mx - r) * sl;  // infinite the first time
+          const bool move = grown > kGrow;
+          if (any_far || __any_sync(0xFFFFFFFFu, move)) {
+            const float keep = move ? ex2_approx(-grown) : 1.f;
+            if (move) r = mx;
+            const bool far = live && r != -INFINITY && fabsf(r * sl) > kFar;
+            if (move) neg = far ? kOff : kOff - r * sl;
+            any_far = __any_sync(0xFFFFFFFFu, far);
+            if (any_far) {
+              const float off = far ? -r : 0.f;
+              const unsigned long long off2 = f2_pack(off, off);
+              auto take_off = [&](uint32_t* y, int n) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
-              tmem_st32(o_t + c, o);
+                for (int c = 0; c < n; c += 2) {
+                  float a, b;
+                  f2_unpack(f2_add(f2_pack(__uint_as_float(y[c]), __uint_as_float(y[c + 1])), off2),
+                            a, b);
+                  y[c] = __float_as_uint(a);
+                  y[c + 1] = __float_as_uint(b);
+                }
+              };
+              if constexpr (kCols == kKeys) {
+                take_off(x, kKeys);
+              } else {  // where they are read again (what is masked will be again)
+#pragma unroll 1
+                for (int c = 0; c < kKeys; c += 32) {
+                  uint32_t y[32];
+                  tmem_ld32(s_t + c, y);
+                  tc::tmem_wait_ld();
+                  take_off(y, 32);
+                  tmem_st32(s_t + c, y);
+                }
+                tmem_wait_st();
+              }
+            }
+            if (k > 0) {
+              l *= keep;
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(o_t + c, o);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+                tmem_st32(o_t + c, o);
+              }
             }
           }
-          const float neg = kOff - (r == -INFINITY ? 0.f : r);
           const unsigned long long sl2 = f2_pack(sl, sl), neg2 = f2_pack(neg, neg);
           unsigned long long sum = 0ull, sum1 = 0ull;
 #pragma unroll 1
@@ -1083,10 +1122,10 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
           if (!(ok = wait_warp(&m->merge[1], n_merge & 1, fail, P.status))) break;
           tc::fence_after_thread_sync();
           const float2 x1 = m->x[row];
-          const float rn = fmaxf(r, x1.x);
+          const float rn = fmaxf(r, x1.x);  // (scores of one row and head: the same scale)
           if (rn != -INFINITY) {
-            f0 = ex2_approx(r - rn);
-            keep1 = ex2_approx(x1.x - rn);
+            f0 = ex2_approx((r - rn) * sl);
+            keep1 = ex2_approx((x1.x - rn) * sl);
           }
           l = l * f0 + x1.y * keep1;
           r = rn;
@@ -1166,9 +1205,9 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         }
         if (live && !(joined && w == 1)) {
           if (split) {
-            reinterpret_cast<float2*>(wsp + ws.stats)[prow] = make_float2(r, l);
+            reinterpret_cast<float2*>(wsp + ws.stats)[prow] = make_float2(r * sl, l);
           } else if (P.lse) {
-            P.lse[trow] = l == 0.f ? -INFINITY : (r - kOff + lg2_approx(l)) * kLn2;
+            P.lse[trow] = l == 0.f ? -INFINITY : (r * sl - kOff + lg2_approx(l)) * kLn2;
           }
         }
       }
