@@ -414,9 +414,10 @@ dspark_status dspark_paged_tables(
  *
  * For every token t with slot_map[t] >= 0 and every head h:
  *   k_cache[slot / page_size, h, slot % page_size, :] = k[t, h, :]
- * and the same for v; in an 8-bit cache round(k / k_scale[h]) (IEEE division,
- * nearest even, clamped to +-448, NaN stays NaN). Tokens with a negative slot
- * are skipped; a slot past the cache is skipped and gives DSPARK_ERR_BOUNDS.
+ * and the same for v; in an 8-bit cache, or with scales, round(k / k_scale[h])
+ * (IEEE division in fp32, nearest even, in 8 bits clamped to +-448, NaN stays
+ * NaN). Tokens with a negative slot are skipped; a slot past the cache is
+ * skipped and gives DSPARK_ERR_BOUNDS.
  *
  * Arguments
  *   k, v          [T, kv_heads, head_dim] dtype, tokens k_stride / v_stride

@@ -106,3 +106,60 @@ def test_scores_whose_fp32_steps_are_large(dtype, cache, lens, news):
         assert ((got[t, h * G] - v).abs() <= (u_p + u + 2.0 ** -20) * v.abs() + 2.0 ** -24).all()
     e_x = 2 * (D + 8) * 2.0 ** -24 * slack[:n] + 2.0 ** -18
     assert ((a.lse[:n].double() - lse[:n]).abs() <= e_x + lse[:n].abs() * 2.0 ** -22).all()
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("both", [True, False])
+def test_append_divides_by_the_scales_of_a_16_bit_cache(dtype, both):
+    """round(x / scale) to the cache's type, and attention over such a cache sees
+    the rows that were appended."""
+    torch = require_gpu()
+    from verify_dspark_markov_step_gb300 import kv_append, paged_attention
+    dt = getattr(torch, dtype)
+    T, H, D, page = 300, 3, 64, 32
+    g = torch.Generator(device="cuda").manual_seed(6)
+    N = -(-T // page) + 1
+    k, v, q = (torch.randn(T, H, D, device="cuda", generator=g).to(dt) for _ in range(3))
+    kc, vc = (torch.full((N, H, page, D), 3.0, dtype=dt, device="cuda") for _ in range(2))
+    ks = torch.tensor([0.3, 7.0, -1.7], device="cuda")
+    vs = torch.tensor([1.9, 0.011, -3.0], device="cuda") if both else None
+    edge = torch.tensor([math.nan, math.inf, -math.inf, -0.0], device="cuda").to(dt)
+    last = k[T - 1, 1, :4].clone()
+    k[T - 1, 1, :4] = edge
+    slots = torch.arange(T, device="cuda") + page
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def append():
+        kv_append(k, v, kc, vc, slots, k_scale=ks, v_scale=vs, status=status)
+        torch.cuda.synchronize()
+        assert status.item() == 0
+    want = [po.append(x, c, slots, s) for x, c, s in ((k, kc, ks), (v, vc, vs))]
+    append()
+    u = _half_eps(torch, dt)
+    for got, w in zip((kc, vc), want):
+        got = got.double()
+        assert torch.equal(got.isnan(), w.isnan())
+        fin = w.isfinite()
+        assert torch.equal(got[~fin].nan_to_num(), w[~fin].nan_to_num())
+        # the quotient to fp32, then to 16 bits (fp16 below 2^-14: steps of 2^-24)
+        off = (got - w)[fin].abs()
+        assert (off <= w[fin].abs() * (u + 2.0 ** -23) + 2.0 ** -25).all()
+    if not both:
+        assert torch.equal(vc[1:].transpose(1, 2).reshape(-1, H, D)[:T], v)
+    k[T - 1, 1, :4] = last
+    append()
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    out = torch.empty_like(q)
+    paged_attention(q, kc, vc, i32([list(range(1, N))]), i32([0]), i32([0, T]), i32([T]), out,
+                    k_scale=ks, v_scale=vs, status=status)
+    torch.cuda.synchronize()
+    pages = [x.new_zeros(N, H, page, D) for x in (k, v)]
+    for c, x in zip(pages, (k, v)):  # the rows as they were given
+        c[1:] = torch.nn.functional.pad(x, (0, 0, 0, 0, 0, (N - 1) * page - T)) \
+            .view(N - 1, page, H, D).transpose(1, 2)
+    want, _, mass, slack = po.attention(q, *pages, [list(range(1, N))], [0], [0, T], [T], D ** -0.5)
+    # roundings of the keys move a score by u * slack, those of values, of
+    # probabilities and of the output what they are
+    e_x = (u + 2 * (D + 8) * 2.0 ** -24) * slack[..., None] + 2.0 ** -18
+    room = (2 * e_x * (1 + e_x) + 2 * u) * mass * (1 + u) + u * want.abs() + 2.0 ** -24
+    assert ((out.double() - want).abs() <= room).all()

@@ -5,7 +5,8 @@
 // tokens' side (which may be a view into a fused projection) and written into
 // the page, as it is or divided by the head's scale and rounded to 8 bits. The
 // quotient is the IEEE one, by products with the scale's reciprocal and a
-// correction: 8 divisions a piece would cost as much time as the memory.
+// correction: 8 divisions a piece would cost as much time as the memory. In a
+// 16-bit cache with scales, which is rare, it is by division.
 //
 // Bound by memory for long prompts (each value read once and written once; 16384
 // tokens of 8 heads of 128 in bf16: 20.6 us, 6.5 TB/s) and by instruction issue
@@ -97,8 +98,29 @@ __device__ __forceinline__ uint2 quantise(uint4 x, unsigned long long r2, unsign
   return make_uint2(y[0] | (y[1] << 16), y[2] | (y[3] << 16));
 }
 
+// The 8 values of a piece over the scale, rounded to fp32 and to their own type.
+template <bool kF16>
+__device__ __forceinline__ uint4 scaled16(uint4 x, float scale) {
+  uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    unpack<kF16>(w[i], a, b);
+    a = __fdiv_rn(a, scale);
+    b = __fdiv_rn(b, scale);
+    if constexpr (kF16)
+      asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(b), "f"(a));
+    else
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(b), "f"(a));
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// What becomes of a value: its bits, 8 bits of its quotient by the scale, 16.
+enum Form { kCopy, kTo8, kTo16 };
+
 // `width` threads share a token, `abreast` tokens are taken at a time.
-template <bool kQuantise, bool kF16, int kPer>
+template <Form kForm, bool kF16, int kPer>
 __global__ void __launch_bounds__(kThreads, 5)
 kv_append_kernel(KvAppendParams P, int width, int abreast) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -125,7 +147,7 @@ kv_append_kernel(KvAppendParams P, int width, int abreast) {
             src + static_cast<int64_t>(t0 + i * abreast) * P.src_stride[which]);
     const int64_t head = h * P.head_stride[which] + (c - h * cd) * 8;
     float scale = 1.f;
-    if (kQuantise && P.scale[which]) scale = P.scale[which][h];
+    if (kForm != kCopy && P.scale[which]) scale = P.scale[which][h];
     const bool slow = !temp_div_t_ok(scale);
     const float rcp = __frcp_rn(scale);
     const unsigned long long r2 = f2_pack(rcp, rcp), nt2 = f2_pack(-scale, -scale);
@@ -139,17 +161,18 @@ kv_append_kernel(KvAppendParams P, int width, int abreast) {
       const int block = static_cast<int>(slot[i] >> P.page_shift);
       const int off = static_cast<int>(slot[i]) & ((1 << P.page_shift) - 1);
       const int64_t at = block * P.block_stride[which] + off * P.token_stride[which] + head;
-      if constexpr (kQuantise) {
+      if constexpr (kForm == kTo8) {
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(P.dst[which]) + at) =
             quantise<kF16>(x[i], r2, nt2, scale, slow);
       } else {
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.dst[which]) + at) = x[i];
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.dst[which]) + at) =
+            kForm == kTo16 ? scaled16<kF16>(x[i], scale) : x[i];
       }
     }
   }
 }
 
-template <bool kQuantise, bool kF16, int kPer>
+template <Form kForm, bool kF16, int kPer>
 cudaError_t launch(const KvAppendParams& p, int width, int abreast, cudaStream_t stream) {
   const int per = abreast * kPer;
   // (may be set up while the kernel before it ends, and waits for it)
@@ -162,26 +185,29 @@ cudaError_t launch(const KvAppendParams& p, int width, int abreast, cudaStream_t
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_append_kernel<kQuantise, kF16, kPer>, p, width, abreast);
+  return cudaLaunchKernelEx(&cfg, kv_append_kernel<kForm, kF16, kPer>, p, width, abreast);
 }
 
-template <bool kQuantise, bool kF16>
+template <Form kForm, bool kF16>
 cudaError_t launch_per(const KvAppendParams& p, cudaStream_t stream) {
   const int pieces = 2 * (p.H * p.D / 8);
   const int width = pieces < kThreads ? pieces : kThreads;
   const int abreast = kThreads / width;
   // up to four CTAs an SM with a token a thread, kBatch tokens a thread beyond
   return p.T <= 152 * 4 * abreast
-             ? launch<kQuantise, kF16, 1>(p, width, abreast, stream)
-             : launch<kQuantise, kF16, kBatch>(p, width, abreast, stream);
+             ? launch<kForm, kF16, 1>(p, width, abreast, stream)
+             : launch<kForm, kF16, kBatch>(p, width, abreast, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t stream) {
-  if (p.cache_dtype != DSPARK_E4M3) return launch_per<false, false>(p, stream);
-  return p.dtype == DSPARK_F16 ? launch_per<true, true>(p, stream)
-                               : launch_per<true, false>(p, stream);
+  const bool f16 = p.dtype == DSPARK_F16;
+  if (p.cache_dtype == DSPARK_E4M3)
+    return f16 ? launch_per<kTo8, true>(p, stream) : launch_per<kTo8, false>(p, stream);
+  if (p.scale[0] || p.scale[1])
+    return f16 ? launch_per<kTo16, true>(p, stream) : launch_per<kTo16, false>(p, stream);
+  return launch_per<kCopy, false>(p, stream);
 }
 
 }  // namespace dspark
