@@ -120,36 +120,66 @@ class ToyTarget:
         return (x @ self.embed.T).float()
 
 
+def _laid_out(rows, used, query_start, max_tokens):
+    """The entries of rows [B, n] that are used (truth values [B, n]) at their requests'
+    places among the planned step's tokens [max_tokens]; 0 where no token is."""
+    i = torch.arange(rows.shape[1], device=rows.device)
+    at = torch.where(used, query_start[:-1, None].long() + i, max_tokens)
+    out = rows.new_zeros(max_tokens + 1)
+    out[at] = rows
+    return out[:-1]
+
+
 def speculative_loop(step, target: ToyTarget, cache: PagedCache, prompts, steps, draft_logits):
     """``steps`` speculative steps after the prompts (a list of token lists, one for each
     request of the DecodeStep ``step``). draft_logits(tokens) gives the drafter's base
     logits [B, K, V] from the anchors [B]. Returns the emitted tokens (prompt excluded)
-    of each request."""
+    of each request.
+
+    Padding requests (slot < 0) emit nothing, and neither does a request whose prompt the
+    tables refuse. A request that they refuse later (the status says so) emits nothing in
+    that step and is planned again in the next, as it was."""
     w = step.w
     B, K, V = w.B, w.K, w.V
     dev = step.device
+    prompts = [list(p) if s >= 0 else [] for p, s in zip(prompts, w.req_state_idx.tolist())]
+    if any(s >= 0 and not p for p, s in zip(prompts, w.req_state_idx.tolist())):
+        raise ValueError("a prompt must have a token at least")
+    longest = max(1, *(len(p) for p in prompts))
     lens = torch.tensor([len(p) for p in prompts], dtype=torch.int32, device=dev)
-    flat = torch.tensor([t for p in prompts for t in p], dtype=torch.int64, device=dev)
-    query_start, *_ = cache.plan(step.rsi, lens, flat.numel())
-    logits = target.forward(flat, cache)
+    rows = torch.tensor([p + [0] * (longest - len(p)) for p in prompts], dtype=torch.int64,
+                        device=dev)
+    total = max(1, sum(len(p) for p in prompts))
+    query_start, seq_lens, *_ = cache.plan(step.rsi, lens, total)
+    served = seq_lens > 0
+    used = served[:, None] & (torch.arange(longest, device=dev) < lens[:, None])
+    logits = target.forward(_laid_out(rows, used, query_start, total), cache)
     # the prompts are in the cache; their last logits choose the first anchors
-    cache.cached_lens.index_add_(0, step.rsi, lens)
-    anchor = logits[query_start[1:].long() - 1].argmax(1)
-    emitted = [anchor[:, None]]
+    cache.cached_lens.index_add_(0, step.rsi.clamp(min=0), torch.where(served, lens, 0))
+    rsi = torch.where(served, step.rsi, -1)
+    last = (query_start[1:].long() - 1).clamp(min=0)
+    anchor = torch.where(served, logits[last].argmax(1), 0)
+    emitted = [torch.where(served, anchor, -1)[:, None]]
     new = torch.full((B,), K + 1, dtype=torch.int32, device=dev)
-    accepted = None
+    accepted = torch.full((B,), -1, dtype=torch.int32, device=dev)  # not yet in cached_lens
+    i = torch.arange(K + 1, device=dev)
     for _ in range(steps):
         step.base.copy_(draft_logits(anchor))
         step.anchor.copy_(anchor)
-        query_start, seq_lens, positions, _ = cache.plan(step.rsi, new, B * (K + 1), accepted)
-        step.pos.copy_(positions[query_start[:-1].long()] + 1)  # of the first draft
+        query_start, seq_lens, *_ = cache.plan(rsi, new, B * (K + 1), accepted)
+        served = seq_lens > 0
+        step.pos.copy_((seq_lens - K).clamp(min=0))  # of the first draft
         step.markov()
-        tokens = torch.cat([anchor[:, None], step.draft.long()], 1).reshape(-1)
-        step.target.copy_(target.forward(tokens, cache).view(B, K + 1, V))
+        tokens = torch.cat([anchor[:, None], step.draft.long()], 1)
+        tokens = _laid_out(tokens, served[:, None].expand(-1, K + 1), query_start, B * (K + 1))
+        at = (query_start[:-1, None].long() + i).clamp(max=B * (K + 1) - 1)
+        step.target.copy_(target.forward(tokens, cache)[at])
         step.verify()
-        accepted = step.num_accepted
-        anchor = step.out.long().gather(1, accepted.long()[:, None])[:, 0]
-        emitted.append(step.out.long().clone())
+        accepted = torch.where(served, step.num_accepted, accepted)
+        out = step.out.long()
+        anchor = torch.where(served, out.gather(1, accepted.long().clamp(min=0)[:, None])[:, 0],
+                             anchor)
+        emitted.append(torch.where(served[:, None], out, -1))
     out = torch.cat(emitted, 1).tolist()
     return [[t for t in row if t >= 0] for row in out]
 
