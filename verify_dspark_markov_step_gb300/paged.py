@@ -19,7 +19,12 @@ class PagedCache:
     """Caches of ``layers`` layers for ``slots`` request slots of up to ``max_len``
     tokens, ``num_blocks`` blocks of ``page_size`` tokens shared by all slots (the same
     tables serve every layer). ``cache_dtype`` is the rows' dtype or float8_e4m3fn;
-    ``k_scale``/``v_scale`` [layers, kv_heads] belong to the latter."""
+    ``k_scale``/``v_scale`` [layers, kv_heads] are what its values stand for multiples of.
+
+    The calls run on ``stream``, or on torch's current stream. A step's plan, appends and
+    attentions share the tables and the plan's results: on several streams the caller
+    orders them. Each stream has an attention workspace of its own, so attentions of one
+    plan may run on different streams side by side."""
 
     def __init__(self, *, layers, slots, max_len, num_blocks, page_size, q_heads, kv_heads,
                  head_dim, dtype=torch.bfloat16, cache_dtype=None, k_scale=None, v_scale=None,
@@ -40,7 +45,7 @@ class PagedCache:
         self.status = ints((1,))
         self._dims = (q_heads, kv_heads, head_dim)
         self._made = {}
-        self._workspace = None
+        self._workspaces = {}  # by stream
 
     def plan(self, req_state_idx, new_lens, max_tokens, num_accepted=None, stream=None):
         """Block tables and slots of a step in which request b brings new_lens[b] tokens
@@ -51,11 +56,12 @@ class PagedCache:
         B = req_state_idx.shape[0]
         if (B, max_tokens) not in self._made:
             dev = self.pool.device
-            self._made[B, max_tokens] = (
-                torch.empty(B + 1, dtype=torch.int32, device=dev),
-                torch.empty(B, dtype=torch.int32, device=dev),
-                torch.empty(max_tokens, dtype=torch.int64, device=dev),
-                torch.empty(max_tokens, dtype=torch.int64, device=dev))
+            with torch.cuda.stream(stream):  # memory of the stream that uses it
+                self._made[B, max_tokens] = (
+                    torch.empty(B + 1, dtype=torch.int32, device=dev),
+                    torch.empty(B, dtype=torch.int32, device=dev),
+                    torch.empty(max_tokens, dtype=torch.int64, device=dev),
+                    torch.empty(max_tokens, dtype=torch.int64, device=dev))
         self.req_state_idx = req_state_idx
         self.step = self._made[B, max_tokens]
         _lib.paged_tables(req_state_idx, new_lens, self.cached_lens, self.block_table,
@@ -77,13 +83,15 @@ class PagedCache:
     def attend(self, layer, q, out, causal=True, window=0, scale=None, lse=None, stream=None):
         """The planned step's attention of q [max_tokens, q_heads, head_dim] over a
         layer's pages, into out."""
-        if self._workspace is None:
+        key = _lib._raw_stream(stream, self.pool)
+        if key not in self._workspaces:
             need = _lib.paged_attention_workspace_bytes(_lib.MAX_PAGED_BATCH, *self._dims)
-            self._workspace = _lib.workspace(need, self.pool.device)
+            with torch.cuda.stream(stream):
+                self._workspaces[key] = _lib.workspace(need, self.pool.device)
         _lib.paged_attention(q, self.k[layer], self.v[layer], self.block_table,
                              self.req_state_idx, self.step[0], self.step[1], out, scale=scale,
                              causal=causal, window=window, lse=lse,
-                             workspace_buf=self._workspace, status=self.status, stream=stream,
+                             workspace_buf=self._workspaces[key], status=self.status, stream=stream,
                              **self._scales(layer))
 
     def status_code(self) -> int:
@@ -107,17 +115,19 @@ class ToyTarget:
         self.proj = [w(width, width) for _ in range(layers)]
 
     def forward(self, tokens, cache: PagedCache, stream=None):
-        """Logits [T, V] (fp32) of the planned step's tokens [T]."""
+        """Logits [T, V] (fp32) of the planned step's tokens [T], all on ``stream`` (or the
+        current one), which has to come after whatever made the tokens."""
         Hq, H, D = self.heads
-        x = self.embed[tokens]
-        for layer, (wqkv, wo) in enumerate(zip(self.qkv, self.proj)):
-            qkv = x @ wqkv
-            q, k, v = qkv.split((Hq * D, H * D, H * D), 1)
-            cache.append(layer, k.unflatten(1, (H, D)), v.unflatten(1, (H, D)), stream=stream)
-            out = torch.zeros(x.shape[0], Hq, D, dtype=x.dtype, device=x.device)
-            cache.attend(layer, q.unflatten(1, (Hq, D)), out, stream=stream)
-            x = x + out.flatten(1) @ wo
-        return (x @ self.embed.T).float()
+        with torch.cuda.stream(stream):
+            x = self.embed[tokens]
+            for layer, (wqkv, wo) in enumerate(zip(self.qkv, self.proj)):
+                qkv = x @ wqkv
+                q, k, v = qkv.split((Hq * D, H * D, H * D), 1)
+                cache.append(layer, k.unflatten(1, (H, D)), v.unflatten(1, (H, D)), stream=stream)
+                out = torch.zeros(x.shape[0], Hq, D, dtype=x.dtype, device=x.device)
+                cache.attend(layer, q.unflatten(1, (Hq, D)), out, stream=stream)
+                x = x + out.flatten(1) @ wo
+            return (x @ self.embed.T).float()
 
 
 def _laid_out(rows, used, query_start, max_tokens):
