@@ -96,3 +96,22 @@ def test_a_workspace_belongs_to_the_stream_that_uses_it(rec):
     assert used[0] is used[4] and used[1] is used[3] and used[2] is used[5]
     assert len({id(w) for w in used}) == 3
     assert rec.made == [None, one, two]
+
+
+def test_plans_of_many_sizes_share_their_buffers(rec):
+    """Lengths of prompts vary without end: the plans' buffers stay within four times
+    the largest plan, and none is freed (a captured graph may still write to it)."""
+    cache = _cache()
+    rsi = torch.zeros(3, dtype=torch.int32)
+    kept, storages = [], {}
+    for T in [4096, 1, 7, *range(1000, 4000, 7), 0, 4096]:
+        for B in (1, 2, 3):
+            made = cache.plan(rsi[:B], rsi[:B], T)
+            assert [tuple(t.shape) for t in made] == [(B + 1,), (B,), (T,), (T,)]
+            assert [t.dtype for t in made] == [torch.int32] * 2 + [torch.int64] * 2
+            assert all(t.is_contiguous() for t in made) and made is cache.step
+            for t in made:
+                storages[t.untyped_storage().data_ptr()] = t.untyped_storage().nbytes()
+            kept.append(made)
+    assert sum(storages.values()) <= 4 * (2 * 8 * 4096) + 2 * 4 * 1025
+    assert all(a.data_ptr() == b.data_ptr() for a, b in zip(kept[2], kept[-1]))

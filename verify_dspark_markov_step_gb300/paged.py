@@ -44,31 +44,42 @@ class PagedCache:
         self.pool = torch.tensor([num_blocks, 0], dtype=torch.int32, device=device)
         self.status = ints((1,))
         self._dims = (q_heads, kv_heads, head_dim)
-        self._made = {}
+        self._made = {}  # buffers of plans, by the power of two that holds their tokens
+        self._last = None, None
         self._workspaces = {}  # by stream
 
     def plan(self, req_state_idx, new_lens, max_tokens, num_accepted=None, stream=None):
         """Block tables and slots of a step in which request b brings new_lens[b] tokens
         (at most max_tokens in all); with num_accepted the slots' lengths first grow by
         what the last step's verification kept. Returns (query_start, seq_lens,
-        positions, slot_map), which the next plan of as many requests and tokens
-        overwrites."""
-        B = req_state_idx.shape[0]
-        if (B, max_tokens) not in self._made:
-            dev = self.pool.device
-            with torch.cuda.stream(stream):  # memory of the stream that uses it
-                self._made[B, max_tokens] = (
-                    torch.empty(B + 1, dtype=torch.int32, device=dev),
-                    torch.empty(B, dtype=torch.int32, device=dev),
-                    torch.empty(max_tokens, dtype=torch.int64, device=dev),
-                    torch.empty(max_tokens, dtype=torch.int64, device=dev))
+        positions, slot_map), which later plans may overwrite."""
         self.req_state_idx = req_state_idx
-        self.step = self._made[B, max_tokens]
+        self.step = self._buffers(req_state_idx.shape[0], max_tokens, stream)
         _lib.paged_tables(req_state_idx, new_lens, self.cached_lens, self.block_table,
                           self.held_blocks, self.free_blocks, self.pool, *self.step,
                           self.page_size, num_accepted=num_accepted, status=self.status,
                           stream=stream)
         return self.step
+
+    def _buffers(self, B, T, stream):
+        """Views of a plan's buffers. Sizes that vary share them, and none is given back:
+        a captured plan goes on writing where it did."""
+        if self._last[0] == (B, T):
+            return self._last[1]
+        size = max(1024, 1 << max(0, T - 1).bit_length())
+        with torch.cuda.stream(stream):  # memory of the stream that uses it
+
+            def made(key, count, dtype):
+                if key not in self._made:
+                    self._made[key] = torch.empty(count, dtype=dtype, device=self.pool.device)
+                return self._made[key]
+            requests = made("requests", 2 * _lib.MAX_PAGED_BATCH + 1, torch.int32)
+            tokens = made(size, 2 * size, torch.int64)
+        most = _lib.MAX_PAGED_BATCH
+        views = (requests[:B + 1], requests[most + 1:most + 1 + B], tokens[:T],
+                 tokens[size:size + T])
+        self._last = (B, T), views
+        return views
 
     def _scales(self, layer):
         return {"k_scale": None if self.k_scale is None else self.k_scale[layer],
