@@ -111,7 +111,8 @@ class PagedCache:
 
 class ToyTarget:
     """A random transformer without feed-forward blocks: embedding, ``layers`` of
-    attention with a residual, and the embedding again as the output head."""
+    attention with a residual, and an output head ([V, width], the embedding again unless
+    another is set)."""
 
     def __init__(self, V, layers, q_heads, kv_heads, head_dim, dtype=torch.bfloat16, seed=0,
                  device="cuda"):
@@ -121,7 +122,7 @@ class ToyTarget:
         def w(*shape):
             return (torch.randn(*shape, device=device, generator=g) * shape[0] ** -0.5).to(dtype)
         self.heads = (q_heads, kv_heads, head_dim)
-        self.embed = torch.randn(V, width, device=device, generator=g).to(dtype)
+        self.embed = self.head = torch.randn(V, width, device=device, generator=g).to(dtype)
         self.qkv = [w(width, (q_heads + 2 * kv_heads) * head_dim) for _ in range(layers)]
         self.proj = [w(width, width) for _ in range(layers)]
 
@@ -138,7 +139,7 @@ class ToyTarget:
                 out = torch.zeros(x.shape[0], Hq, D, dtype=x.dtype, device=x.device)
                 cache.attend(layer, q.unflatten(1, (Hq, D)), out, stream=stream)
                 x = x + out.flatten(1) @ wo
-            return (x @ self.embed.T).float()
+            return (x @ self.head.T).float()
 
 
 def _laid_out(rows, used, query_start, max_tokens):
