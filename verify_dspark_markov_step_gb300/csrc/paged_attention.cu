@@ -107,9 +107,8 @@ constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kGrow = 8.0f;  // the reference moves when the maximum passes it by 2^8
 // A reference beyond this (in powers of two) is taken off the scores before they
 // are scaled: a rounded 2^29 is off by enough to bring a p past fp16's range, or
-// to zero. Done where a maximum moves, beside the branch that every tile has for
-// that: a branch of its own in every tile took 1344 us for 1318 (4096 tokens over
-// 12288).
+// to zero. Done behind the branch that every tile has for a maximum that moves: one
+// of its own in every tile took 1344 us for 1311 (4096 tokens over 12288).
 constexpr float kFar = 1024.f;
 
 template <int D, bool kQuant>
@@ -690,8 +689,10 @@ __device__ void make_plan(const PagedAttentionParams& P, Misc* m, unsigned long 
 }
 
 // ---- the kernel ----------------------------------------------------------------------
-// kF16: the MMA's type is fp16 (fp16 rows, or an 8-bit cache), else bf16.
-template <int D, bool kF16, bool kQuant>
+// kF16: the MMA's type is fp16 (fp16 rows, or an 8-bit cache), else bf16. kScaled:
+// a 16-bit cache with key scales (apart, since the scale's sign in the issuer's
+// descriptor and its size in the softmax are 1 to 2% of a short request's time).
+template <int D, bool kF16, bool kQuant, bool kScaled>
 __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
 paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                        const __grid_constant__ CUtensorMap tmap_k,
@@ -766,7 +767,11 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     uint32_t n_q = 0, n_seg = 0, n_item = 0, n_scan = 0, n_merge = 0;
     uint32_t base = 0;  // tiles loaded before this segment
     bool tail_split = false;
-    const float sl0 = fabsf(P.scale) * kLog2e;
+    // (a product with the scores of what is masked, which are -inf, has to stay
+    // -inf: the scale is not below the least positive number, whose products with
+    // finite scores are 2^-21 at most)
+    auto bounded = [](float x) { return fminf(fmaxf(x, 0x1p-149f), 3e38f); };
+    const float sl0 = kQuant || kScaled ? fabsf(P.scale) * kLog2e : bounded(fabsf(P.scale) * kLog2e);
     const int tok = row / G;  // token within the row tile
     bool ok = true;
     for (;;) {
@@ -778,8 +783,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
       if (s.twin) s.h += w;  // this warpgroup's head
       // (the scales' signs are the queries', here or in the product: a masked
       // score is -inf and the largest score the largest exponent)
-      const float k_scale = P.kv.k_scale ? P.kv.k_scale[s.h] : 1.f;
-      float sl = sl0 * fabsf(k_scale);
+      const float k_scale = (kQuant || kScaled) && P.kv.k_scale ? P.kv.k_scale[s.h] : 1.f;
+      float sl = kQuant || kScaled ? sl0 * fabsf(k_scale) : sl0;
       const int items = s.items(w);
       // one thread of the warpgroup gives back what its MMAs have read: a tile
       // once, or twice where the other warpgroup has no use for it
@@ -864,13 +869,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
           if (live) sl *= scales[row];
         }
       }
-      // A product with the scores of what is masked, which are -inf, has to stay
-      // -inf: not below the least positive number, whose products with finite
-      // scores are 2^-21 at most.
-      sl = fminf(fmaxf(sl, 0x1p-149f), 3e38f);
+      if (kQuant || kScaled) sl = bounded(sl);
       float r = -INFINITY, l = 0.f;  // reference (a score, not scaled), sum
-      float neg = kOff;              // what is added to the scaled scores
-      bool any_far = false;          // a row of the warp has a reference beyond kFar
       for (int k = 0; k < items; ++k, ++n_item) {
         const int key0 = s.tile(w, k) * kKeys;
         if (!(ok = wait_warp(&m->s_full[w], n_item & 1, fail, P.status))) break;
@@ -924,13 +924,26 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
           }
           const float grown = (mx - r) * sl;  // infinite the first time
           const bool move = grown > kGrow;
-          if (any_far || __any_sync(0xFFFFFFFFu, move)) {
-            const float keep = move ? ex2_approx(-grown) : 1.f;
-            if (move) r = mx;
-            const bool far = live && r != -INFINITY && fabsf(r * sl) > kFar;
-            if (move) neg = far ? kOff : kOff - r * sl;
-            any_far = __any_sync(0xFFFFFFFFu, far);
-            if (any_far) {
+          if (move) r = mx;
+          const float ref = r == -INFINITY ? 0.f : r * sl;
+          float neg = kOff - ref;
+          const bool far = live && fabsf(ref) > kFar;
+          if (__any_sync(0xFFFFFFFFu, far || (move && k > 0))) {
+            if (k > 0) {
+              const float keep = move ? ex2_approx(-grown) : 1.f;
+              l *= keep;
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(o_t + c, o);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+                tmem_st32(o_t + c, o);
+              }
+            }
+            if (__any_sync(0xFFFFFFFFu, far)) {
+              if (far) neg = kOff;
               const float off = far ? -r : 0.f;
               const unsigned long long off2 = f2_pack(off, off);
               auto take_off = [&](uint32_t* y, int n) {
@@ -955,18 +968,6 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                   tmem_st32(s_t + c, y);
                 }
                 tmem_wait_st();
-              }
-            }
-            if (k > 0) {
-              l *= keep;
-#pragma unroll 1
-              for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
-                tmem_ld32(o_t + c, o);
-                tc::tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
-                tmem_st32(o_t + c, o);
               }
             }
           }
@@ -1341,9 +1342,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
       // their head's sign)
       const uint32_t id_qk = idesc_of(!kF16, false, kKeys) | (P.scale < 0.f ? 1u << 13 : 0u);
       // (a vote, so that the descriptor stays in a uniform register)
-      auto id_of = [&](int h) {
-        const bool flip = !kQuant && P.kv.k_scale && P.kv.k_scale[h] < 0.f;
-        return id_qk ^ (__any_sync(0xFFFFFFFFu, flip) ? 1u << 13 : 0u);
+      auto id_of = [&](int h) {  // (kScaled)
+        return id_qk ^ (__any_sync(0xFFFFFFFFu, P.kv.k_scale[h] < 0.f) ? 1u << 13 : 0u);
       };
       const bool leader = elect_one();
       const uint64_t q_desc = tc::sw128_kmajor_desc(smem_addr(smem + C::q));
@@ -1361,7 +1361,11 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         if (s.two() && !wait_warp(&there[n_q1 & 1], (n_q1 >> 1) & 1, fail, P.status)) break;
         tc::fence_after_thread_sync();
         const int nt = s.loads(), ni = s.pair ? 2 * nt : nt;
-        const uint32_t id0 = id_of(s.h), id1 = s.twin ? id_of(s.h + 1) : id0;
+        uint32_t id0 = id_qk, id1 = id_qk;
+        if constexpr (kScaled) {
+          id0 = id_of(s.h);
+          id1 = s.twin ? id_of(s.h + 1) : id0;
+        }
         auto keys_of = [&](int i) { return base + s.k_place(s.pair ? i >> 1 : i); };
         auto scores = [&](int i, uint32_t ki) {  // S_w = Q K^T of item i
           const int w = i & 1;
@@ -1372,7 +1376,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) {
             const uint32_t off = ((c >> 2) * (kRows * 128) + (c & 3) * 32) >> 4;
-            mma_ss(tmem + w * kKeys, qd + off, kd + off, w ? id1 : id0, c != 0);
+            mma_ss(tmem + w * kKeys, qd + off, kd + off, kScaled && w ? id1 : id0, c != 0);
           }
           tc::mma_commit(&m->s_full[w]);
         };
@@ -1633,12 +1637,12 @@ bool make_q_map(CUtensorMap* map, const PagedAttentionParams& p) {
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool kF16, bool kQuant>
+template <int D, bool kF16, bool kQuant, bool kScaled>
 cudaError_t launch(const PagedAttentionParams& p, const CUtensorMap& mq, const CUtensorMap& mk,
                    const CUtensorMap& mv, int sms, cudaStream_t stream) {
   using C = Cfg<D, kQuant>;
   cudaError_t err =
-      cudaFuncSetAttribute(paged_attention_kernel<D, kF16, kQuant>,
+      cudaFuncSetAttribute(paged_attention_kernel<D, kF16, kQuant, kScaled>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
   if (err != cudaSuccess) return err;
   const int grid = sms < kMaxCtas ? sms : kMaxCtas;
@@ -1653,7 +1657,7 @@ cudaError_t launch(const PagedAttentionParams& p, const CUtensorMap& mq, const C
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  err = cudaLaunchKernelEx(&cfg, paged_attention_kernel<D, kF16, kQuant>, mq, mk, mv, p);
+  err = cudaLaunchKernelEx(&cfg, paged_attention_kernel<D, kF16, kQuant, kScaled>, mq, mk, mv, p);
   if (err != cudaSuccess || p.whole) return err;
   cfg.gridDim = dim3(grid, 16);
   cfg.blockDim = dim3(256);
@@ -1664,9 +1668,12 @@ cudaError_t launch(const PagedAttentionParams& p, const CUtensorMap& mq, const C
 template <int D>
 cudaError_t launch_dim(const PagedAttentionParams& p, const CUtensorMap& mq, const CUtensorMap& mk,
                        const CUtensorMap& mv, int sms, cudaStream_t stream) {
-  if (p.kv.dtype == DSPARK_E4M3) return launch<D, true, true>(p, mq, mk, mv, sms, stream);
-  return p.dtype == DSPARK_F16 ? launch<D, true, false>(p, mq, mk, mv, sms, stream)
-                               : launch<D, false, false>(p, mq, mk, mv, sms, stream);
+  if (p.kv.dtype == DSPARK_E4M3) return launch<D, true, true, false>(p, mq, mk, mv, sms, stream);
+  if (p.kv.k_scale)
+    return p.dtype == DSPARK_F16 ? launch<D, true, false, true>(p, mq, mk, mv, sms, stream)
+                                 : launch<D, false, false, true>(p, mq, mk, mv, sms, stream);
+  return p.dtype == DSPARK_F16 ? launch<D, true, false, false>(p, mq, mk, mv, sms, stream)
+                               : launch<D, false, false, false>(p, mq, mk, mv, sms, stream);
 }
 
 }  // namespace
