@@ -445,6 +445,9 @@ dspark_status dspark_kv_append(const void* k, const void* v, dspark_dtype dtype,
  *   lse[t, hq] = log sum_j exp(x_j)
  *   out[t, hq, :] = v_scale[h] * sum_j exp(x_j - lse) v[j, h, :]
  * and what it does not see does not reach it, whatever the cache holds there.
+ * The weights exp(x_j - lse) are held in 16 bits beside the values: one more than
+ * 2^-31 below the row's largest counts as 0 in fp16 (fp16 rows, an 8-bit cache),
+ * so that an infinite value of such a weight gives NaN.
  * A row that sees nothing gives out 0 and lse -inf. Requests without tokens
  * are skipped; rows of no request are not written. A slot or length out of
  * range makes the request's rows see nothing, a page outside the cache reads

@@ -10,7 +10,7 @@
 //
 // Bound by memory for long prompts (each value read once and written once; 16384
 // tokens of 8 heads of 128 in bf16: 20.6 us, 6.5 TB/s) and by instruction issue
-// beside it where values are rounded to 8 bits (20.4 us, 71% of the slots; 48
+// beside it where values are rounded to 8 bits (20.5 us, 70% of the slots; 48
 // registers for five CTAs an SM: 22.7 without that limit); by latency for a
 // decode step (256 tokens 1.9 us), where a thread takes one token instead of
 // kBatch, so that few tokens are spread over the GPU.

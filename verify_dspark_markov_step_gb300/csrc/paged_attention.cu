@@ -57,13 +57,14 @@
 // 0 * NaN would spread) onto a slow exact path.
 //
 // Bound and measured (GB300). Few new tokens: memory; 32 requests x 8 tokens over
-// 22k, 64/8 heads of 128, bf16: 431 us, 6.87 TB/s (a copy makes 6.70); 4 x 8
-// tokens 69 us, one token (32/8 heads) 28 us, of which 8 us pass before the first
-// scores (plan, first page, first tile) and 4 in the join. Prompts: the tensor
-// cores; 4096 tokens over 12288: 1.21 ms, 1.58 PFLOP/s at full clocks, the tensor
-// pipe active 68%. An 8-bit cache: shared memory, through which a tile passes
-// three times (raw, converted, operands): about 1800 clocks a tile of K and V at
-// 128 bytes a clock, 1870 taken; 256 x 4 tokens over 2-6k, 32/4 heads: 268 us.
+// 22k, 64/8 heads of 128, bf16: 431 to 440 us, 6.75 TB/s or more (a copy makes
+// 6.70); 4 x 8 tokens 70 us, one token (32/8 heads) 28.7 us, of which 8 us pass
+// before the first scores (plan, first page, first tile) and 4 in the join.
+// Prompts: the tensor cores; 4096 tokens over 12288: 1.30 ms among other work, 1.48
+// PFLOP/s (1.22 ms by itself on a cool card), the tensor pipe active 68%. An 8-bit
+// cache: shared memory, through which a tile passes three times here (raw,
+// converted, operands): about 1800 clocks a tile of K and V at 128 bytes a clock,
+// 1870 taken; 256 x 4 tokens over 2-6k, 32/4 heads: 268 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>

@@ -16,10 +16,11 @@
 // counter that it resets. Table entries that are new and stack entries above
 // the old top are read by nobody and are written at once.
 //
-// Bound: latency for a decode step (one CTA: two dependent rounds of loads, three
-// scans, a dependent round for the tokens; 4.6 us for 32 requests x 8 tokens), the
-// same and the 16 bytes per token of positions and slot map for long prompts
-// (9.4 us for 256 requests and 262 thousand tokens, 4.2 MB).
+// Bound: latency. A decode step is one CTA: two dependent rounds of loads, three
+// scans, a dependent round for the tokens (32 requests x 8 tokens: 4.5 us back to
+// back, 8.5 with cold caches). For long prompts a thread places eight tokens, each
+// by a bisection and a dependent load (256 requests, room for 262 thousand tokens,
+// 4.2 MB of positions and slots: 9.6 us, 11.7 cold; the bytes alone are 0.6).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
