@@ -434,6 +434,70 @@ dspark_status dspark_kv_append(const void* k, const void* v, dspark_dtype dtype,
                                dspark_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * dspark_qk_rope -- the norm of each query and key head and its rotation by the
+ * token's position, in one pass over the rows.
+ *
+ * For every token t with positions[t] >= 0 and every query (key) head's row x of
+ * head_dim values, all in fp32, rounded once into q_out (k_out):
+ *   with a weight w:  x_d = x_d w_d / sqrt(mean_d x_d^2 + eps)
+ *   for i < rotary_dim / 2, with t_i = 2 pi positions[t] turns[i] / 2^64 and the
+ *   pair (a, b) = (x_i, x_(i + rotary_dim / 2)), or (x_2i, x_(2i+1)) if interleaved:
+ *     (a, b) = factor (a cos t_i - b sin t_i, b cos t_i + a sin t_i)
+ * The other head_dim - rotary_dim values of a row are only normalised. Tokens with
+ * a negative position are skipped: their rows in q_out and k_out stay as they are.
+ *
+ * Arguments
+ *   q, q_out      [T, q_heads, head_dim] dtype, tokens q_stride / q_out_stride
+ *                 elements apart (the heads of a token are contiguous). q_out is
+ *                 q itself with the same stride (in place), or apart from it.
+ *   k, k_out      [T, kv_heads, head_dim], the same; kv_heads = 0: no keys
+ *   dtype         DSPARK_BF16 or DSPARK_F16
+ *   positions     [T] int64
+ *   turns         [rotary_dim / 2] uint64: the angle of a position in units of
+ *                 2^-64 turns, rint(frequency / (2 pi) 2^64) modulo 2^64 for a
+ *                 frequency in radians a position. The angle is exact but for
+ *                 that rounding, whatever the position.
+ *   factor        finite (the factor on attention that a scaling of the
+ *                 frequencies asks for, else 1)
+ *   rotary_dim    a multiple of 16 up to head_dim; 0: no rotation (turns is not
+ *                 read)
+ *   q_weight, k_weight  [head_dim] dtype, or NULL: no norm. The squares are
+ *                 summed in fp32: rows with values past 2^60 have no norm.
+ *   eps           finite, >= 0
+ *   head_dim      a multiple of 16 up to 256
+ *   q_heads in [1, 2^17], kv_heads in [0, 1024], T in [0, 2^30).
+ * Alignment: rows, weights and all strides (in bytes): 16.
+ *
+ * dspark_qk_rope_append -- the same, with the keys and the values in their pages:
+ * q as above; for every token t with positions[t] >= 0 and slot_map[t] >= 0 the
+ * rotated keys and the values as they are go where dspark_kv_append would put them.
+ * In an 8-bit cache, or with scales, the keys' fp32 results are divided by their
+ * scale and rounded once. A slot past the cache is skipped, with DSPARK_ERR_BOUNDS.
+ *   v             [T, kv_heads, head_dim] dtype, tokens v_stride elements apart
+ *   cache         head_dim 64 or 128 and kv_heads are its
+ *   slot_map      [T] int64; of two tokens with one slot either may win
+ * Alignment: the caches and their strides, too.
+ * ------------------------------------------------------------------------ */
+dspark_status dspark_qk_rope(const void* q, void* q_out, const void* k,
+                             void* k_out, dspark_dtype dtype, int64_t q_stride,
+                             int64_t q_out_stride, int64_t k_stride,
+                             int64_t k_out_stride, const int64_t* positions,
+                             const uint64_t* turns, float factor,
+                             int rotary_dim, int interleaved,
+                             const void* q_weight, const void* k_weight,
+                             float eps, int q_heads, int kv_heads, int head_dim,
+                             int T, dspark_stream_t stream);
+
+dspark_status dspark_qk_rope_append(
+    const void* q, void* q_out, const void* k, const void* v,
+    dspark_dtype dtype, int64_t q_stride, int64_t q_out_stride,
+    int64_t k_stride, int64_t v_stride, const dspark_paged_kv* cache,
+    const int64_t* positions, const int64_t* slot_map, const uint64_t* turns,
+    float factor, int rotary_dim, int interleaved, const void* q_weight,
+    const void* k_weight, float eps, int q_heads, int T, int32_t* status,
+    dspark_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * dspark_paged_attention -- attention of a step's new tokens over the pages.
  *
  * Request b owns the query rows t = query_start[b] .. query_start[b+1] - 1;

@@ -8,6 +8,7 @@ The computation lives in the CUDA library built from ``csrc/`` (C ABI in
 * ``step``       -- one decode step (Markov loop + verification) on device tensors
 * ``paged``      -- the paged key/value cache of the verification pass, and a
                     speculative decoding loop on it
+* ``rotary``     -- frequencies of rotary positions for the rotating calls
 * ``workloads``  -- seeded synthetic inputs
 """
 
@@ -18,7 +19,7 @@ def __getattr__(name):
     if name in ("markov_sample", "rejection_sample", "noise", "markov_workspace_bytes",
                 "verify_workspace_bytes", "status_string", "DsparkError", "lib",
                 "paged_tables", "kv_append", "paged_attention",
-                "paged_attention_workspace_bytes"):
+                "paged_attention_workspace_bytes", "qk_rope", "qk_rope_append"):
         from . import _lib
         globals()[name] = value = getattr(_lib, name)
         return value

@@ -49,6 +49,8 @@ EXPORTS = (
     "dspark_noise",
     "dspark_paged_tables",
     "dspark_kv_append",
+    "dspark_qk_rope",
+    "dspark_qk_rope_append",
     "dspark_paged_attention_workspace_bytes",
     "dspark_paged_attention",
     "dspark_status_string",
@@ -121,6 +123,14 @@ def lib(path: str | None = None) -> ctypes.CDLL:
         L.dspark_paged_tables.argtypes = [vp] * 12 + [i32] * 6 + [vp, vp]
         L.dspark_kv_append.restype = i32
         L.dspark_kv_append.argtypes = [vp, vp, i32, i64, i64, kvp, vp, i32, vp, vp]
+        f32 = ctypes.c_float
+        L.dspark_qk_rope.restype = i32
+        L.dspark_qk_rope.argtypes = ([vp] * 4 + [i32] + [i64] * 4 + [vp, vp, f32, i32, i32, vp, vp,
+                                                                     f32] + [i32] * 4 + [vp])
+        L.dspark_qk_rope_append.restype = i32
+        L.dspark_qk_rope_append.argtypes = ([vp] * 4 + [i32] + [i64] * 4
+                                            + [kvp, vp, vp, vp, f32, i32, i32, vp, vp, f32, i32,
+                                               i32, vp, vp])
         L.dspark_paged_attention_workspace_bytes.restype = sz
         L.dspark_paged_attention_workspace_bytes.argtypes = [i32] * 4
         L.dspark_paged_attention.restype = i32
@@ -587,6 +597,87 @@ def kv_append(k, v, k_cache, v_cache, slot_map, k_scale=None, v_scale=None, stat
         _maybe(status, "status", torch.int32), _raw_stream(stream, slot_map))
     if code:
         _check(code, "dspark_kv_append")
+
+
+def _here(t, name):
+    """Refuses tensors of another device than the current one: a launch goes to the
+    current device."""
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, which is not the current device")
+
+
+def _rotation(turns, head_dim, q_weight, k_weight, dtype):
+    """(address of the turns, rotary_dim, addresses of the weights)."""
+    shape = (head_dim,)
+    weights = (_maybe(q_weight, "q_weight", dtype, shape),
+               _maybe(k_weight, "k_weight", dtype, shape))
+    if turns is None:
+        return None, 0, *weights
+    if turns.dim() != 1:
+        raise ValueError("turns must be [rotary_dim / 2]")
+    return _of(turns, "turns", torch.int64), 2 * turns.shape[0], *weights
+
+
+def _rows_out(out, name, like):
+    """_rows of where rows go: as many as `like` has, of its dtype."""
+    at, dt, stride = _rows(out, name)
+    if out.shape != like.shape or out.dtype is not like.dtype:
+        raise ValueError(f"{name} must be {list(like.shape)} {like.dtype}")
+    return at, stride
+
+
+def qk_rope(q, k, positions, turns=None, factor=1.0, interleaved=False, q_weight=None,
+            k_weight=None, eps=1e-6, q_out=None, k_out=None, stream=None):
+    """dspark_qk_rope on torch tensors (see include/dspark.h): the norm of each head (with
+    q_weight / k_weight [head_dim]) and the rotation by positions [T] of rows q [T,
+    q_heads, head_dim] and k [T, kv_heads, head_dim] or None (views of a fused projection
+    will do), in place or into q_out / k_out. turns [rotary_dim / 2] and factor are a
+    rotary.Rotary's."""
+    qp, dt, qs = _rows(q, "q")
+    T, Hq, D = q.shape
+    qo, qos = (qp, qs) if q_out is None else _rows_out(q_out, "q_out", q)
+    kp = ko = None
+    ks = kos = H = 0
+    if k is not None:
+        kp, kdt, ks = _rows(k, "k")
+        H = k.shape[1]
+        if k.shape != (T, H, D) or kdt != dt:
+            raise ValueError(f"k must be [{T}, kv_heads, {D}] of q's dtype")
+        ko, kos = (kp, ks) if k_out is None else _rows_out(k_out, "k_out", k)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    _here(q, "q")
+    turns_p, R, qw, kw = _rotation(turns, D, q_weight, k_weight, q.dtype)
+    code = (_lib or lib()).dspark_qk_rope(
+        qp, qo, kp, ko, dt, qs, qos, ks, kos, _of(positions, "positions", torch.int64, (T,)),
+        turns_p, factor, R, bool(interleaved), qw, kw, eps, Hq, H, D, T, _raw_stream(stream, q))
+    if code:
+        _check(code, "dspark_qk_rope")
+
+
+def qk_rope_append(q, k, v, k_cache, v_cache, positions, slot_map, turns=None, factor=1.0,
+                   interleaved=False, q_weight=None, k_weight=None, eps=1e-6, q_out=None,
+                   k_scale=None, v_scale=None, status=None, stream=None):
+    """dspark_qk_rope_append on torch tensors (see include/dspark.h): as qk_rope for q, and
+    the keys, normalised and rotated, and the values into the caches as by kv_append."""
+    cache, H, D = _paged_kv(k_cache, v_cache, k_scale, v_scale)
+    qp, dt, qs = _rows(q, "q")
+    T, Hq = q.shape[:2]
+    kp, kdt, ks = _rows(k, "k")
+    vp, vdt, vs = _rows(v, "v")
+    if q.shape[2] != D or k.shape != (T, H, D) or v.shape != (T, H, D) or not dt == kdt == vdt:
+        raise ValueError(f"q, k and v must be [{T}, heads, {D}] of one dtype, k and v with "
+                         f"{H} heads")
+    qo, qos = (qp, qs) if q_out is None else _rows_out(q_out, "q_out", q)
+    _here(q, "q")
+    turns_p, R, qw, kw = _rotation(turns, D, q_weight, k_weight, q.dtype)
+    i64 = torch.int64
+    code = (_lib or lib()).dspark_qk_rope_append(
+        qp, qo, kp, vp, dt, qs, qos, ks, vs, cache, _of(positions, "positions", i64, (T,)),
+        _of(slot_map, "slot_map", i64, (T,)), turns_p, factor, R, bool(interleaved), qw, kw, eps,
+        Hq, T, _maybe(status, "status", torch.int32), _raw_stream(stream, q))
+    if code:
+        _check(code, "dspark_qk_rope_append")
 
 
 def paged_attention_workspace_bytes(B, q_heads, kv_heads, head_dim) -> int:

@@ -14,11 +14,11 @@
 // registers for five CTAs an SM: 22.7 without that limit); by latency for a
 // decode step (256 tokens 1.9 us), where a thread takes one token instead of
 // kBatch, so that few tokens are spread over the GPU.
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include "common.cuh"
+#include "kv_values.cuh"
 #include "paged.h"
 
 namespace dspark {
@@ -27,33 +27,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBatch = 4;  // tokens per thread, all loaded before the first is stored
-
-__device__ __forceinline__ float half_bits_to_float(uint32_t bits) {
-  float f;
-  asm("{ .reg .b16 h; cvt.u16.u32 h, %1; cvt.f32.f16 %0, h; }" : "=f"(f) : "r"(bits));
-  return f;
-}
-
-// Two values to 8 bits, nearest even, clamped to the largest finite value,
-// NaN kept; `lo` in the low byte.
-__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
-  uint32_t r;
-  asm("{ .reg .b16 h; cvt.rn.satfinite.e4m3x2.f32 h, %1, %2; cvt.u32.u16 %0, h; }"
-      : "=r"(r)
-      : "f"(hi), "f"(lo));
-  return r;
-}
-
-template <bool kF16>
-__device__ __forceinline__ void unpack(uint32_t w, float& a, float& b) {
-  if constexpr (kF16) {
-    a = half_bits_to_float(w & 0xFFFFu);
-    b = half_bits_to_float(w >> 16);
-  } else {
-    a = __uint_as_float(w << 16);
-    b = __uint_as_float(w & 0xFFFF0000u);
-  }
-}
 
 // A piece by divisions (out of line: hardly ever called).
 template <bool kF16>
@@ -108,10 +81,7 @@ __device__ __forceinline__ uint4 scaled16(uint4 x, float scale) {
     unpack<kF16>(w[i], a, b);
     a = __fdiv_rn(a, scale);
     b = __fdiv_rn(b, scale);
-    if constexpr (kF16)
-      asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(b), "f"(a));
-    else
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(b), "f"(a));
+    w[i] = pack16<kF16>(a, b);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }

@@ -44,6 +44,28 @@ struct KvAppendParams {
 };
 cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t stream);
 
+// Norm and rotation of query and key rows, keys and values into their pages
+// (qk_rope.cu).
+struct QkRopeParams {
+  const void* src[3];       // queries, keys, values
+  int64_t src_stride[3];    // elements between tokens
+  void* dst[3];             // rows, or (keys and values) the caches
+  int64_t dst_stride[3];    // elements between tokens
+  int64_t block_stride[2], head_stride[2];
+  const float* scale[2];    // [kv_heads] or null
+  const int64_t* positions;
+  const int64_t* slot_map;  // null: no cache
+  int64_t num_slots;
+  const uint64_t* turns;    // [rotary / 2]
+  const void* weight[2];    // [D] of the rows' type, or null: no norm
+  float factor, eps, inv_d;
+  int rotary;               // 0: no rotation
+  int interleaved, dtype, cache_dtype;
+  int T, Hq, H, D, page_shift;
+  int32_t* status;
+};
+cudaError_t launch_qk_rope(const QkRopeParams& p, cudaStream_t stream);
+
 // Attention of new tokens over the pages (paged_attention.cu).
 struct PagedAttentionParams {
   const void* q;

@@ -47,6 +47,37 @@ dspark_status check_cache(const dspark_paged_kv* c, int dtype) {
   return DSPARK_OK;
 }
 
+// The checks both rotating calls make of the rotation and the norms.
+dspark_status check_rotation(const uint64_t* turns, float factor, int rotary_dim, int interleaved,
+                             const void* q_weight, const void* k_weight, float eps, int head_dim) {
+  if (interleaved != 0 && interleaved != 1) return DSPARK_ERR_INVALID_ARG;
+  if (rotary_dim < 0 || rotary_dim > head_dim || (rotary_dim > 0 && (!turns || !isfinite(factor))))
+    return DSPARK_ERR_INVALID_ARG;
+  if ((q_weight || k_weight) && !(isfinite(eps) && eps >= 0.f)) return DSPARK_ERR_INVALID_ARG;
+  if (rotary_dim % 16 != 0) return DSPARK_ERR_UNSUPPORTED;
+  if (!aligned16(q_weight) || !aligned16(k_weight) || (reinterpret_cast<uintptr_t>(turns) & 7u))
+    return DSPARK_ERR_ALIGNMENT;
+  return DSPARK_OK;
+}
+
+// A parameter block with the rotation and the norms.
+dspark::QkRopeParams rotation_params(const int64_t* positions, const uint64_t* turns, float factor,
+                                     int rotary_dim, int interleaved, const void* q_weight,
+                                     const void* k_weight, float eps, int head_dim) {
+  dspark::QkRopeParams p = {};
+  p.positions = positions;
+  p.turns = turns;
+  p.weight[0] = q_weight;
+  p.weight[1] = k_weight;
+  p.factor = factor;
+  p.eps = eps;
+  p.inv_d = 1.f / static_cast<float>(head_dim);
+  p.rotary = rotary_dim;
+  p.interleaved = interleaved;
+  p.D = head_dim;
+  return p;
+}
+
 }  // namespace
 
 extern "C" {
@@ -127,6 +158,98 @@ dspark_status dspark_kv_append(const void* k, const void* v, dspark_dtype dtype,
   p.page_shift = page_shift_of(cache->page_size);
   p.status = status;
   if (dspark::launch_kv_append(p, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return DSPARK_ERR_CUDA;
+  return DSPARK_OK;
+}
+
+dspark_status dspark_qk_rope(const void* q, void* q_out, const void* k, void* k_out,
+                             dspark_dtype dtype, int64_t q_stride, int64_t q_out_stride,
+                             int64_t k_stride, int64_t k_out_stride, const int64_t* positions,
+                             const uint64_t* turns, float factor, int rotary_dim, int interleaved,
+                             const void* q_weight, const void* k_weight, float eps, int q_heads,
+                             int kv_heads, int head_dim, int T, dspark_stream_t stream) {
+  if (T < 0 || T >= 1 << 30 || q_heads < 1 || q_heads > 1 << 17 || kv_heads < 0 ||
+      kv_heads > 1024 || !half_dtype(dtype))
+    return DSPARK_ERR_INVALID_ARG;
+  if (head_dim < 16 || head_dim > 256 || head_dim % 16 != 0) return DSPARK_ERR_UNSUPPORTED;
+  const dspark_status bad = check_rotation(turns, factor, rotary_dim, interleaved, q_weight,
+                                           k_weight, eps, head_dim);
+  if (bad != DSPARK_OK || T == 0) return bad;
+  const bool keys = kv_heads > 0;
+  if (!q || !q_out || !positions || (keys && (!k || !k_out))) return DSPARK_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(q_out) || !stride_ok(q_stride, 2) || !stride_ok(q_out_stride, 2))
+    return DSPARK_ERR_ALIGNMENT;
+  if (keys && (!aligned16(k) || !aligned16(k_out) || !stride_ok(k_stride, 2) ||
+               !stride_ok(k_out_stride, 2)))
+    return DSPARK_ERR_ALIGNMENT;
+  dspark::QkRopeParams p = rotation_params(positions, turns, factor, rotary_dim, interleaved,
+                                           q_weight, keys ? k_weight : nullptr, eps, head_dim);
+  p.src[0] = q;
+  p.src[1] = k;
+  p.src_stride[0] = q_stride;
+  p.src_stride[1] = k_stride;
+  p.dst[0] = q_out;
+  p.dst[1] = k_out;
+  p.dst_stride[0] = q_out_stride;
+  p.dst_stride[1] = k_out_stride;
+  p.dtype = dtype;
+  p.T = T;
+  p.Hq = q_heads;
+  p.H = kv_heads;
+  if (dspark::launch_qk_rope(p, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return DSPARK_ERR_CUDA;
+  return DSPARK_OK;
+}
+
+dspark_status dspark_qk_rope_append(const void* q, void* q_out, const void* k, const void* v,
+                                    dspark_dtype dtype, int64_t q_stride, int64_t q_out_stride,
+                                    int64_t k_stride, int64_t v_stride,
+                                    const dspark_paged_kv* cache, const int64_t* positions,
+                                    const int64_t* slot_map, const uint64_t* turns, float factor,
+                                    int rotary_dim, int interleaved, const void* q_weight,
+                                    const void* k_weight, float eps, int q_heads, int T,
+                                    int32_t* status, dspark_stream_t stream) {
+  if (T < 0 || T >= 1 << 30 || q_heads < 1 || q_heads > 1 << 17) return DSPARK_ERR_INVALID_ARG;
+  dspark_status bad = check_cache(cache, dtype);
+  if (bad == DSPARK_OK)
+    bad = check_rotation(turns, factor, rotary_dim, interleaved, q_weight, k_weight, eps,
+                         cache->head_dim);
+  if (bad != DSPARK_OK || T == 0) return bad;
+  if (!q || !q_out || !k || !v || !positions || !slot_map) return DSPARK_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(v) ||
+      !stride_ok(q_stride, 2) || !stride_ok(q_out_stride, 2) || !stride_ok(k_stride, 2) ||
+      !stride_ok(v_stride, 2))
+    return DSPARK_ERR_ALIGNMENT;
+  dspark::QkRopeParams p = rotation_params(positions, turns, factor, rotary_dim, interleaved,
+                                           q_weight, k_weight, eps, cache->head_dim);
+  p.src[0] = q;
+  p.src[1] = k;
+  p.src[2] = v;
+  p.src_stride[0] = q_stride;
+  p.src_stride[1] = k_stride;
+  p.src_stride[2] = v_stride;
+  p.dst[0] = q_out;
+  p.dst[1] = cache->k;
+  p.dst[2] = cache->v;
+  p.dst_stride[0] = q_out_stride;
+  p.dst_stride[1] = cache->k_token_stride;
+  p.dst_stride[2] = cache->v_token_stride;
+  p.block_stride[0] = cache->k_block_stride;
+  p.block_stride[1] = cache->v_block_stride;
+  p.head_stride[0] = cache->k_head_stride;
+  p.head_stride[1] = cache->v_head_stride;
+  p.scale[0] = cache->k_scale;
+  p.scale[1] = cache->v_scale;
+  p.slot_map = slot_map;
+  p.num_slots = static_cast<int64_t>(cache->num_blocks) * cache->page_size;
+  p.dtype = dtype;
+  p.cache_dtype = cache->dtype;
+  p.T = T;
+  p.Hq = q_heads;
+  p.H = cache->kv_heads;
+  p.page_shift = page_shift_of(cache->page_size);
+  p.status = status;
+  if (dspark::launch_qk_rope(p, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
     return DSPARK_ERR_CUDA;
   return DSPARK_OK;
 }
