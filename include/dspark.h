@@ -410,6 +410,101 @@ dspark_status dspark_paged_tables(
     int page_size, int32_t* status, dspark_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Blocks that several rows hold.
+ *
+ * shares [N] int32 counts for each block the rows of the block table that hold it
+ * beyond the first; all 0 before the first call. dspark_paged_fork makes shared
+ * blocks; where a cache has them, every call on its tables gets `shares`. New tokens
+ * never reach a shared block: a fork has a copy of a last block that is not full.
+ *
+ * dspark_paged_tables_shared -- dspark_paged_tables for such a cache: a request that
+ * would return a block which another row holds too (its cached_lens was lowered into
+ * its shared blocks) is treated as padding, with DSPARK_ERR_BOUNDS. shares may be NULL.
+ *
+ * dspark_paged_fork -- the tokens of slots src into slots dst.
+ *   For every i in order with src[i], dst[i] >= 0: dst's cached_lens becomes L =
+ *   src's, its held_blocks ceil(L / page_size). With shares the L / page_size full
+ *   blocks are src's own (their counts grow by 1) and a last one that is not full is
+ *   new; without, all are new. New blocks come off the stack in the order of the forks
+ *   and their columns; copies[0 .. count[0]) gets a pair (src's block, the new one)
+ *   for each, in that order, for dspark_paged_copy.
+ *   Tokens that an accept count has yet to add to cached_lens are not forked.
+ *   A fork that cannot be made is skipped and *status set: a slot, length or held
+ *   count out of range, a dst that holds blocks or is named before, a src that is a
+ *   dst of the call, or copies past max_copies (the first that does not fit and all
+ *   after it that have some) give DSPARK_ERR_BOUNDS; blocks that the stack does not
+ *   have (the same) DSPARK_ERR_CACHE_FULL.
+ *
+ * dspark_paged_free -- gives up all blocks of slots.
+ *   The slots' cached_lens and held_blocks become 0, their table entries -1. A block
+ *   that no other row holds goes on the stack: last slot first and of each the last
+ *   column first, at the place of the last of the call's slots that held it. (So
+ *   forks that are freed in their order leave the stack as it was.) Slots < 0 are
+ *   skipped; a slot or held count out of range or a slot that is named before too,
+ *   with DSPARK_ERR_BOUNDS.
+ *
+ * dspark_paged_compact -- the held blocks become the first ones.
+ *   With U = N - (blocks on the stack), the blocks from U on that are not on the
+ *   stack, in ascending order, get the numbers of those below U that are:
+ *   copies[0 .. count[0]) are the pairs (old number, new number), and the table
+ *   entries of all slots and shares follow. free_blocks[i] = N - 1 - i for i < N - U.
+ *   The blocks' contents are moved by dspark_paged_copy, on the same stream before
+ *   anything that reads them. A table entry within held_blocks that is out of range or
+ *   on the stack stays as it is, with DSPARK_ERR_BOUNDS.
+ *
+ * dspark_paged_copy -- blocks copied in the caches of all layers.
+ *   For i < count[0]: block copies[i][1] of each of the n_caches caches becomes a copy
+ *   of block copies[i][0], keys and values. No block is both read and written, and of
+ *   two copies into one either may win. A block out of range is skipped, a count past
+ *   max_copies cut off, with DSPARK_ERR_BOUNDS.
+ *
+ * Arguments (others as for dspark_paged_tables)
+ *   src, dst, slots  [n] int32, n in [0, 1024]
+ *   copies        [max_copies, 2] int32, 8-byte aligned (entries past count[0] are
+ *                 unspecified); for compaction max_copies >= N / 2
+ *   count         [1] int32 (written by fork and compaction)
+ *   caches        HOST array of n_caches in [0, 2^16], which differ in k, v and the
+ *                 scales (not read) alone
+ *   workspace     at least dspark_paged_compact_workspace_bytes(N) bytes
+ * ------------------------------------------------------------------------ */
+dspark_status dspark_paged_tables_shared(
+    const int32_t* req_state_idx, const int32_t* new_lens, int32_t* cached_lens,
+    const int32_t* num_accepted, int32_t* block_table, int32_t* held_blocks,
+    int32_t* free_blocks, int32_t* pool, const int32_t* shares,
+    int32_t* query_start, int32_t* seq_lens, int64_t* positions,
+    int64_t* slot_map, int B, int S, int M, int N, int T, int page_size,
+    int32_t* status, dspark_stream_t stream);
+
+dspark_status dspark_paged_fork(
+    const int32_t* src, const int32_t* dst, int32_t* cached_lens,
+    int32_t* block_table, int32_t* held_blocks, const int32_t* free_blocks,
+    int32_t* pool, int32_t* shares, int32_t* copies, int32_t* count, int n,
+    int S, int M, int N, int max_copies, int page_size, int32_t* status,
+    dspark_stream_t stream);
+
+dspark_status dspark_paged_free(const int32_t* slots, int32_t* cached_lens,
+                                int32_t* block_table, int32_t* held_blocks,
+                                int32_t* free_blocks, int32_t* pool,
+                                int32_t* shares, int n, int S, int M, int N,
+                                int32_t* status, dspark_stream_t stream);
+
+size_t dspark_paged_compact_workspace_bytes(int N);
+
+dspark_status dspark_paged_compact(int32_t* block_table,
+                                   const int32_t* held_blocks,
+                                   int32_t* free_blocks, int32_t* pool,
+                                   int32_t* shares, int32_t* copies,
+                                   int32_t* count, int S, int M, int N,
+                                   int max_copies, void* workspace,
+                                   size_t workspace_bytes, int32_t* status,
+                                   dspark_stream_t stream);
+
+dspark_status dspark_paged_copy(const dspark_paged_kv* caches, int n_caches,
+                                const int32_t* copies, const int32_t* count,
+                                int max_copies, int32_t* status,
+                                dspark_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * dspark_kv_append -- keys and values of new tokens into their pages.
  *
  * For every token t with slot_map[t] >= 0 and every head h:

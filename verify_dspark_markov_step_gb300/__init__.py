@@ -19,7 +19,9 @@ def __getattr__(name):
     if name in ("markov_sample", "rejection_sample", "noise", "markov_workspace_bytes",
                 "verify_workspace_bytes", "status_string", "DsparkError", "lib",
                 "paged_tables", "kv_append", "paged_attention",
-                "paged_attention_workspace_bytes", "qk_rope", "qk_rope_append"):
+                "paged_attention_workspace_bytes", "qk_rope", "qk_rope_append",
+                "paged_fork", "paged_free", "paged_compact", "paged_compact_workspace_bytes",
+                "paged_copy", "PagedCaches"):
         from . import _lib
         globals()[name] = value = getattr(_lib, name)
         return value

@@ -48,6 +48,12 @@ EXPORTS = (
     "dspark_rejection_sample",
     "dspark_noise",
     "dspark_paged_tables",
+    "dspark_paged_tables_shared",
+    "dspark_paged_fork",
+    "dspark_paged_free",
+    "dspark_paged_compact_workspace_bytes",
+    "dspark_paged_compact",
+    "dspark_paged_copy",
     "dspark_kv_append",
     "dspark_qk_rope",
     "dspark_qk_rope_append",
@@ -121,6 +127,18 @@ def lib(path: str | None = None) -> ctypes.CDLL:
         kvp = ctypes.POINTER(PagedKv)
         L.dspark_paged_tables.restype = i32
         L.dspark_paged_tables.argtypes = [vp] * 12 + [i32] * 6 + [vp, vp]
+        L.dspark_paged_tables_shared.restype = i32
+        L.dspark_paged_tables_shared.argtypes = [vp] * 13 + [i32] * 6 + [vp, vp]
+        L.dspark_paged_fork.restype = i32
+        L.dspark_paged_fork.argtypes = [vp] * 10 + [i32] * 6 + [vp, vp]
+        L.dspark_paged_free.restype = i32
+        L.dspark_paged_free.argtypes = [vp] * 7 + [i32] * 4 + [vp, vp]
+        L.dspark_paged_compact_workspace_bytes.restype = sz
+        L.dspark_paged_compact_workspace_bytes.argtypes = [i32]
+        L.dspark_paged_compact.restype = i32
+        L.dspark_paged_compact.argtypes = [vp] * 7 + [i32] * 4 + [vp, sz, vp, vp]
+        L.dspark_paged_copy.restype = i32
+        L.dspark_paged_copy.argtypes = [kvp, i32, vp, vp, i32, vp, vp]
         L.dspark_kv_append.restype = i32
         L.dspark_kv_append.argtypes = [vp, vp, i32, i64, i64, kvp, vp, i32, vp, vp]
         f32 = ctypes.c_float
@@ -558,26 +576,125 @@ def _paged_kv(k_cache, v_cache, k_scale, v_scale):
 
 def paged_tables(req_state_idx, new_lens, cached_lens, block_table, held_blocks, free_blocks,
                  pool, query_start, seq_lens, positions, slot_map, page_size, num_accepted=None,
-                 status=None, stream=None):
+                 status=None, stream=None, shares=None):
     """dspark_paged_tables on torch tensors (see include/dspark.h): the step's
     block tables, query offsets, positions and slot map from the request
     lengths; updates cached_lens (with num_accepted), block_table,
-    held_blocks, free_blocks and pool."""
+    held_blocks, free_blocks and pool. shares [N]: of a cache whose blocks are
+    shared (dspark_paged_tables_shared)."""
     i32, i64 = torch.int32, torch.int64
     B, (S, M) = req_state_idx.shape[0], block_table.shape
     N, T = free_blocks.shape[0], slot_map.shape[0]
-    code = (_lib or lib()).dspark_paged_tables(
+    code = (_lib or lib()).dspark_paged_tables_shared(
         _of(req_state_idx, "req_state_idx", i32, (B,)), _of(new_lens, "new_lens", i32, (B,)),
         _of(cached_lens, "cached_lens", i32, (S,)),
         _maybe(num_accepted, "num_accepted", i32, (B,)),
         _of(block_table, "block_table", i32), _of(held_blocks, "held_blocks", i32, (S,)),
         _of(free_blocks, "free_blocks", i32, (N,)), _of(pool, "pool", i32, (2,)),
+        _maybe(shares, "shares", i32, (N,)),
         _of(query_start, "query_start", i32, (B + 1,)), _of(seq_lens, "seq_lens", i32, (B,)),
         _of(positions, "positions", i64, (T,)), _of(slot_map, "slot_map", i64, (T,)),
         B, S, M, N, T, page_size, _maybe(status, "status", i32),
         _raw_stream(stream, query_start))
     if code:
         _check(code, "dspark_paged_tables")
+
+
+def _pages_of(cached_lens, block_table, held_blocks, free_blocks, pool, shares):
+    """Addresses of a cache's tables, S, M and N."""
+    i32 = torch.int32
+    S, M = block_table.shape
+    N = free_blocks.shape[0]
+    return (_maybe(cached_lens, "cached_lens", i32, (S,)), _of(block_table, "block_table", i32),
+            _of(held_blocks, "held_blocks", i32, (S,)), _of(free_blocks, "free_blocks", i32),
+            _of(pool, "pool", i32, (2,)), _maybe(shares, "shares", i32, (N,)), S, M, N)
+
+
+def paged_fork(src, dst, cached_lens, block_table, held_blocks, free_blocks, pool, copies, count,
+               page_size, shares=None, status=None, stream=None):
+    """dspark_paged_fork on torch tensors (see include/dspark.h): the tokens of slots src
+    [n] into slots dst [n], by copies of their blocks or (with shares [N]) sharing the
+    full ones. copies [C, 2] and count [1] are what paged_copy has to copy then."""
+    i32 = torch.int32
+    n = src.shape[0]
+    lens, table, held, free, pool_p, shares_p, S, M, N = _pages_of(
+        cached_lens, block_table, held_blocks, free_blocks, pool, shares)
+    _here(block_table, "block_table")
+    code = (_lib or lib()).dspark_paged_fork(
+        _of(src, "src", i32, (n,)), _of(dst, "dst", i32, (n,)), lens, table, held, free, pool_p,
+        shares_p, _of(copies, "copies", i32, (copies.shape[0], 2)), _of(count, "count", i32, (1,)),
+        n, S, M, N, copies.shape[0], page_size, _maybe(status, "status", i32),
+        _raw_stream(stream, block_table))
+    if code:
+        _check(code, "dspark_paged_fork")
+
+
+def paged_free(slots, cached_lens, block_table, held_blocks, free_blocks, pool, shares=None,
+               status=None, stream=None):
+    """dspark_paged_free on torch tensors (see include/dspark.h): gives up all blocks of
+    slots [n]."""
+    i32 = torch.int32
+    n = slots.shape[0]
+    lens, table, held, free, pool_p, shares_p, S, M, N = _pages_of(
+        cached_lens, block_table, held_blocks, free_blocks, pool, shares)
+    _here(block_table, "block_table")
+    code = (_lib or lib()).dspark_paged_free(
+        _of(slots, "slots", i32, (n,)), lens, table, held, free, pool_p, shares_p, n, S, M, N,
+        _maybe(status, "status", i32), _raw_stream(stream, block_table))
+    if code:
+        _check(code, "dspark_paged_free")
+
+
+def paged_compact_workspace_bytes(num_blocks) -> int:
+    return int(lib().dspark_paged_compact_workspace_bytes(num_blocks))
+
+
+def paged_compact(block_table, held_blocks, free_blocks, pool, copies, count, shares=None,
+                  workspace_buf=None, status=None, stream=None):
+    """dspark_paged_compact on torch tensors (see include/dspark.h): the held blocks get the
+    first numbers. copies [C, 2] (C at least half the blocks) and count [1] are what
+    paged_copy has to copy then."""
+    i32 = torch.int32
+    _, table, held, free, pool_p, shares_p, S, M, N = _pages_of(
+        None, block_table, held_blocks, free_blocks, pool, shares)
+    _here(block_table, "block_table")
+    if workspace_buf is None:
+        with torch.cuda.stream(stream):  # memory of the stream that uses it
+            workspace_buf = workspace(paged_compact_workspace_bytes(N), block_table.device)
+    code = (_lib or lib()).dspark_paged_compact(
+        table, held, free, pool_p, shares_p, _of(copies, "copies", i32, (copies.shape[0], 2)),
+        _of(count, "count", i32, (1,)), S, M, N, copies.shape[0], workspace_buf.data_ptr(),
+        workspace_buf.nbytes, _maybe(status, "status", i32), _raw_stream(stream, block_table))
+    if code:
+        _check(code, "dspark_paged_compact")
+
+
+class PagedCaches:
+    """The caches of some layers as paged_copy takes them: pairs (k_cache, v_cache) of one
+    shape, dtype and strides."""
+
+    def __init__(self, caches):
+        self.tensors = [(k, v) for k, v in caches]  # (kept alive)
+        self.array = (PagedKv * len(self.tensors))()
+        for i, (k, v) in enumerate(self.tensors):
+            kv, _, _ = _paged_kv(k, v, None, None)
+            ctypes.pointer(self.array[i])[0] = kv
+
+
+def paged_copy(caches, copies, count, status=None, stream=None):
+    """dspark_paged_copy on torch tensors (see include/dspark.h): blocks copied in all
+    caches, a list of pairs (k_cache, v_cache) or a PagedCaches of them, by the pairs
+    (from, to) that paged_fork and paged_compact leave in copies [C, 2] and count [1]."""
+    if not isinstance(caches, PagedCaches):
+        caches = PagedCaches(caches)
+    i32 = torch.int32
+    _here(copies, "copies")
+    code = (_lib or lib()).dspark_paged_copy(
+        caches.array, len(caches.tensors), _of(copies, "copies", i32, (copies.shape[0], 2)),
+        _of(count, "count", i32, (1,)), copies.shape[0], _maybe(status, "status", i32),
+        _raw_stream(stream, copies))
+    if code:
+        _check(code, "dspark_paged_copy")
 
 
 def kv_append(k, v, k_cache, v_cache, slot_map, k_scale=None, v_scale=None, status=None,

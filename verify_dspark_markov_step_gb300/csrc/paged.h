@@ -24,10 +24,68 @@ struct PagedTablesParams {
   int32_t* seq_lens;
   int64_t* positions;
   int64_t* slot_map;
+  const int32_t* shares;  // [N] or null
   int B, S, M, N, T, page_shift;
   int32_t* status;
 };
 cudaError_t launch_paged_tables(const PagedTablesParams& p, cudaStream_t stream);
+
+// Forking, freeing and compacting the block tables, copying blocks (paged_blocks.cu).
+struct PagedForkParams {
+  const int32_t* src;
+  const int32_t* dst;
+  int32_t* cached_lens;
+  int32_t* block_table;
+  int32_t* held_blocks;
+  const int32_t* free_blocks;
+  int32_t* pool;
+  int32_t* shares;  // or null
+  int2* copies;
+  int32_t* count;
+  int n, S, M, N, C, page_shift;
+  int32_t* status;
+};
+cudaError_t launch_paged_fork(const PagedForkParams& p, cudaStream_t stream);
+
+struct PagedFreeParams {
+  const int32_t* slots;
+  int32_t* cached_lens;
+  int32_t* block_table;
+  int32_t* held_blocks;
+  int32_t* free_blocks;
+  int32_t* pool;
+  int32_t* shares;  // or null
+  int n, S, M, N;
+  int32_t* status;
+};
+cudaError_t launch_paged_free(const PagedFreeParams& p, cudaStream_t stream);
+
+struct PagedCompactParams {
+  int32_t* block_table;
+  const int32_t* held_blocks;
+  int32_t* free_blocks;
+  int32_t* pool;
+  int32_t* shares;  // or null
+  int2* copies;
+  int32_t* count;
+  int32_t* moved;   // [N] scratch
+  int S, M, N;
+  int32_t* status;
+};
+cudaError_t launch_paged_compact(const PagedCompactParams& p, cudaStream_t stream);
+
+constexpr int kCopyCaches = 64;  // layers of one launch
+struct PagedCopyParams {
+  uint8_t* base[2 * kCopyCaches];  // keys and values of each layer
+  int64_t block_bytes[2], head_bytes[2], token_bytes[2];
+  const int2* copies;
+  const int32_t* count;
+  int C, num_blocks, caches;
+  int pieces;                // 16-byte pieces of a block
+  int row_shift, page_shift; // pieces of a token's row, tokens of a block (log2)
+  int32_t* status;
+};
+cudaError_t launch_paged_copy(const PagedCopyParams& p, cudaStream_t stream);
 
 // Keys and values of new tokens into their pages (kv_append.cu).
 struct KvAppendParams {

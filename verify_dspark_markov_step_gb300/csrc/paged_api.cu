@@ -12,6 +12,14 @@ namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+// Sizes that the calls on the tables' blocks share.
+bool blocks_ok(int n, int S, int M, int N) {
+  return n >= 0 && n <= DSPARK_MAX_PAGED_BATCH && S >= 1 && M >= 1 && M <= 1 << 20 && N >= 1 &&
+         N < 1 << 30;
+}
+
 bool half_dtype(int d) { return d == DSPARK_BF16 || d == DSPARK_F16; }
 
 // log2 of a page size the library takes, or -1.
@@ -82,13 +90,12 @@ dspark::QkRopeParams rotation_params(const int64_t* positions, const uint64_t* t
 
 extern "C" {
 
-dspark_status dspark_paged_tables(const int32_t* req_state_idx, const int32_t* new_lens,
-                                  int32_t* cached_lens, const int32_t* num_accepted,
-                                  int32_t* block_table, int32_t* held_blocks,
-                                  int32_t* free_blocks, int32_t* pool, int32_t* query_start,
-                                  int32_t* seq_lens, int64_t* positions, int64_t* slot_map, int B,
-                                  int S, int M, int N, int T, int page_size, int32_t* status,
-                                  dspark_stream_t stream) {
+dspark_status dspark_paged_tables_shared(
+    const int32_t* req_state_idx, const int32_t* new_lens, int32_t* cached_lens,
+    const int32_t* num_accepted, int32_t* block_table, int32_t* held_blocks, int32_t* free_blocks,
+    int32_t* pool, const int32_t* shares, int32_t* query_start, int32_t* seq_lens,
+    int64_t* positions, int64_t* slot_map, int B, int S, int M, int N, int T, int page_size,
+    int32_t* status, dspark_stream_t stream) {
   if (B < 0 || B > DSPARK_MAX_PAGED_BATCH || S < 1 || M < 1 || M > 1 << 20 || N < 1 ||
       N >= 1 << 30 || T < 0 || T >= 1 << 30)
     return DSPARK_ERR_INVALID_ARG;
@@ -111,6 +118,7 @@ dspark_status dspark_paged_tables(const int32_t* req_state_idx, const int32_t* n
   p.seq_lens = seq_lens;
   p.positions = positions;
   p.slot_map = slot_map;
+  p.shares = shares;
   p.B = B;
   p.S = S;
   p.M = M;
@@ -120,6 +128,167 @@ dspark_status dspark_paged_tables(const int32_t* req_state_idx, const int32_t* n
   p.status = status;
   if (dspark::launch_paged_tables(p, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
     return DSPARK_ERR_CUDA;
+  return DSPARK_OK;
+}
+
+dspark_status dspark_paged_tables(const int32_t* req_state_idx, const int32_t* new_lens,
+                                  int32_t* cached_lens, const int32_t* num_accepted,
+                                  int32_t* block_table, int32_t* held_blocks,
+                                  int32_t* free_blocks, int32_t* pool, int32_t* query_start,
+                                  int32_t* seq_lens, int64_t* positions, int64_t* slot_map, int B,
+                                  int S, int M, int N, int T, int page_size, int32_t* status,
+                                  dspark_stream_t stream) {
+  return dspark_paged_tables_shared(req_state_idx, new_lens, cached_lens, num_accepted, block_table,
+                                    held_blocks, free_blocks, pool, nullptr, query_start, seq_lens,
+                                    positions, slot_map, B, S, M, N, T, page_size, status, stream);
+}
+
+dspark_status dspark_paged_fork(const int32_t* src, const int32_t* dst, int32_t* cached_lens,
+                                int32_t* block_table, int32_t* held_blocks,
+                                const int32_t* free_blocks, int32_t* pool, int32_t* shares,
+                                int32_t* copies, int32_t* count, int n, int S, int M, int N,
+                                int max_copies, int page_size, int32_t* status,
+                                dspark_stream_t stream) {
+  if (!blocks_ok(n, S, M, N) || max_copies < 0 || max_copies >= 1 << 30)
+    return DSPARK_ERR_INVALID_ARG;
+  const int shift = page_shift_of(page_size);
+  if (shift < 0) return DSPARK_ERR_UNSUPPORTED;
+  if (!count || !pool) return DSPARK_ERR_INVALID_ARG;
+  if (n > 0 && (!src || !dst || !cached_lens || !block_table || !held_blocks || !free_blocks ||
+                (max_copies > 0 && !copies)))
+    return DSPARK_ERR_INVALID_ARG;
+  if (!aligned8(copies)) return DSPARK_ERR_ALIGNMENT;
+  dspark::PagedForkParams p;
+  p.src = src;
+  p.dst = dst;
+  p.cached_lens = cached_lens;
+  p.block_table = block_table;
+  p.held_blocks = held_blocks;
+  p.free_blocks = free_blocks;
+  p.pool = pool;
+  p.shares = shares;
+  p.copies = reinterpret_cast<int2*>(copies);
+  p.count = count;
+  p.n = n;
+  p.S = S;
+  p.M = M;
+  p.N = N;
+  p.C = max_copies;
+  p.page_shift = shift;
+  p.status = status;
+  if (dspark::launch_paged_fork(p, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return DSPARK_ERR_CUDA;
+  return DSPARK_OK;
+}
+
+dspark_status dspark_paged_free(const int32_t* slots, int32_t* cached_lens, int32_t* block_table,
+                                int32_t* held_blocks, int32_t* free_blocks, int32_t* pool,
+                                int32_t* shares, int n, int S, int M, int N, int32_t* status,
+                                dspark_stream_t stream) {
+  if (!blocks_ok(n, S, M, N)) return DSPARK_ERR_INVALID_ARG;
+  if (n == 0) return DSPARK_OK;
+  if (!slots || !cached_lens || !block_table || !held_blocks || !free_blocks || !pool)
+    return DSPARK_ERR_INVALID_ARG;
+  dspark::PagedFreeParams p;
+  p.slots = slots;
+  p.cached_lens = cached_lens;
+  p.block_table = block_table;
+  p.held_blocks = held_blocks;
+  p.free_blocks = free_blocks;
+  p.pool = pool;
+  p.shares = shares;
+  p.n = n;
+  p.S = S;
+  p.M = M;
+  p.N = N;
+  p.status = status;
+  if (dspark::launch_paged_free(p, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return DSPARK_ERR_CUDA;
+  return DSPARK_OK;
+}
+
+size_t dspark_paged_compact_workspace_bytes(int N) {
+  return N < 1 ? 0 : (static_cast<size_t>(N) * 4 + 255) & ~size_t(255);
+}
+
+dspark_status dspark_paged_compact(int32_t* block_table, const int32_t* held_blocks,
+                                   int32_t* free_blocks, int32_t* pool, int32_t* shares,
+                                   int32_t* copies, int32_t* count, int S, int M, int N,
+                                   int max_copies, void* workspace, size_t workspace_bytes,
+                                   int32_t* status, dspark_stream_t stream) {
+  if (!blocks_ok(0, S, M, N) || max_copies < N / 2 || max_copies >= 1 << 30)
+    return DSPARK_ERR_INVALID_ARG;
+  if (!block_table || !held_blocks || !free_blocks || !pool || !count || (N > 1 && !copies))
+    return DSPARK_ERR_INVALID_ARG;
+  if (!aligned8(copies)) return DSPARK_ERR_ALIGNMENT;
+  if (!workspace || workspace_bytes < dspark_paged_compact_workspace_bytes(N) ||
+      !aligned16(workspace))
+    return DSPARK_ERR_WORKSPACE;
+  dspark::PagedCompactParams p;
+  p.block_table = block_table;
+  p.held_blocks = held_blocks;
+  p.free_blocks = free_blocks;
+  p.pool = pool;
+  p.shares = shares;
+  p.copies = reinterpret_cast<int2*>(copies);
+  p.count = count;
+  p.moved = static_cast<int32_t*>(workspace);
+  p.S = S;
+  p.M = M;
+  p.N = N;
+  p.status = status;
+  if (dspark::launch_paged_compact(p, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return DSPARK_ERR_CUDA;
+  return DSPARK_OK;
+}
+
+dspark_status dspark_paged_copy(const dspark_paged_kv* caches, int n_caches, const int32_t* copies,
+                                const int32_t* count, int max_copies, int32_t* status,
+                                dspark_stream_t stream) {
+  if (n_caches < 0 || n_caches > 1 << 16 || max_copies < 0 || max_copies >= 1 << 30)
+    return DSPARK_ERR_INVALID_ARG;
+  if (n_caches > 0 && !caches) return DSPARK_ERR_INVALID_ARG;
+  for (int i = 0; i < n_caches; ++i) {
+    const dspark_paged_kv& c = caches[i];
+    const dspark_status bad = check_cache(&c, c.dtype == DSPARK_E4M3 ? DSPARK_BF16 : c.dtype);
+    if (bad != DSPARK_OK) return bad;
+    const dspark_paged_kv& o = caches[0];
+    if (c.dtype != o.dtype || c.num_blocks != o.num_blocks || c.kv_heads != o.kv_heads ||
+        c.page_size != o.page_size || c.head_dim != o.head_dim ||
+        c.k_block_stride != o.k_block_stride || c.k_head_stride != o.k_head_stride ||
+        c.k_token_stride != o.k_token_stride || c.v_block_stride != o.v_block_stride ||
+        c.v_head_stride != o.v_head_stride || c.v_token_stride != o.v_token_stride)
+      return DSPARK_ERR_UNSUPPORTED;
+  }
+  if (n_caches == 0 || max_copies == 0) return DSPARK_OK;
+  if (!copies || !count) return DSPARK_ERR_INVALID_ARG;
+  if (!aligned8(copies)) return DSPARK_ERR_ALIGNMENT;
+  const dspark_paged_kv& o = caches[0];
+  const int64_t es = o.dtype == DSPARK_E4M3 ? 1 : 2;
+  dspark::PagedCopyParams p;
+  p.block_bytes[0] = o.k_block_stride * es;
+  p.block_bytes[1] = o.v_block_stride * es;
+  p.head_bytes[0] = o.k_head_stride * es;
+  p.head_bytes[1] = o.v_head_stride * es;
+  p.token_bytes[0] = o.k_token_stride * es;
+  p.token_bytes[1] = o.v_token_stride * es;
+  p.copies = reinterpret_cast<const int2*>(copies);
+  p.count = count;
+  p.C = max_copies;
+  p.num_blocks = o.num_blocks;
+  p.page_shift = page_shift_of(o.page_size);
+  p.row_shift = (o.head_dim == 128 ? 3 : 2) + (es == 2 ? 1 : 0);
+  p.pieces = (o.kv_heads << p.page_shift) << p.row_shift;
+  p.status = status;
+  for (int first = 0; first < n_caches; first += dspark::kCopyCaches) {
+    p.caches = n_caches - first < dspark::kCopyCaches ? n_caches - first : dspark::kCopyCaches;
+    for (int i = 0; i < p.caches; ++i) {
+      p.base[2 * i] = static_cast<uint8_t*>(caches[first + i].k);
+      p.base[2 * i + 1] = static_cast<uint8_t*>(caches[first + i].v);
+    }
+    if (dspark::launch_paged_copy(p, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+      return DSPARK_ERR_CUDA;
+  }
   return DSPARK_OK;
 }
 

@@ -1,0 +1,500 @@
+// paged_blocks.cu -- the upkeep of the paged cache: slots forked and freed, the
+// blocks compacted, and blocks copied in all layers.
+//
+// The table calls are prefix sums over the call's slots and then independent work
+// per block of them, as for the step's tables (paged_tables.cu), with two
+// differences. A block that several rows hold is counted (`shares`: the rows beyond
+// the first), and whether a block comes free is only known once every row of the call
+// has given it up; and compaction renumbers all blocks. Both are a few phases over
+// the same data with a barrier between them: one launch of one cluster of CTAs (a
+// single CTA where there is little to do), whose barrier is the hardware's.
+//
+// Which row puts a shared block on the stack must not depend on timing: after all
+// rows of the call have taken their share off the count, each of a block that came
+// out below zero lowers it further to -2 - (its place in the call); the lowest, the
+// last request, wins and pushes the block.
+//
+// Copies are bound by memory, the table calls by latency.
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "block_scan.cuh"
+#include "common.cuh"
+#include "paged.h"
+
+namespace dspark {
+
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxN = DSPARK_MAX_PAGED_BATCH;
+constexpr int kCluster = 8;
+// Up to this many table entries a single CTA does them all: a cluster's barriers cost
+// more than its threads gain.
+constexpr int kFewEntries = 4096;
+static_assert(kMaxN <= kThreads, "a slot per thread");
+
+// The last b < n with start[b] <= e.
+__device__ __forceinline__ int find(const int* start, int n, int e) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (start[mid] <= e)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+// The sum over the cluster's CTAs of `mine`, and of those before this one.
+__device__ __forceinline__ int cluster_sum(cg::cluster_group& cl, int* shared, int mine,
+                                           int* before) {
+  if (threadIdx.x == 0) *shared = mine;
+  cl.sync();
+  int total = 0, first = 0;
+  const int rank = static_cast<int>(cl.block_rank()), size = static_cast<int>(cl.num_blocks());
+  for (int c = 0; c < size; ++c) {
+    const int v = *cl.map_shared_rank(shared, c);
+    if (c < rank) first += v;
+    total += v;
+  }
+  cl.sync();  // read by all
+  *before = first;
+  return total;
+}
+
+__device__ __forceinline__ int pool_count(const int32_t* pool, int N, bool tell, int32_t* status) {
+  const int count = pool[0];
+  if (count >= 0 && count <= N) return count;
+  if (tell) report(status, DSPARK_ERR_BOUNDS);
+  return count < 0 ? 0 : N;
+}
+
+struct ForkSmem {
+  unsigned long long warp[33];
+  int src[kMaxN], dst[kMaxN];
+  int start[kMaxN + 1];  // first entry of each fork
+  int keep[kMaxN];       // shared blocks
+  int take0[kMaxN];      // blocks taken by the forks before
+};
+
+__global__ void __launch_bounds__(kThreads, 1) paged_fork_kernel(PagedForkParams P) {
+  __shared__ ForkSmem sm;
+  cg::cluster_group cl = cg::this_cluster();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int tid = threadIdx.x, rank = static_cast<int>(cl.block_rank());
+  const int size = static_cast<int>(cl.num_blocks());
+  const bool first = rank == 0;  // reports errors
+  const int M = P.M, N = P.N, sh = P.page_shift;
+  const int count = pool_count(P.pool, N, first && tid == 0, P.status);
+
+  int src = -1, dst = -1;
+  if (tid < P.n) {
+    src = P.src[tid];
+    dst = P.dst[tid];
+    if (src < 0 || dst < 0) src = dst = -1;
+    sm.src[tid] = src;
+    sm.dst[tid] = dst;
+  }
+  __syncthreads();
+  bool ok = false;
+  int len = 0, need = 0, keep = 0;
+  if (src >= 0) {
+    bool bad = src >= P.S || dst >= P.S;
+    if (!bad) {
+      len = P.cached_lens[src];
+      const int held = P.held_blocks[src];
+      need = static_cast<int>((static_cast<int64_t>(len) + (1 << sh) - 1) >> sh);
+      bad = len < 0 || held > M || need > held || P.held_blocks[dst] != 0;
+      for (int j = 0; j < P.n; ++j)
+        bad |= sm.dst[j] == src || (j < tid && sm.dst[j] == dst);
+    }
+    ok = !bad;
+    if (bad && first) report(P.status, DSPARK_ERR_BOUNDS);
+    if (!ok) need = 0;
+    keep = P.shares ? (ok ? len >> sh : 0) : 0;
+  }
+  unsigned long long total;
+  int take = need - keep;
+  const unsigned long long taken = block_scan(static_cast<unsigned int>(take), sm.warp, &total);
+  if (ok && take > 0) {
+    if (taken > static_cast<unsigned long long>(count)) {
+      ok = false;
+      if (first) report(P.status, DSPARK_ERR_CACHE_FULL);
+    } else if (taken > static_cast<unsigned long long>(P.C)) {
+      ok = false;
+      if (first) report(P.status, DSPARK_ERR_BOUNDS);
+    }
+  }
+  if (!ok) need = take = 0;
+  const unsigned long long ends = block_scan(
+      (static_cast<unsigned long long>(need) << 32) | static_cast<unsigned int>(take), sm.warp,
+      &total);
+  const int entries = static_cast<int>(total >> 32), all = static_cast<int>(total);
+  if (tid < P.n) {
+    sm.start[tid] = static_cast<int>(ends >> 32) - need;
+    sm.keep[tid] = keep;
+    sm.take0[tid] = static_cast<int>(static_cast<unsigned int>(ends)) - take;
+  }
+  __syncthreads();
+  for (int e = rank * kThreads + tid; e < entries; e += size * kThreads) {
+    const int i = find(sm.start, P.n, e), j = e - sm.start[i], k = j - sm.keep[i];
+    int id = P.block_table[static_cast<int64_t>(sm.src[i]) * M + j];
+    const bool there = id >= 0 && id < N;
+    if (!there) report(P.status, DSPARK_ERR_BOUNDS);
+    if (k < 0) {
+      if (there) atomicAdd(P.shares + id, 1);
+    } else {
+      const int at = sm.take0[i] + k;
+      const int fresh = P.free_blocks[count - 1 - at];
+      P.copies[at] = make_int2(id, fresh);
+      id = fresh;
+    }
+    P.block_table[static_cast<int64_t>(sm.dst[i]) * M + j] = id;
+  }
+  cl.sync();  // every CTA has read the lengths and the pool
+  if (!first) return;
+  if (ok) {
+    P.held_blocks[dst] = need;
+    P.cached_lens[dst] = len;
+  }
+  if (tid == 0) {
+    P.pool[0] = count - all;
+    *P.count = all;
+  }
+}
+
+struct FreeSmem {
+  unsigned long long warp[33];
+  int slot[kMaxN];
+  int start[kMaxN + 1];
+  int sums[kWarps];
+  int shared;
+};
+
+__global__ void __launch_bounds__(kThreads, 1) paged_free_kernel(PagedFreeParams P) {
+  __shared__ FreeSmem sm;
+  cg::cluster_group cl = cg::this_cluster();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = static_cast<int>(cl.block_rank()), size = static_cast<int>(cl.num_blocks());
+  const bool first = rank == 0;
+  const int M = P.M, N = P.N;
+  const int count = pool_count(P.pool, N, first && tid == 0, P.status);
+  int slot = -1, held = 0;
+  if (tid < P.n) sm.slot[tid] = slot = P.slots[tid];
+  __syncthreads();
+  if (slot >= 0) {
+    bool bad = slot >= P.S;
+    for (int j = 0; j < tid; ++j) bad |= sm.slot[j] == slot;
+    if (!bad) {
+      held = P.held_blocks[slot];
+      bad = held < 0 || held > M;
+    }
+    if (bad) {
+      if (first) report(P.status, DSPARK_ERR_BOUNDS);
+      slot = -1;
+      held = 0;
+    }
+  }
+  unsigned long long total;
+  const unsigned long long ends = block_scan(static_cast<unsigned int>(held), sm.warp, &total);
+  if (tid < P.n) sm.start[tid] = static_cast<int>(ends) - held;
+  const int entries = static_cast<int>(total);
+  __syncthreads();
+
+  // the entries of this CTA, and of this warp
+  const int each = (entries + size - 1) / size, per = ((each + kWarps - 1) / kWarps + 31) & ~31;
+  const int w0 = min(rank * each + warp * per, entries);
+  const int w1 = min(min(rank * each + min((warp + 1) * per, each), entries), entries);
+  auto entry = [&](int e, int& i) -> int32_t* {
+    i = find(sm.start, P.n, e);
+    return P.block_table + static_cast<int64_t>(sm.slot[i]) * M + (e - sm.start[i]);
+  };
+  if (P.shares) {
+    for (int e = w0 + lane; e < w1; e += 32) {
+      int i;
+      const int id = *entry(e, i);
+      if (id >= 0 && id < N) atomicSub(P.shares + id, 1);
+    }
+    cl.sync();
+    for (int e = w0 + lane; e < w1; e += 32) {
+      int i;
+      const int id = *entry(e, i);
+      if (id >= 0 && id < N && __ldcg(P.shares + id) < 0) atomicMin(P.shares + id, -2 - i);
+    }
+    cl.sync();
+  }
+  // whether entry e puts its block on the stack
+  auto pushes = [&](int id, int i) -> bool {
+    if (id < 0 || id >= N) return false;
+    return !P.shares || __ldcg(P.shares + id) == -2 - i;
+  };
+  int mine = 0;  // of this warp
+  for (int e = w0 + lane; e - lane < w1; e += 32) {
+    bool push = false;
+    if (e < w1) {
+      int i;
+      const int id = *entry(e, i);
+      if (id < 0 || id >= N) report(P.status, DSPARK_ERR_BOUNDS);
+      push = pushes(id, i);
+    }
+    mine += __popc(__ballot_sync(0xFFFFFFFFu, push));
+  }
+  if (lane == 0) sm.sums[warp] = mine;
+  __syncthreads();
+  int ahead = 0, all = 0;  // of the warps before, of the CTA
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) ahead += sm.sums[w];
+    all += sm.sums[w];
+  }
+  int before;
+  const int pushed = cluster_sum(cl, &sm.shared, all, &before);
+  int r = before + ahead;
+  for (int e = w0 + lane; e - lane < w1; e += 32) {
+    bool push = false;
+    int id = -1;
+    if (e < w1) {
+      int i;
+      int32_t* at = entry(e, i);
+      id = *at;
+      push = pushes(id, i);
+      *at = -1;
+    }
+    const unsigned int who = __ballot_sync(0xFFFFFFFFu, push);
+    if (push) {
+      const int64_t at = static_cast<int64_t>(count) + pushed - 1 -
+                         (r + __popc(who & ((1u << lane) - 1u)));
+      if (at < N) P.free_blocks[at] = id;
+      if (P.shares) P.shares[id] = 0;
+    }
+    r += __popc(who);
+  }
+  if (!first) return;
+  if (slot >= 0) {  // (the lengths were read before the cluster's last barrier)
+    P.held_blocks[slot] = 0;
+    P.cached_lens[slot] = 0;
+  }
+  if (tid == 0) {
+    const int64_t left = static_cast<int64_t>(count) + pushed;
+    if (left > N) report(P.status, DSPARK_ERR_BOUNDS);
+    P.pool[0] = static_cast<int>(left > N ? N : left);
+  }
+}
+
+// With U blocks held, the held ones from U on ("movers") go to the free ones below
+// ("holes"), of which there are as many, in ascending order.
+__global__ void __launch_bounds__(kThreads, 1) paged_compact_kernel(PagedCompactParams P) {
+  __shared__ int sums[2][kWarps];
+  __shared__ int shared[2];
+  cg::cluster_group cl = cg::this_cluster();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = static_cast<int>(cl.block_rank()), size = static_cast<int>(cl.num_blocks());
+  const bool first = rank == 0;
+  const int M = P.M, N = P.N, all = size * kThreads, me = rank * kThreads + tid;
+  const int count = pool_count(P.pool, N, first && tid == 0, P.status);
+
+  // moved[id]: -1 for a free block, 0 for a held one, 1 + its new number for a mover
+  for (int i = me; i < N; i += all) P.moved[i] = 0;
+  cl.sync();
+  int found = 0;
+  for (int i = me; i < count; i += all) {
+    const int id = P.free_blocks[i];
+    if (id >= 0 && id < N)
+      found += atomicExch(P.moved + id, -1) == 0;
+    else
+      report(P.status, DSPARK_ERR_BOUNDS);
+  }
+  found = __reduce_add_sync(0xFFFFFFFFu, found);
+  if (lane == 0) sums[0][warp] = found;
+  __syncthreads();
+  found = 0;
+  for (int w = 0; w < kWarps; ++w) found += sums[0][w];
+  int unused;
+  const int U = N - cluster_sum(cl, &shared[0], found, &unused);
+
+  // ranks of holes and movers: each warp a run of blocks
+  const int64_t each = (static_cast<int64_t>(N) + size - 1) / size;
+  const int64_t per = ((each + kWarps - 1) / kWarps + 31) & ~int64_t(31);
+  const int w0 = static_cast<int>(min(rank * each + warp * per, static_cast<int64_t>(N)));
+  const int w1 = static_cast<int>(
+      min(rank * each + min((warp + 1) * per, each), static_cast<int64_t>(N)));
+  int n_hole = 0, n_mover = 0;
+  for (int i = w0 + lane; i - lane < w1; i += 32) {
+    const int v = i < w1 ? __ldcg(P.moved + i) : 0;
+    n_hole += __popc(__ballot_sync(0xFFFFFFFFu, i < w1 && i < U && v != 0));
+    n_mover += __popc(__ballot_sync(0xFFFFFFFFu, i < w1 && i >= U && v == 0));
+  }
+  if (lane == 0) {
+    sums[0][warp] = n_hole;
+    sums[1][warp] = n_mover;
+  }
+  __syncthreads();
+  int hole = 0, mover = 0, holes = 0, movers = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) {
+      hole += sums[0][w];
+      mover += sums[1][w];
+    }
+    holes += sums[0][w];
+    movers += sums[1][w];
+  }
+  int hole0, mover0;
+  const int moves = cluster_sum(cl, &shared[0], holes, &hole0);
+  cluster_sum(cl, &shared[1], movers, &mover0);
+  hole += hole0;
+  mover += mover0;
+  for (int i = w0 + lane; i - lane < w1; i += 32) {
+    const int v = i < w1 ? __ldcg(P.moved + i) : 0;
+    const bool is_hole = i < w1 && i < U && v != 0, is_mover = i < w1 && i >= U && v == 0;
+    const unsigned int who = __ballot_sync(0xFFFFFFFFu, is_hole);
+    const unsigned int which = __ballot_sync(0xFFFFFFFFu, is_mover);
+    const unsigned int below = (1u << lane) - 1u;
+    if (is_hole) P.copies[hole + __popc(who & below)].y = i;
+    if (is_mover) P.copies[mover + __popc(which & below)].x = i;
+    hole += __popc(who);
+    mover += __popc(which);
+  }
+  cl.sync();
+  for (int i = me; i < moves; i += all) {
+    const int from = __ldcg(&P.copies[i].x), to = __ldcg(&P.copies[i].y);
+    P.moved[from] = to + 1;
+    if (P.shares) {
+      P.shares[to] = P.shares[from];
+      P.shares[from] = 0;
+    }
+  }
+  cl.sync();
+  for (int s = rank * kWarps + warp; s < P.S; s += size * kWarps) {
+    int held = P.held_blocks[s];
+    if (held < 0 || held > M) {
+      if (lane == 0) report(P.status, DSPARK_ERR_BOUNDS);
+      held = held < 0 ? 0 : M;
+    }
+    int32_t* row = P.block_table + static_cast<int64_t>(s) * M;
+    for (int j = lane; j < held; j += 32) {
+      const int id = row[j];
+      const int to = id >= U && id < N ? __ldcg(P.moved + id) : id >= 0 && id < U ? id + 1 : 0;
+      if (to > 0)
+        row[j] = to - 1;
+      else
+        report(P.status, DSPARK_ERR_BOUNDS);
+    }
+  }
+  for (int i = me; i < N - U; i += all) P.free_blocks[i] = N - 1 - i;
+  if (first && tid == 0) {
+    P.pool[0] = N - U;
+    *P.count = moves;
+  }
+}
+
+// ---- copies ------------------------------------------------------------------------
+constexpr int kCopyThreads = 256, kCopyEach = 4;  // 16-byte pieces a thread holds
+
+// blockIdx.y: keys or values of a layer; blockIdx.x takes chunks of the copies in turn.
+__global__ void __launch_bounds__(kCopyThreads) paged_copy_kernel(PagedCopyParams P) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int which = blockIdx.y & 1;
+  uint8_t* base = P.base[blockIdx.y];
+  int n = *P.count;
+  if (n < 0 || n > P.C) {
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) report(P.status, DSPARK_ERR_BOUNDS);
+    n = n < 0 ? 0 : P.C;
+  }
+  constexpr int kChunk = kCopyThreads * kCopyEach;
+  const int chunks = (P.pieces + kChunk - 1) / kChunk;
+  const int step_n = gridDim.x / chunks, step_c = gridDim.x - step_n * chunks;
+  int i = blockIdx.x / chunks, c = blockIdx.x - i * chunks;
+  while (i < n) {
+    const int2 move = P.copies[i];
+    if (move.x >= 0 && move.x < P.num_blocks && move.y >= 0 && move.y < P.num_blocks) {
+      const uint8_t* from = base + move.x * P.block_bytes[which];
+      uint8_t* to = base + move.y * P.block_bytes[which];
+      uint4 x[kCopyEach];
+      int64_t at[kCopyEach];
+#pragma unroll
+      for (int k = 0; k < kCopyEach; ++k) {
+        const int u = c * kChunk + k * kCopyThreads + threadIdx.x;
+        const int row = u >> P.row_shift;
+        at[k] = (row >> P.page_shift) * P.head_bytes[which] +
+                (row & ((1 << P.page_shift) - 1)) * P.token_bytes[which] +
+                ((u & ((1 << P.row_shift) - 1)) << 4);
+        if (u < P.pieces) x[k] = *reinterpret_cast<const uint4*>(from + at[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < kCopyEach; ++k)
+        if (c * kChunk + k * kCopyThreads + threadIdx.x < P.pieces)
+          *reinterpret_cast<uint4*>(to + at[k]) = x[k];
+    } else if (threadIdx.x == 0) {
+      report(P.status, DSPARK_ERR_BOUNDS);
+    }
+    i += step_n;
+    c += step_c;
+    if (c >= chunks) {
+      c -= chunks;
+      ++i;
+    }
+  }
+}
+
+// One cluster of `ctas` CTAs, which may be set up while the kernel before it ends.
+template <typename Params>
+cudaError_t launch_cluster(void (*kernel)(Params), const Params& p, int ctas, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_fork(const PagedForkParams& p, cudaStream_t stream) {
+  const int64_t entries = static_cast<int64_t>(p.n) * p.M;
+  return launch_cluster(paged_fork_kernel, p, entries <= kFewEntries ? 1 : kCluster, stream);
+}
+
+cudaError_t launch_paged_free(const PagedFreeParams& p, cudaStream_t stream) {
+  const int64_t entries = static_cast<int64_t>(p.n) * p.M;
+  return launch_cluster(paged_free_kernel, p, entries <= kFewEntries ? 1 : kCluster, stream);
+}
+
+cudaError_t launch_paged_compact(const PagedCompactParams& p, cudaStream_t stream) {
+  const int64_t entries = static_cast<int64_t>(p.S) * p.M + p.N;
+  return launch_cluster(paged_compact_kernel, p, entries <= kFewEntries ? 1 : kCluster, stream);
+}
+
+cudaError_t launch_paged_copy(const PagedCopyParams& p, cudaStream_t stream) {
+  // eight CTAs an SM over all layers, keys and values
+  int ctas = (152 * 8 + 2 * p.caches - 1) / (2 * p.caches);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, 2 * p.caches);
+  cfg.blockDim = dim3(kCopyThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_copy_kernel, p);
+}
+
+}  // namespace dspark

@@ -24,6 +24,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "block_scan.cuh"
 #include "common.cuh"
 #include "paged.h"
 
@@ -47,34 +48,6 @@ struct TablesSmem {
   int after[kMaxB];       // blocks returned by the requests after
   int last;
 };
-
-// Inclusive prefix sum over the block's threads.
-__device__ unsigned long long block_scan(unsigned long long v, unsigned long long* s_warp,
-                                         unsigned long long* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long u = __shfl_up_sync(0xFFFFFFFFu, v, o);
-    if (lane >= o) v += u;
-  }
-  if (lane == 31) s_warp[warp] = v;
-  __syncthreads();
-  if (warp == 0) {
-    const int nw = blockDim.x >> 5;
-    unsigned long long w = lane < nw ? s_warp[lane] : 0ull;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long u = __shfl_up_sync(0xFFFFFFFFu, w, o);
-      if (lane >= o) w += u;
-    }
-    s_warp[lane] = w;
-  }
-  __syncthreads();
-  if (warp > 0) v += s_warp[warp - 1];
-  *total = s_warp[(blockDim.x >> 5) - 1];
-  __syncthreads();  // s_warp is free again
-  return v;
-}
 
 __global__ void __launch_bounds__(1024) paged_tables_kernel(PagedTablesParams P) {
   __shared__ TablesSmem sm;
@@ -105,6 +78,12 @@ __global__ void __launch_bounds__(1024) paged_tables_kernel(PagedTablesParams P)
         cached = static_cast<int64_t>(c) + acc + 1;
         need = (cached + fresh + (1 << sh) - 1) >> sh;
         ok = acc >= -1 && c >= 0 && fresh >= 0 && held >= 0 && held <= M && need <= M;
+        // a block that other rows hold too is not this call's to put on the stack
+        if (P.shares && ok)
+          for (int j = static_cast<int>(need); j < held; ++j) {
+            const int id = P.block_table[static_cast<int64_t>(slot) * M + j];
+            if (id >= 0 && id < N && P.shares[id] > 0) ok = false;
+          }
       }
       if (!ok && first) report(P.status, DSPARK_ERR_BOUNDS);
     }
