@@ -599,7 +599,8 @@ dspark_status dspark_qk_rope_append(
  * its n rows are the last n of its seq_lens[b] tokens, so row i has position
  * P_i = seq_lens[b] - n + i. Query head hq reads the keys and values of head
  * h = hq / (q_heads / kv_heads). Row i sees the key at position j if
- *   0 <= j < seq_lens[b],  j <= P_i (causal),  j > P_i - window (window > 0):
+ *   0 <= j < seq_lens[b],  j <= P_i (causal),
+ *   j > P_i - window or j < sinks (window > 0; sinks = 0 without the argument):
  *   x_j = scale * k_scale[h] * sum_d q[t, hq, d] k[j, h, d]       (fp32)
  *   lse[t, hq] = log sum_j exp(x_j)
  *   out[t, hq, :] = v_scale[h] * sum_j exp(x_j - lse) v[j, h, :]
@@ -623,6 +624,9 @@ dspark_status dspark_qk_rope_append(
  *   query_start   [B+1] int32, seq_lens [B] int32
  *   q_heads       a multiple of kv_heads, at most 128 * kv_heads
  *   causal 0 or 1; window >= 0, 0 = none; scale finite
+ *   sinks         >= 0 first tokens that stay visible beside the window; without a
+ *                 window all tokens are, and sinks says nothing. Only pages that
+ *                 some row sees are read: the others' table entries may be -1.
  *   B in [0, 1024], S >= 1, M in [1, 2^20], T in [0, 2^24).
  *   workspace     at least dspark_paged_attention_workspace_bytes() bytes
  *                 (43 MB for head_dim 128, 22 MB for 64), 256-byte aligned, no
@@ -639,6 +643,15 @@ dspark_status dspark_paged_attention(
     const int32_t* seq_lens, void* out, float* lse, float scale, int causal,
     int window, int q_heads, int B, int S, int M, int T, void* workspace,
     size_t workspace_bytes, int32_t* status, dspark_stream_t stream);
+
+dspark_status dspark_paged_attention_sinks(
+    const void* q, dspark_dtype dtype, int64_t q_stride,
+    const dspark_paged_kv* cache, const int32_t* block_table,
+    const int32_t* req_state_idx, const int32_t* query_start,
+    const int32_t* seq_lens, void* out, float* lse, float scale, int causal,
+    int window, int sinks, int q_heads, int B, int S, int M, int T,
+    void* workspace, size_t workspace_bytes, int32_t* status,
+    dspark_stream_t stream);
 
 /* Human-readable name of a status code (static storage; never NULL). */
 const char* dspark_status_string(int status);

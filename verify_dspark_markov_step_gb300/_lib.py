@@ -59,6 +59,7 @@ EXPORTS = (
     "dspark_qk_rope_append",
     "dspark_paged_attention_workspace_bytes",
     "dspark_paged_attention",
+    "dspark_paged_attention_sinks",
     "dspark_status_string",
     "dspark_version",
 )
@@ -155,6 +156,10 @@ def lib(path: str | None = None) -> ctypes.CDLL:
         L.dspark_paged_attention.argtypes = [vp, i32, i64, kvp, vp, vp, vp, vp, vp, vp,
                                              ctypes.c_float, i32, i32, i32, i32, i32, i32, i32,
                                              vp, sz, vp, vp]
+        L.dspark_paged_attention_sinks.restype = i32
+        L.dspark_paged_attention_sinks.argtypes = [vp, i32, i64, kvp, vp, vp, vp, vp, vp, vp,
+                                                   f32, i32, i32, i32, i32, i32, i32, i32, i32,
+                                                   vp, sz, vp, vp]
         L.dspark_status_string.restype = ctypes.c_char_p
         L.dspark_status_string.argtypes = [i32]
         L.dspark_version.restype = i32
@@ -803,11 +808,12 @@ def paged_attention_workspace_bytes(B, q_heads, kv_heads, head_dim) -> int:
 
 def paged_attention(q, k_cache, v_cache, block_table, req_state_idx, query_start, seq_lens, out,
                     scale=None, causal=True, window=0, k_scale=None, v_scale=None, lse=None,
-                    workspace_buf=None, status=None, stream=None):
+                    workspace_buf=None, status=None, stream=None, sinks=0):
     """dspark_paged_attention on torch tensors (see include/dspark.h): the
     attention of rows q [T, q_heads, head_dim] (a view of a fused projection
     will do) over the caches, into out and, if given, lse [T, q_heads]. scale
-    is 1 / sqrt(head_dim) if not given."""
+    is 1 / sqrt(head_dim) if not given; sinks first tokens stay visible beside a
+    window."""
     cache, H, cd = _paged_kv(k_cache, v_cache, k_scale, v_scale)
     qp, dt, qs = _rows(q, "q")
     T, Hq, D = q.shape
@@ -822,12 +828,12 @@ def paged_attention(q, k_cache, v_cache, block_table, req_state_idx, query_start
             with torch.cuda.stream(stream):
                 workspace_buf = workspace(need, q.device)
     i32 = torch.int32
-    code = (_lib or lib()).dspark_paged_attention(
+    code = (_lib or lib()).dspark_paged_attention_sinks(
         qp, dt, qs, cache, _of(block_table, "block_table", i32),
         _of(req_state_idx, "req_state_idx", i32, (B,)),
         _of(query_start, "query_start", i32, (B + 1,)), _of(seq_lens, "seq_lens", i32, (B,)),
         _of(out, "out", q.dtype, q.shape), _maybe(lse, "lse", torch.float32, (T, Hq)),
-        D ** -0.5 if scale is None else scale, bool(causal), window, Hq, B, S, M, T,
+        D ** -0.5 if scale is None else scale, bool(causal), window, sinks, Hq, B, S, M, T,
         workspace_buf.data_ptr(), workspace_buf.nbytes, _maybe(status, "status", i32),
         _raw_stream(stream, q))
     if code:

@@ -137,6 +137,7 @@ struct PagedAttentionParams {
   float* lse;
   float scale;
   int causal, window;
+  int sinks;  // first tokens seen beside the window (0 without one)
   int dtype;
   int Hq, B, S, M, T, page_shift;
   int whole;  // no unit is split over CTAs (set at launch)

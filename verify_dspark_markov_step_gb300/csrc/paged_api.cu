@@ -437,10 +437,22 @@ dspark_status dspark_paged_attention(const void* q, dspark_dtype dtype, int64_t 
                                      int causal, int window, int q_heads, int B, int S, int M,
                                      int T, void* workspace, size_t workspace_bytes,
                                      int32_t* status, dspark_stream_t stream) {
+  return dspark_paged_attention_sinks(q, dtype, q_stride, cache, block_table, req_state_idx,
+                                      query_start, seq_lens, out, lse, scale, causal, window, 0,
+                                      q_heads, B, S, M, T, workspace, workspace_bytes, status,
+                                      stream);
+}
+
+dspark_status dspark_paged_attention_sinks(
+    const void* q, dspark_dtype dtype, int64_t q_stride, const dspark_paged_kv* cache,
+    const int32_t* block_table, const int32_t* req_state_idx, const int32_t* query_start,
+    const int32_t* seq_lens, void* out, float* lse, float scale, int causal, int window, int sinks,
+    int q_heads, int B, int S, int M, int T, void* workspace, size_t workspace_bytes,
+    int32_t* status, dspark_stream_t stream) {
   if (B < 0 || B > DSPARK_MAX_PAGED_BATCH || S < 1 || M < 1 || M > 1 << 20 || T < 0 ||
       T >= 1 << 24 || q_heads < 1)
     return DSPARK_ERR_INVALID_ARG;
-  if (!isfinite(scale) || (causal != 0 && causal != 1) || window < 0)
+  if (!isfinite(scale) || (causal != 0 && causal != 1) || window < 0 || sinks < 0)
     return DSPARK_ERR_INVALID_ARG;
   const dspark_status bad = check_cache(cache, dtype);
   if (bad != DSPARK_OK) return bad;
@@ -466,6 +478,7 @@ dspark_status dspark_paged_attention(const void* q, dspark_dtype dtype, int64_t 
   p.scale = scale;
   p.causal = causal;
   p.window = window > 1 << 28 ? 0 : window;  // longer than any cache
+  p.sinks = p.window == 0 ? 0 : sinks < 1 << 28 ? sinks : 1 << 28;
   p.dtype = dtype;
   p.Hq = q_heads;
   p.B = B;

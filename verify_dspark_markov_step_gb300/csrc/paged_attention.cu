@@ -50,6 +50,12 @@
 // fp16 by a power of two per row. Pages: a 128-key tile is 128 / page_size TMA
 // boxes.
 //
+// First tokens that stay visible beside a window ("sinks"): a unit's key tiles are
+// numbered on from the sinks' to the window's as if nothing lay between them, so the
+// split, the rings and the masks' cost are those of a window longer by the sinks, and
+// the tiles in between are never loaded. Kernels of their own, so that the others'
+// masks stay a single range.
+//
 // What a row does not see must not reach it: masked scores are replaced (not
 // added to), value rows past the request's last token are zeroed in shared
 // memory, and in tiles that some row sees only in part a non-finite value of a
@@ -483,18 +489,39 @@ __device__ __forceinline__ void key_range(const PagedAttentionParams& P, int n, 
   if (hi <= lo) lo = hi = 0;
 }
 
-// Key tiles of a unit; a unit whose rows see nothing still has one (empty) tile.
+// Tiles before the tile of `lo` that hold sinks; a unit's (or row's) range is [lo, hi).
+__device__ __forceinline__ int sink_tiles(const PagedAttentionParams& P, int lo, int hi) {
+  return min(lo / kKeys, (min(P.sinks, hi) + kKeys - 1) / kKeys);
+}
+
+// Key tiles of a unit; a unit whose rows see nothing still has one (empty) tile. With
+// sinks they start as many before the window's first as there are tiles of sinks.
+template <bool kSinks>
 __device__ __forceinline__ void unit_tiles(const PagedAttentionParams& P, const Request& r, int tp,
                                            int u, int& jb, int& je) {
   int lo, hi;
   key_range(P, r.n, r.len, u * 2 * tp, min(r.n, (u + 1) * 2 * tp), lo, hi);
   jb = lo / kKeys;
   je = max(jb + 1, (hi + kKeys - 1) / kKeys);
+  if constexpr (kSinks) jb -= sink_tiles(P, lo, hi);
+}
+
+// Where a segment's tiles are: those below `window` are sinks', numbered `gap` too high.
+struct Places {
+  int window, gap;
+  __device__ int real(int j) const { return j < window ? j - gap : j; }
+};
+__device__ __forceinline__ Places places_of(const PagedAttentionParams& P, int lo, int hi) {
+  Places p;
+  p.window = lo / kKeys;
+  p.gap = p.window - sink_tiles(P, lo, hi);
+  return p;
 }
 
 // The segments of this CTA in order. Positions count the units' costs from the
 // run's start: the first kUnitTiles places of a unit stand for no tile. Units that
 // start before `end` are this CTA's, up to `limit`.
+template <bool kSinks>
 struct Walk {
   const PagedAttentionParams& P;
   int tp, b, h, u, jb, je;
@@ -509,7 +536,7 @@ struct Walk {
     h = m->start_h;
     long long rem = m->start_rem;
     for (;; ++u) {
-      unit_tiles(P, r, tp, u, jb, je);
+      unit_tiles<kSinks>(P, r, tp, u, jb, je);
       if (rem < cost()) break;
       rem -= cost();
     }
@@ -532,7 +559,7 @@ struct Walk {
         } while (r.n == 0);
       }
     }
-    unit_tiles(P, r, tp, u, jb, je);
+    unit_tiles<kSinks>(P, r, tp, u, jb, je);
     v = 0;
   }
   __device__ bool next(Seg& s) {
@@ -572,7 +599,7 @@ struct Walk {
 
 // Where this CTA's run starts: the key tiles of every request summed up (one
 // request per thread, long prompts by whole warps), `pre` as scratch.
-template <int kThreads>
+template <int kThreads, bool kSinks>
 __device__ void make_plan(const PagedAttentionParams& P, Misc* m, unsigned long long* pre, int tp) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int B = P.B;
@@ -580,7 +607,7 @@ __device__ void make_plan(const PagedAttentionParams& P, Misc* m, unsigned long 
   unsigned int n_units = 0, least = 0xFFFFFFFFu, largest = 0;  // of units' costs
   auto count = [&](const Request& o, int u) -> unsigned int {
     int jb, je;
-    unit_tiles(P, o, tp, u, jb, je);
+    unit_tiles<kSinks>(P, o, tp, u, jb, je);
     const unsigned int c = je - jb + kUnitTiles;
     least = min(least, c);
     largest = max(largest, c);
@@ -692,8 +719,9 @@ __device__ void make_plan(const PagedAttentionParams& P, Misc* m, unsigned long 
 // ---- the kernel ----------------------------------------------------------------------
 // kF16: the MMA's type is fp16 (fp16 rows, or an 8-bit cache), else bf16. kScaled:
 // a 16-bit cache with key scales (apart, since the scale's sign in the issuer's
-// descriptor and its size in the softmax are 1 to 2% of a short request's time).
-template <int D, bool kF16, bool kQuant, bool kScaled>
+// descriptor and its size in the softmax are 1 to 2% of a short request's time). kSinks:
+// a window, and first tokens that stay visible.
+template <int D, bool kF16, bool kQuant, bool kScaled, bool kSinks>
 __global__ void __launch_bounds__(Cfg<D, kQuant>::kThreads, 1)
 paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                        const __grid_constant__ CUtensorMap tmap_k,
@@ -750,7 +778,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     tc::tmem_relinquish();
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  make_plan<C::kThreads>(P, m, reinterpret_cast<unsigned long long*>(smem + C::kv), tp);
+  make_plan<C::kThreads, kSinks>(P, m, reinterpret_cast<unsigned long long*>(smem + C::kv), tp);
   fence_proxy_async_smem();  // the plan's scratch is TMA's from here on
   tc::fence_before_thread_sync();
   __syncthreads();
@@ -816,11 +844,24 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
       const bool warp_live = (warp & 3) * 32 < nrow;
       int lo, hi;
       key_range(P, s.r.n, s.r.len, first + tok, first + tok + 1, lo, hi);
-      if (!live) lo = hi = 0;
+      int sk = 0, all_sk = 0;  // sinks that the row, and every row of the tile, sees
+      Places at{};
+      if constexpr (kSinks) {
+        sk = min(P.sinks, hi);
+        if (sk >= lo) lo = sk = 0;
+        int unit_lo, unit_hi;
+        key_range(P, s.r.n, s.r.len, s.t0, s.t1, unit_lo, unit_hi);
+        at = places_of(P, unit_lo, unit_hi);
+      }
+      if (!live) lo = hi = sk = 0;
       // keys seen by every row of the tile
       int all_lo, all_hi, unused;
       key_range(P, s.r.n, s.r.len, first, first + 1, unused, all_hi);
       key_range(P, s.r.n, s.r.len, first + ntok - 1, first + ntok, all_lo, unused);
+      if constexpr (kSinks) {
+        all_sk = min(P.sinks, all_hi);
+        if (all_sk >= all_lo) all_lo = all_sk = 0;
+      }
       if constexpr (kQuant) {
         // The row tile to fp16, in place, each row's largest value brought to 2^14
         // by a power of two: exact but for values 2^-28 below it. D / 8
@@ -873,7 +914,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
       if (kQuant || kScaled) sl = bounded(sl);
       float r = -INFINITY, l = 0.f;  // reference (a score, not scaled), sum
       for (int k = 0; k < items; ++k, ++n_item) {
-        const int key0 = s.tile(w, k) * kKeys;
+        const int key0 = (kSinks ? at.real(s.tile(w, k)) : s.tile(w, k)) * kKeys;
         if (!(ok = wait_warp(&m->s_full[w], n_item & 1, fail, P.status))) break;
         tc::fence_after_thread_sync();
         if (giver) {  // these scores are there: the keys, and the values before
@@ -889,6 +930,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
           // does not see
           tail = key0 + kKeys > s.r.len;
           scan = key0 < all_lo || min(key0 + kKeys, s.r.len) > all_hi;
+          if (kSinks && min(key0 + kKeys, s.r.len) <= all_sk) scan = false;
         }
         if (warp_live) {
           // (all 128 scores at once where the registers hold them, else 64 at a
@@ -904,7 +946,11 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
               for (int g = 0; g < kCols; g += 32) {  // bit c: the row sees key g + c
                 const int a = min(max(clo - g, 0), 32), z = min(max(chi - g, 0), 32);
                 const uint32_t below = z == 32 ? 0xFFFFFFFFu : (1u << z) - 1u;
-                const uint32_t sees = a == 32 ? 0u : below >> a << a;
+                uint32_t sees = a == 32 ? 0u : below >> a << a;
+                if constexpr (kSinks) {
+                  const int y = min(max(sk - key0 - c0 - g, 0), 32);
+                  sees |= y == 32 ? 0xFFFFFFFFu : (1u << y) - 1u;
+                }
 #pragma unroll
                 for (int c = 0; c < 32; ++c)
                   if (!(sees >> c & 1u)) x[g + c] = 0xFF800000u;
@@ -1014,7 +1060,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
             for (int c = 0; c < D / 8; ++c)
               *reinterpret_cast<uint4*>(v_s + (c >> 3) * (kKeys * 128) + row * 128 +
                                         (((c ^ row) & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
-          } else if (scan && (key >= all_hi || key < all_lo)) {
+          } else if (scan && (key >= all_hi || (key < all_lo && !(kSinks && key < all_sk)))) {
             constexpr uint32_t kInf = kF16 ? 0x7C00u : 0x7F80u;
             bool bad = false;
 #pragma unroll
@@ -1057,7 +1103,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     else
                       unpack_bf16(pw, p0, p1);
                     const float p = (c & 1) ? p1 : p0;
-                    const bool sees = key0 + c >= lo && key0 + c < hi;
+                    const bool sees =
+                        (key0 + c >= lo && key0 + c < hi) || (kSinks && key0 + c < sk);
                     const unsigned char* vr =
                         v_s + (c0 >> 6) * (kKeys * 128) + c * 128;
 #pragma unroll
@@ -1255,17 +1302,20 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
       const int bc = bi / boxes, bk = (bi - bc * boxes) * box;  // half of the row, first key
       uint32_t base = 0;                            // tiles loaded before this segment
       bool ok = true;
-      Walk walk(P, m, tp);
+      Walk<kSinks> walk(P, m, tp);
       Seg s;
       while (ok && walk.next(s)) {
         int lo, hi;
         key_range(P, s.r.n, s.r.len, s.t0, s.t1, lo, hi);
+        const int sk = kSinks ? min(P.sinks, hi) : 0;
+        const Places at = kSinks ? places_of(P, lo, hi) : Places{};
         const int64_t row0 = static_cast<int64_t>(s.r.slot < 0 ? 0 : s.r.slot) * P.M;
         // this lane's page of tile j; num_blocks (which TMA reads as zeros) where
         // there is nothing to see
         auto page_of = [&](int j) -> int {
-          const int key = j * kKeys + bk;
-          if (bi >= nb || key >= hi || key + box <= lo) return P.kv.num_blocks;
+          const int key = (kSinks ? at.real(j) : j) * kKeys + bk;
+          if (bi >= nb || key >= hi || (key + box <= lo && !(kSinks && key < sk)))
+            return P.kv.num_blocks;
           const int id = P.block_table[row0 + (key >> P.page_shift)];
           if (id >= 0 && id < P.kv.num_blocks) return id;
           report(P.status, DSPARK_ERR_BOUNDS);
@@ -1283,7 +1333,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
           }
           __syncwarp();
           if (bi < nb) {
-            const int y = (s.load_tile(i) * kKeys + bk) & (page - 1);
+            const int tile = kSinks ? at.real(s.load_tile(i)) : s.load_tile(i);
+            const int y = (tile * kKeys + bk) & (page - 1);
             unsigned char* dst = ring + st * kBytes + bk * (kQuant ? D : 128);
             tma_load_4d(dst + bc * (kKeys * 128), map, bc * 64, y, s.load_head(i), id, &full[st],
                         pol);
@@ -1308,7 +1359,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
       // ---- scout: segments and their query rows ---------------------------------------
       uint32_t n_q = 0;
       bool ok = true;
-      Walk walk(P, m, tp);
+      Walk<kSinks> walk(P, m, tp);
       Seg s;
       for (;;) {
         const bool more = walk.next(s);
@@ -1638,12 +1689,12 @@ bool make_q_map(CUtensorMap* map, const PagedAttentionParams& p) {
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool kF16, bool kQuant, bool kScaled>
+template <int D, bool kF16, bool kQuant, bool kScaled, bool kSinks>
 cudaError_t launch(const PagedAttentionParams& p, const CUtensorMap& mq, const CUtensorMap& mk,
                    const CUtensorMap& mv, int sms, cudaStream_t stream) {
   using C = Cfg<D, kQuant>;
   cudaError_t err =
-      cudaFuncSetAttribute(paged_attention_kernel<D, kF16, kQuant, kScaled>,
+      cudaFuncSetAttribute(paged_attention_kernel<D, kF16, kQuant, kScaled, kSinks>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
   if (err != cudaSuccess) return err;
   const int grid = sms < kMaxCtas ? sms : kMaxCtas;
@@ -1658,7 +1709,7 @@ cudaError_t launch(const PagedAttentionParams& p, const CUtensorMap& mq, const C
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  err = cudaLaunchKernelEx(&cfg, paged_attention_kernel<D, kF16, kQuant, kScaled>, mq, mk, mv, p);
+  err = cudaLaunchKernelEx(&cfg, paged_attention_kernel<D, kF16, kQuant, kScaled, kSinks>, mq, mk, mv, p);
   if (err != cudaSuccess || p.whole) return err;
   cfg.gridDim = dim3(grid, 16);
   cfg.blockDim = dim3(256);
@@ -1666,15 +1717,16 @@ cudaError_t launch(const PagedAttentionParams& p, const CUtensorMap& mq, const C
   return cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, p, kF16 ? 7 : 0);
 }
 
-template <int D>
+template <int D, bool kSinks>
 cudaError_t launch_dim(const PagedAttentionParams& p, const CUtensorMap& mq, const CUtensorMap& mk,
                        const CUtensorMap& mv, int sms, cudaStream_t stream) {
-  if (p.kv.dtype == DSPARK_E4M3) return launch<D, true, true, false>(p, mq, mk, mv, sms, stream);
+  if (p.kv.dtype == DSPARK_E4M3)
+    return launch<D, true, true, false, kSinks>(p, mq, mk, mv, sms, stream);
   if (p.kv.k_scale)
-    return p.dtype == DSPARK_F16 ? launch<D, true, false, true>(p, mq, mk, mv, sms, stream)
-                                 : launch<D, false, false, true>(p, mq, mk, mv, sms, stream);
-  return p.dtype == DSPARK_F16 ? launch<D, true, false, false>(p, mq, mk, mv, sms, stream)
-                               : launch<D, false, false, false>(p, mq, mk, mv, sms, stream);
+    return p.dtype == DSPARK_F16 ? launch<D, true, false, true, kSinks>(p, mq, mk, mv, sms, stream)
+                                 : launch<D, false, false, true, kSinks>(p, mq, mk, mv, sms, stream);
+  return p.dtype == DSPARK_F16 ? launch<D, true, false, false, kSinks>(p, mq, mk, mv, sms, stream)
+                               : launch<D, false, false, false, kSinks>(p, mq, mk, mv, sms, stream);
 }
 
 }  // namespace
@@ -1701,14 +1753,17 @@ cudaError_t launch_paged_attention(PagedAttentionParams p, cudaStream_t stream) 
     const int64_t tokens = p.causal ? 2 * (kRows / (p.Hq / kv.kv_heads)) : p.T;
     keys = min(keys, p.window + tokens);
   }
-  p.whole = (keys + kKeys - 1) / kKeys + (p.window > 0 ? 1 : 0) <=
+  p.whole = (keys + kKeys - 1) / kKeys + (p.window > 0 ? 1 : 0) + (p.sinks + kKeys - 1) / kKeys <=
             (3 * p.B * kv.kv_heads >= sms ? kWholeTiles : kWholeTilesFewUnits);
   if (!make_map(&mk, kv.k, kv, kv.k_block_stride, kv.k_head_stride, kv.k_token_stride) ||
       !make_map(&mv, kv.v, kv, kv.v_block_stride, kv.v_head_stride, kv.v_token_stride))
     return cudaErrorInvalidValue;
   if (!make_q_map(&mq, p)) return cudaErrorInvalidValue;
-  return kv.head_dim == 64 ? launch_dim<64>(p, mq, mk, mv, sms, stream)
-                           : launch_dim<128>(p, mq, mk, mv, sms, stream);
+  if (p.sinks > 0)
+    return kv.head_dim == 64 ? launch_dim<64, true>(p, mq, mk, mv, sms, stream)
+                             : launch_dim<128, true>(p, mq, mk, mv, sms, stream);
+  return kv.head_dim == 64 ? launch_dim<64, false>(p, mq, mk, mv, sms, stream)
+                           : launch_dim<128, false>(p, mq, mk, mv, sms, stream);
 }
 
 }  // namespace dspark
