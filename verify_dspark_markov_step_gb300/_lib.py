@@ -552,6 +552,16 @@ def _paged_kv(k_cache, v_cache, k_scale, v_scale):
     """The dspark_paged_kv of caches [num_blocks, kv_heads, page_size, head_dim]
     of any strides with contiguous head_dim (this thread's, until its next call),
     kv_heads and head_dim."""
+    try:
+        kv = _kv.kv
+    except AttributeError:
+        kv = _kv.kv = PagedKv()
+    H, D = _pack_kv(kv, 0, k_cache, v_cache, k_scale, v_scale)
+    return kv, H, D
+
+
+def _pack_kv(to, at, k_cache, v_cache, k_scale, v_scale):
+    """Writes a dspark_paged_kv; returns kv_heads and head_dim."""
     for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{name} must be a CUDA tensor")
@@ -567,16 +577,12 @@ def _paged_kv(k_cache, v_cache, k_scale, v_scale):
     vb, vh, vt, vd = v_cache.stride()
     if (kd != 1 or vd != 1) and D > 1:
         raise ValueError("k_cache and v_cache: the values of a token must be contiguous")
-    try:
-        kv = _kv.kv
-    except AttributeError:
-        kv = _kv.kv = PagedKv()
     _KV_FIELDS.pack_into(
-        kv, 0, k_cache.data_ptr(), v_cache.data_ptr(),
+        to, at, k_cache.data_ptr(), v_cache.data_ptr(),
         0 if k_scale is None else _of(k_scale, "k_scale", torch.float32, (H,)),
         0 if v_scale is None else _of(v_scale, "v_scale", torch.float32, (H,)),
         kb, kh, kt, vb, vh, vt, _PAGED_DTYPES[dt], N, H, P, D)
-    return kv, H, D
+    return H, D
 
 
 def paged_tables(req_state_idx, new_lens, cached_lens, block_table, held_blocks, free_blocks,
@@ -682,8 +688,7 @@ class PagedCaches:
         self.tensors = [(k, v) for k, v in caches]  # (kept alive)
         self.array = (PagedKv * len(self.tensors))()
         for i, (k, v) in enumerate(self.tensors):
-            kv, _, _ = _paged_kv(k, v, None, None)
-            ctypes.pointer(self.array[i])[0] = kv
+            _pack_kv(self.array, i * ctypes.sizeof(PagedKv), k, v, None, None)
 
 
 def paged_copy(caches, copies, count, status=None, stream=None):
@@ -724,7 +729,7 @@ def kv_append(k, v, k_cache, v_cache, slot_map, k_scale=None, v_scale=None, stat
 def _here(t, name):
     """Refuses tensors of another device than the current one: a launch goes to the
     current device."""
-    if t.get_device() != torch.cuda.current_device():
+    if t.get_device() != torch._C._cuda_getDevice():
         raise ValueError(f"{name} is on cuda:{t.get_device()}, which is not the current device")
 
 

@@ -11,11 +11,23 @@
 // which the series of sine and cosine to the ninth and eighth power are exact to
 // 2^-25. All of this is fp32; a value is rounded once, to the type it is stored in.
 //
-// Layout. D / 16 lanes (up to a power of two) share a head's row, 16 values each:
-// the two 16-byte pieces that hold both halves of eight pairs, so a pair never
-// leaves its lane and the norm's sum is all that lanes exchange. The heads of a
-// token follow each other in one or more warps ("parts": enough to fill the GPU with
-// few tokens), and the eight sines and cosines of a lane serve all of them.
+// Layout. D / 16 lanes (up to a power of two) share a head's row, 16 values each: two
+// 16-byte pieces, each of which neighbouring lanes have side by side, with both halves
+// of eight pairs, so a pair never leaves its lane and the norm's sum is all that lanes
+// exchange. A warp takes a few heads at a time of one token and one kind of row; the
+// eight sines and cosines of a lane (each worked out once a warp, and folded with the
+// weights) serve all of its rounds. Rows come through a ring in shared memory, three
+// rounds ahead (cp.async; every lane reads what it has loaded itself, so nothing is
+// waited for but its own copies), and leave by wide stores; arithmetic is in packed
+// pairs.
+//
+// Bound and measured. Prompts: memory; 16384 tokens, 32/8 heads of 128 in fp16, rows to
+// rows: 50.6 us, 6.6 TB/s (98% of a copy; with rows one round ahead in registers 68);
+// 64/8 heads with norms into an e4m3 cache 103 us, 6.2 TB/s (91%), instruction issue
+// (62% of the slots) beside it: six CTAs of 128 threads an SM (80 registers, a few
+// spilled in the norms' kernels; five, which spill nothing, 105.5; three of 256 104;
+// kinds of rows mixed in a warp 115). A decode step: latency; 256 tokens 3.5 to 4.6 us,
+// one 2.6.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -27,7 +39,8 @@ namespace dspark {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+constexpr int kStages = 4;  // rounds of rows on their way to a lane, and the one it works on
 
 // What becomes of keys and values: rows, the cache's pages as they are, in 8
 // bits by their scales, in 16 bits by their scales.
@@ -88,178 +101,348 @@ __device__ __forceinline__ uint2 to8(const float (&v)[8], float rcp, float scale
   return make_uint2(y[0] | (y[1] << 16), y[2] | (y[3] << 16));
 }
 
-template <bool kF16>
-__device__ __forceinline__ void unpack8(uint4 w, float (&v)[8]) {
-  unpack<kF16>(w.x, v[0], v[1]);
-  unpack<kF16>(w.y, v[2], v[3]);
-  unpack<kF16>(w.z, v[4], v[5]);
-  unpack<kF16>(w.w, v[6], v[7]);
+// Pairs (x[i], y[i]) of a lane's two pieces: of their i-th values, or of neighbours.
+template <bool kF16, bool kSplit>
+__device__ __forceinline__ void take(uint4 a, uint4 b, float (&x)[8], float (&y)[8]) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (kSplit) {
+      if (i < 4)
+        unpack<kF16>(w[i], x[2 * i], x[2 * i + 1]);
+      else
+        unpack<kF16>(w[i], y[2 * i - 8], y[2 * i - 7]);
+    } else {
+      unpack<kF16>(w[i], x[i], y[i]);
+    }
+  }
+}
+template <bool kF16, bool kSplit>
+__device__ __forceinline__ void give(const float (&x)[8], const float (&y)[8], uint4& a, uint4& b) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (kSplit)
+      w[i] = i < 4 ? pack16<kF16>(x[2 * (i & 3)], x[2 * (i & 3) + 1])
+                   : pack16<kF16>(y[2 * (i & 3)], y[2 * (i & 3) + 1]);
+    else
+      w[i] = pack16<kF16>(x[i], y[i]);
+  }
+  a = make_uint4(w[0], w[1], w[2], w[3]);
+  b = make_uint4(w[4], w[5], w[6], w[7]);
+}
+// Pairs of neighbours as they lie in the two pieces.
+__device__ __forceinline__ void unweave(float (&x)[8], float (&y)[8]) {
+  float v[16];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[2 * i] = x[i];
+    v[2 * i + 1] = y[i];
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[i] = v[i];
+    y[i] = v[8 + i];
+  }
 }
 
-template <bool kF16>
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-  return make_uint4(pack16<kF16>(v[0], v[1]), pack16<kF16>(v[2], v[3]), pack16<kF16>(v[4], v[5]),
-                    pack16<kF16>(v[6], v[7]));
+__device__ __forceinline__ void copy_async(uint4* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(to))),
+               "l"(from)
+               : "memory");
 }
 
-// `width` lanes a head (a power of two), `parts` warps a token, `per` rounds of 32 /
-// width heads a warp. kSplit: pairs are (i, i + rotary / 2), else (2 i, 2 i + 1).
-template <Form kForm, bool kF16, bool kSplit>
-__global__ void __launch_bounds__(kThreads, 3)
-qk_rope_kernel(QkRopeParams P, int width, int parts, int per) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31;
-  const int64_t warp = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+// How a launch's warps share the rows: `width` lanes a head (a power of two), 32 /
+// width heads a round; a kind of row (queries, keys, values) has `parts` warps a
+// token, `per` rounds each, and the CTAs from `first` on.
+struct Split {
+  int width;
+  struct {
+    int parts, per;
+    unsigned first;
+  } of[3];
+};
+
+// Where a lane's rows lie: the first values of its two pieces, of which neighbouring
+// lanes' are side by side, and whether they are rotated.
+template <bool kSplit>
+struct Lane {
+  int l, g;     // within the head, head of the round
+  int c0, c1;
+  bool mine, turn0, turn1;
+  __device__ __forceinline__ Lane(const QkRopeParams& P, int width) {
+    const int lane = threadIdx.x & 31, R = P.rotary;
+    l = lane & (width - 1);
+    g = lane / width;
+    mine = 16 * l < P.D;
+    if (kSplit) {  // the halves of eight pairs, or what is left of the row
+      const bool pairs = 16 * l < R;
+      c0 = pairs ? 8 * l : R / 2 + 8 * l;
+      c1 = c0 + (pairs ? R : P.D - R) / 2;
+      turn0 = turn1 = pairs;
+    } else {       // neighbours lie within a piece
+      c0 = 8 * l;
+      c1 = c0 + P.D / 2;
+      turn0 = c0 < R;
+      turn1 = c1 < R;
+    }
+  }
+};
+
+// x' = x ca + y nsa, y' = y cb + x sb for a lane's eight pairs (x, y), two at a time:
+// cosine and sine, the factor on them, the weights of a norm.
+struct Coefficients {
+  unsigned long long ca[4], nsa[4], cb[4], sb[4];
+};
+
+template <bool kF16, bool kSplit, bool kNorm>
+__device__ __forceinline__ void coefficients(const QkRopeParams& P, const Lane<kSplit>& L,
+                                             int width, int64_t position, const void* weight,
+                                             Coefficients& k) {
+  // the round's heads have the same angles: the lanes of each work out a share of the
+  // eight (two heads a round at least)
+  const int abreast = 32 / width, lg = abreast == 2 ? 2 : abreast == 4 ? 1 : 0, each = 1 << lg;
+  float mc[4], ms[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    mc[j] = 1.f;
+    ms[j] = 0.f;
+    const int i = (L.g << lg) + j;
+    // the i-th pair of this lane: of its halves, or four of each piece
+    const int f = kSplit ? 8 * L.l + i : (i < 4 ? L.c0 / 2 + i : L.c1 / 2 + i - 4);
+    if (j < each && i < 8 && 2 * f < P.rotary && L.mine) {
+      const uint64_t at = static_cast<uint64_t>(position) * P.turns[f];
+      cos_sin(static_cast<uint32_t>(at >> 32), mc[j], ms[j]);
+      mc[j] *= P.factor;
+      ms[j] *= P.factor;
+    }
+  }
+  float cs[8], sn[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int from = (i >> lg) * width + L.l, j = i & (each - 1);
+    const float c = j == 0 ? mc[0] : j == 1 ? mc[1] : j == 2 ? mc[2] : mc[3];
+    const float s = j == 0 ? ms[0] : j == 1 ? ms[1] : j == 2 ? ms[2] : ms[3];
+    cs[i] = __shfl_sync(0xFFFFFFFFu, c, from);
+    sn[i] = __shfl_sync(0xFFFFFFFFu, s, from);
+  }
+  float wx[8], wy[8];  // of the pairs' first and second values
+#pragma unroll
+  for (int i = 0; i < 8; ++i) wx[i] = wy[i] = 1.f;
+  if (kNorm && weight && L.mine) {
+    const uint16_t* w = static_cast<const uint16_t*>(weight);
+    take<kF16, kSplit>(*reinterpret_cast<const uint4*>(w + L.c0),
+                       *reinterpret_cast<const uint4*>(w + L.c1), wx, wy);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const unsigned long long c = f2_pack(cs[2 * i], cs[2 * i + 1]);
+    const unsigned long long s = f2_pack(sn[2 * i], sn[2 * i + 1]);
+    const unsigned long long ns = f2_pack(-sn[2 * i], -sn[2 * i + 1]);
+    const unsigned long long x = f2_pack(wx[2 * i], wx[2 * i + 1]);
+    const unsigned long long y = f2_pack(wy[2 * i], wy[2 * i + 1]);
+    k.ca[i] = kNorm ? f2_mul(c, x) : c;
+    k.cb[i] = kNorm ? f2_mul(c, y) : c;
+    k.nsa[i] = kNorm ? f2_mul(ns, y) : ns;
+    k.sb[i] = kNorm ? f2_mul(s, x) : s;
+  }
+}
+
+// The pairs of a row rotated and, with a norm, weighed and normalised: that comes
+// last, so that the lanes' exchange runs beside the rotation.
+template <bool kSplit, bool kNorm>
+__device__ __forceinline__ void turn(const QkRopeParams& P, const Lane<kSplit>& L, int width,
+                                     bool normed, const Coefficients& k, float (&x)[8],
+                                     float (&y)[8]) {
+  unsigned long long p[4], q[4], n2 = 0ull;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    p[i] = f2_pack(x[2 * i], x[2 * i + 1]);
+    q[i] = f2_pack(y[2 * i], y[2 * i + 1]);
+  }
+  if (kNorm && normed) {
+    unsigned long long sum2 = f2_mul(p[0], p[0]), sum3 = f2_mul(q[0], q[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) {
+      sum2 = f2_fma(p[i], p[i], sum2);
+      sum3 = f2_fma(q[i], q[i], sum3);
+    }
+    float s0, s1;
+    f2_unpack(f2_add(sum2, sum3), s0, s1);
+    s0 += s1;
+    for (int o = width >> 1; o > 0; o >>= 1) s0 += __shfl_xor_sync(0xFFFFFFFFu, s0, o);
+    const float norm = rsqrtf(fmaf(s0, P.inv_d, P.eps));
+    n2 = f2_pack(norm, norm);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (kSplit || i < 2 ? L.turn0 : L.turn1) {
+      const unsigned long long u = f2_fma(p[i], k.ca[i], f2_mul(q[i], k.nsa[i]));
+      q[i] = f2_fma(q[i], k.cb[i], f2_mul(p[i], k.sb[i]));
+      p[i] = u;
+    } else if (kNorm) {  // (a sine of 0 would make NaN of an infinite neighbour)
+      p[i] = f2_mul(p[i], k.ca[i]);
+      q[i] = f2_mul(q[i], k.cb[i]);
+    }
+    if (kNorm && normed) {
+      p[i] = f2_mul(p[i], n2);
+      q[i] = f2_mul(q[i], n2);
+    }
+    f2_unpack(p[i], x[2 * i], x[2 * i + 1]);
+    f2_unpack(q[i], y[2 * i], y[2 * i + 1]);
+  }
+}
+
+// One warp's rounds of one kind of row.
+template <int kWhat, Form kForm, bool kF16, bool kSplit, bool kNorm>
+__device__ __forceinline__ void rounds(const QkRopeParams& P, int width, int parts, int per,
+                                       unsigned block, uint4 (&ring)[kStages][2][kThreads]) {
+  constexpr bool kTurns = kWhat < 2, kPages = kForm != kRows && kWhat > 0;
+  const int64_t warp = static_cast<int64_t>(block) * (kThreads / 32) + (threadIdx.x >> 5);
   const int t = static_cast<int>(warp / parts);
   if (t >= P.T) return;
   const int part = static_cast<int>(warp - static_cast<int64_t>(t) * parts);
-  const int l = lane & (width - 1), abreast = 32 / width;
-  const int R = P.rotary;
-  const bool mine = 16 * l < P.D, turns = 16 * l < R;
-  // the first values of this lane's two pieces
-  const int c0 = kSplit ? (turns ? 8 * l : 16 * l) : 16 * l;
-  const int c1 = kSplit && turns ? c0 + R / 2 : c0 + 8;
-  const int heads = kForm == kRows ? P.Hq + P.H : P.Hq + 2 * P.H;
-  int n = part * per * abreast + lane / width;  // head row of the token: queries, keys, values
-  const int end = min(heads, (part + 1) * per * abreast);
+  const Lane<kSplit> L(P, width);
+  const int abreast = 32 / width, heads = kWhat == 0 ? P.Hq : P.H;
+  const int first = part * per * abreast;  // head
+  const int n = min(per, (heads - first + abreast - 1) / abreast);
+  int h = first + L.g;
 
-  auto source = [&](int r, int& what, int& h) -> const uint16_t* {
-    what = r < P.Hq ? 0 : r < P.Hq + P.H ? 1 : 2;
-    h = what == 0 ? r : what == 1 ? r - P.Hq : r - P.Hq - P.H;
-    return static_cast<const uint16_t*>(P.src[what]) + t * P.src_stride[what] +
-           static_cast<int64_t>(h) * P.D;
+  // Rows into this lane's own places of the ring, so that nobody else waits.
+  const uint16_t* src = static_cast<const uint16_t*>(P.src[kWhat]) +
+                        t * P.src_stride[kWhat] + static_cast<int64_t>(h) * P.D + L.c0;
+  const int across = L.c1 - L.c0, step = abreast * P.D;
+  int ahead = L.mine ? h : heads;  // head of the next row to load
+  auto load = [&](int stage) {
+    if (ahead < heads && ahead < first + n * abreast) {
+      copy_async(&ring[stage][0][threadIdx.x], src);
+      copy_async(&ring[stage][1][threadIdx.x], src + across);
+    }
+    src += step;
+    ahead += abreast;
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-  int what, h;
-  if (mine && n < end) {  // (not waiting for the position)
-    const uint16_t* src = source(n, what, h);
-    a = *reinterpret_cast<const uint4*>(src + c0);
-    b = *reinterpret_cast<const uint4*>(src + c1);
-  }
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) load(i);  // (not waiting for the position)
   const int64_t position = P.positions[t];
-  int64_t slot = -1;
-  if (kForm != kRows) {
-    slot = P.slot_map[t];
-    if (slot >= P.num_slots) {
-      if (part == 0 && lane == 0 && position >= 0) report(P.status, DSPARK_ERR_BOUNDS);
-      slot = -1;
+  bool skip = position < 0;
+  uint8_t* dst = nullptr;  // of this lane's first piece
+  int64_t next;            // bytes to the next round's
+  constexpr int kBytes = kPages && kForm == kTo8 ? 1 : 2;
+  if (kPages) {
+    const int64_t slot = P.slot_map[t];
+    if (slot >= P.num_slots && !skip && kWhat == 1 && part == 0 && (threadIdx.x & 31) == 0)
+      report(P.status, DSPARK_ERR_BOUNDS);
+    skip |= slot < 0 || slot >= P.num_slots;
+    if (!skip) {
+      const int64_t block_at = (slot >> P.page_shift) * P.block_stride[kWhat - 1];
+      const int off = static_cast<int>(slot) & ((1 << P.page_shift) - 1);
+      dst = static_cast<uint8_t*>(P.dst[kWhat]) +
+            (block_at + off * P.dst_stride[kWhat] + h * P.head_stride[kWhat - 1] + L.c0) * kBytes;
     }
+    next = abreast * P.head_stride[kWhat - 1] * kBytes;
+  } else {
+    dst = static_cast<uint8_t*>(P.dst[kWhat]) +
+          (t * P.dst_stride[kWhat] + static_cast<int64_t>(h) * P.D + L.c0) * kBytes;
+    next = static_cast<int64_t>(step) * kBytes;
   }
-  if (position < 0) return;
-  float cs[8], sn[8];
-  if (turns) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint64_t at = static_cast<uint64_t>(position) * P.turns[8 * l + i];
-      cos_sin(static_cast<uint32_t>(at >> 32), cs[i], sn[i]);
-      cs[i] *= P.factor;
-      sn[i] *= P.factor;
-    }
+  if (skip) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    return;
   }
-  // (the loop is uniform in a warp, whose lanes exchange sums)
-  for (int r0 = part * per * abreast; r0 < end; r0 += abreast, n += abreast) {
-    uint4 an = make_uint4(0u, 0u, 0u, 0u), bn = an;
-    const int next = n + abreast;
-    if (mine && next < end) {
-      int w1, h1;
-      const uint16_t* src = source(next, w1, h1);
-      an = *reinterpret_cast<const uint4*>(src + c0);
-      bn = *reinterpret_cast<const uint4*>(src + c1);
-    }
-    const bool live = mine && n < end;
-    source(n, what, h);
-    float x[8], y[8];
-    unpack8<kF16>(a, x);
-    unpack8<kF16>(b, y);
-    const void* weight = what == 0 ? P.weight[0] : what == 1 ? P.weight[1] : nullptr;
-    if (P.weight[0] || P.weight[1]) {
-      float sum = 0.f;
+  Coefficients k;
+  const void* weight = kTurns ? P.weight[kTurns ? kWhat : 0] : nullptr;
+  if (kTurns) coefficients<kF16, kSplit, kNorm>(P, L, width, position, weight, k);
+  for (int r0 = 0; r0 < n; r0 += kStages) {  // (uniform in a warp, whose lanes exchange sums)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], fmaf(y[i], y[i], sum));
-      for (int o = width >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-      if (live && weight) {
-        const uint16_t* w = static_cast<const uint16_t*>(weight);
-        const float scale = rsqrtf(sum * P.inv_d + P.eps);
-        float w0[8], w1[8];
-        unpack8<kF16>(*reinterpret_cast<const uint4*>(w + c0), w0);
-        unpack8<kF16>(*reinterpret_cast<const uint4*>(w + c1), w1);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[i] *= scale * w0[i];
-          y[i] *= scale * w1[i];
+    for (int s = 0; s < kStages; ++s) {
+      if (r0 + s >= n) break;
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+      uint4 a = ring[s][0][threadIdx.x], b = ring[s][1][threadIdx.x];
+      load((s + kStages - 1) % kStages);  // into the place that the round before has read
+      float scale = 1.f;
+      const bool live = L.mine && h < heads;
+      if (kPages && kForm != kCopy && live && P.scale[kWhat - 1]) scale = P.scale[kWhat - 1][h];
+      float x[8], y[8];
+      if (kTurns || (kPages && kForm != kCopy)) {
+        if (!L.mine) a = b = make_uint4(0u, 0u, 0u, 0u);
+        take<kF16, kSplit>(a, b, x, y);
+      }
+      if (kTurns) turn<kSplit, kNorm>(P, L, width, weight != nullptr, k, x, y);
+      if (kPages && kForm == kTo8) {
+        const bool slow = !temp_div_t_ok(scale);
+        const float rcp = __frcp_rn(scale);
+        if (!kSplit) unweave(x, y);
+        if (live) {
+          *reinterpret_cast<uint2*>(dst) = to8(x, rcp, scale, slow);
+          *reinterpret_cast<uint2*>(dst + across) = to8(y, rcp, scale, slow);
         }
-      }
-    }
-    if (turns && what != 2) {
-      auto turn = [&](float& p, float& q, int i) {
-        const float u = p * cs[i] - q * sn[i];
-        q = q * cs[i] + p * sn[i];
-        p = u;
-      };
+      } else {
+        if (kPages && kForm == kTo16) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (kSplit)
-          turn(x[i], y[i], i);
-        else if (i < 4)
-          turn(x[2 * i], x[2 * i + 1], i);
-        else
-          turn(y[2 * i - 8], y[2 * i - 7], i);
-      }
-    }
-    if (live) {
-      if (what == 0 || kForm == kRows) {
-        uint16_t* dst = static_cast<uint16_t*>(P.dst[what]) + t * P.dst_stride[what] +
-                        static_cast<int64_t>(h) * P.D;
-        *reinterpret_cast<uint4*>(dst + c0) = pack8<kF16>(x);
-        *reinterpret_cast<uint4*>(dst + c1) = pack8<kF16>(y);
-      } else if (slot >= 0) {
-        const int block = static_cast<int>(slot >> P.page_shift);
-        const int off = static_cast<int>(slot) & ((1 << P.page_shift) - 1);
-        const int64_t at = block * P.block_stride[what - 1] + off * P.dst_stride[what] +
-                           h * P.head_stride[what - 1];
-        float scale = 1.f;
-        if (kForm != kCopy && P.scale[what - 1]) scale = P.scale[what - 1][h];
-        if constexpr (kForm == kTo8) {
-          const bool slow = !temp_div_t_ok(scale);
-          const float rcp = __frcp_rn(scale);
-          uint8_t* dst = static_cast<uint8_t*>(P.dst[what]) + at;
-          *reinterpret_cast<uint2*>(dst + c0) = to8(x, rcp, scale, slow);
-          *reinterpret_cast<uint2*>(dst + c1) = to8(y, rcp, scale, slow);
-        } else {
-          uint16_t* dst = static_cast<uint16_t*>(P.dst[what]) + at;
-          if constexpr (kForm == kTo16) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              x[i] = __fdiv_rn(x[i], scale);
-              y[i] = __fdiv_rn(y[i], scale);
-            }
+          for (int i = 0; i < 8; ++i) {
+            x[i] = __fdiv_rn(x[i], scale);
+            y[i] = __fdiv_rn(y[i], scale);
           }
-          *reinterpret_cast<uint4*>(dst + c0) = pack8<kF16>(x);
-          *reinterpret_cast<uint4*>(dst + c1) = pack8<kF16>(y);
+        }
+        if (kTurns || (kPages && kForm == kTo16)) give<kF16, kSplit>(x, y, a, b);
+        if (live) {
+          *reinterpret_cast<uint4*>(dst) = a;
+          *reinterpret_cast<uint4*>(dst + 2 * across) = b;
         }
       }
+      dst += next;
+      h += abreast;
     }
-    a = an;
-    b = bn;
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// kSplit: pairs are (i, i + rotary / 2), else (2 i, 2 i + 1). kNorm: queries or keys
+// have a norm. The CTAs' kinds of rows are apart, so that one's warps end together.
+template <Form kForm, bool kF16, bool kSplit, bool kNorm>
+__global__ void __launch_bounds__(kThreads, 6) qk_rope_kernel(QkRopeParams P, Split split) {
+  __shared__ uint4 ring[kStages][2][kThreads];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const unsigned block = blockIdx.x;
+  if (block < split.of[1].first) {
+    rounds<0, kForm, kF16, kSplit, kNorm>(P, split.width, split.of[0].parts, split.of[0].per,
+                                           block, ring);
+  } else if (kForm == kRows || block < split.of[2].first) {
+    rounds<1, kForm, kF16, kSplit, kNorm>(P, split.width, split.of[1].parts, split.of[1].per,
+                                           block - split.of[1].first, ring);
+  } else if constexpr (kForm != kRows) {
+    rounds<2, kForm, kF16, kSplit, false>(P, split.width, split.of[2].parts, split.of[2].per,
+                                          block - split.of[2].first, ring);
   }
 }
 
-template <Form kForm, bool kF16, bool kSplit>
+template <Form kForm, bool kF16, bool kSplit, bool kNorm>
 cudaError_t launch(const QkRopeParams& p, cudaStream_t stream) {
-  int width = 1;
-  while (16 * width < p.D) width *= 2;
-  const int heads = kForm == kRows ? p.Hq + p.H : p.Hq + 2 * p.H;
-  const int abreast = 32 / width, rounds = (heads + abreast - 1) / abreast;
+  Split split;
+  split.width = 1;
+  while (16 * split.width < p.D) split.width *= 2;
+  const int abreast = 32 / split.width;
   // a token's rounds over as many warps as it takes to give every SM 24
-  constexpr int kWarps = 152 * 24;
-  int parts = (kWarps + p.T - 1) / p.T;
-  if (parts > rounds) parts = rounds;
-  const int per = (rounds + parts - 1) / parts;
-  parts = (rounds + per - 1) / per;
-  const int64_t warps = static_cast<int64_t>(p.T) * parts;
+  constexpr int kWarps = 152 * 24, kPerCta = kThreads / 32;
+  unsigned ctas = 0;
+  const int total = (p.Hq + (kForm == kRows ? 1 : 2) * p.H + abreast - 1) / abreast;
+  const int most = (static_cast<int64_t>(total) * p.T + kWarps - 1) / kWarps;
+  for (int what = 0; what < 3; ++what) {
+    auto& of = split.of[what];
+    const int heads = what == 0 ? p.Hq : what == 1 || kForm != kRows ? p.H : 0;
+    const int rounds = (heads + abreast - 1) / abreast;
+    of.per = rounds < most ? rounds : most;
+    if (of.per < 1) of.per = 1;
+    of.parts = (rounds + of.per - 1) / of.per;
+    of.per = of.parts ? (rounds + of.parts - 1) / of.parts : 1;
+    of.first = ctas;
+    ctas += static_cast<unsigned>((static_cast<int64_t>(p.T) * of.parts + kPerCta - 1) / kPerCta);
+  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((warps + kThreads / 32 - 1) / (kThreads / 32)));
+  cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   // (may be set up while the kernel before it ends, and waits for it)
@@ -268,16 +451,22 @@ cudaError_t launch(const QkRopeParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, qk_rope_kernel<kForm, kF16, kSplit>, p, width, parts, per);
+  return cudaLaunchKernelEx(&cfg, qk_rope_kernel<kForm, kF16, kSplit, kNorm>, p, split);
+}
+
+template <Form kForm, bool kNorm>
+cudaError_t launch_norm(const QkRopeParams& p, cudaStream_t stream) {
+  if (p.dtype == DSPARK_F16)
+    return p.interleaved ? launch<kForm, true, false, kNorm>(p, stream)
+                         : launch<kForm, true, true, kNorm>(p, stream);
+  return p.interleaved ? launch<kForm, false, false, kNorm>(p, stream)
+                       : launch<kForm, false, true, kNorm>(p, stream);
 }
 
 template <Form kForm>
 cudaError_t launch_form(const QkRopeParams& p, cudaStream_t stream) {
-  if (p.dtype == DSPARK_F16)
-    return p.interleaved ? launch<kForm, true, false>(p, stream)
-                         : launch<kForm, true, true>(p, stream);
-  return p.interleaved ? launch<kForm, false, false>(p, stream)
-                       : launch<kForm, false, true>(p, stream);
+  return p.weight[0] || p.weight[1] ? launch_norm<kForm, true>(p, stream)
+                                    : launch_norm<kForm, false>(p, stream);
 }
 
 }  // namespace
