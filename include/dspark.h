@@ -326,12 +326,17 @@ dspark_status dspark_noise(const uint64_t* seed, const int64_t* pos,
  *
  * Between two drafting steps the target model runs the anchor token and the
  * K drafts of every request over that request's cached keys and values, and
- * the rejection sampler decides how many of them stay. The three calls below
- * are the cache's part of that pass, all lengths on the device, so that a step
- * follows from the last one's num_accepted without the host:
+ * the rejection sampler decides how many of them stay. The calls below are the
+ * cache's part of that pass, all lengths on the device, so that a step follows
+ * from the last one's num_accepted without the host:
  *   dspark_paged_tables     block tables, query offsets, positions, slot map
  *   dspark_kv_append        the new keys and values into their pages
- *   dspark_paged_attention  the new tokens' attention over the pages
+ *   dspark_qk_rope_append   the same with the norm of each query and key head and
+ *                           the rotation by position (dspark_qk_rope: rows alone)
+ *   dspark_paged_attention  the new tokens' attention over the pages; with
+ *                           ..._sinks, a window and first tokens that stay visible
+ * and between steps
+ *   dspark_paged_fork, dspark_paged_free, dspark_paged_compact, dspark_paged_copy
  * The pages of the drafter have no counterpart; the layouts are the ones that
  * paged caches commonly have.
  *
@@ -449,7 +454,7 @@ dspark_status dspark_paged_tables(
  *   copies[0 .. count[0]) are the pairs (old number, new number), and the table
  *   entries of all slots and shares follow. free_blocks[i] = N - 1 - i for i < N - U.
  *   The blocks' contents are moved by dspark_paged_copy, on the same stream before
- *   anything that reads them. A table entry within held_blocks that is out of range or
+ *   anything that reads them; slot maps made before are void. A table entry within held_blocks that is out of range or
  *   on the stack stays as it is, with DSPARK_ERR_BOUNDS.
  *
  * dspark_paged_copy -- blocks copied in the caches of all layers.

@@ -57,8 +57,10 @@ def test_rows_refusals(L):
     assert call(pos=None) == -1
     assert call(q=ODD) == -7
     assert call(ko=ODD) == -7
-    assert call(qs=1028) == -7
-    assert call(kos=-256) == -7
+    assert call(qs=1028, qos=1028) == -7
+    assert call(ks=-256, kos=-256) == -7
+    assert call(qo=FAKE, q=FAKE, qos=2048) == -1      # in place with other strides
+    assert call(ko=FAKE, k=FAKE, kos=512) == -1
     assert call(T=0, q=None) == 0
 
 
@@ -91,7 +93,8 @@ def test_append_refusals(L):
     for name in ("q", "qo", "k", "v"):
         assert call(**{name: ODD}) == -7, name
     for name in ("qs", "qos", "ks", "vs"):
-        assert call(**{name: 1028}) == -7, name
+        assert call(**{name: 1028, **({"qos": 1028} if name == "qs" else {"qs": 1028} if name == "qos" else {})}) == -7, name
+    assert call(qos=2048) == -1
     assert call(k_token_stride=132) == -7
     assert call(T=0) == 0
 

@@ -254,3 +254,50 @@ def test_captured_and_on_another_stream():
     # eps / mean square changes by a factor of 4 from 1e-6: 2^-20 of a value, one step of bf16 at most
     assert off <= 2.0 ** -7 * want[0].float().abs().max().item()
     assert torch.equal(vc, want[2])
+
+
+def test_binding_refusals():
+    from verify_dspark_markov_step_gb300 import _lib, qk_rope, qk_rope_append
+    q = torch.zeros(4, 8, 128, device="cuda", dtype=torch.bfloat16)
+    k = torch.zeros(4, 2, 128, device="cuda", dtype=torch.bfloat16)
+    pos = torch.zeros(4, dtype=torch.int64, device="cuda")
+    rot = Rotary(64)
+    for kw, what in (({"positions": pos.int()}, TypeError), ({"positions": pos[:3]}, ValueError),
+                     ({"k": k[:3]}, ValueError), ({"k": k.half()}, ValueError), ({"q": q.float()}, TypeError),
+                     ({"q": q[..., ::2]}, ValueError), ({"q": q.transpose(0, 1)}, ValueError), ({"q": q[0]}, ValueError),
+                     ({"q_out": k}, ValueError), ({"k": None, "k_out": k}, ValueError),
+                     ({"q_weight": q[0, 0, :64].contiguous()}, ValueError), ({"k_weight": torch.ones(128, device="cuda")}, TypeError),
+                     ({"turns": rot.turns[:, None]}, ValueError), ({"turns": rot.turns.double()}, TypeError),
+                     ({"turns": torch.zeros(72, dtype=torch.int64, device="cuda")}, _lib.DsparkError),
+                     ({"turns": rot.turns[:12]}, _lib.DsparkError), ({"turns": rot.turns, "factor": float("inf")}, _lib.DsparkError),
+                     ({"q_weight": q[0, 0], "eps": -1.0}, _lib.DsparkError), ({"q": q.expand(4, 8, 128)[:, :, :].as_strided((4, 8, 128), (0, 128, 1))}, _lib.DsparkError)):
+        with pytest.raises(what):
+            qk_rope(**{"q": q, "k": k, "positions": pos, **kw})
+    cache = torch.zeros(2, 2, 16, 128, device="cuda", dtype=torch.bfloat16)
+    for kw, what in (({"v": k[:3]}, ValueError), ({"k": q}, ValueError), ({"slot_map": pos[:3]}, ValueError),
+                     ({"q": q[..., :64]}, ValueError), ({"v": k.half()}, ValueError), ({"k_cache": cache.half()}, ValueError)):
+        with pytest.raises(what):
+            qk_rope_append(**{"q": q, "k": k, "v": k.clone(), "k_cache": cache, "v_cache": cache, "positions": pos, "slot_map": pos, **kw})
+    qk_rope(q[:0], k[:0], pos[:0], **rot.args())
+    assert (q == 0).all()
+
+
+def test_pages_past_32_bits_of_offset():
+    """Blocks whose values lie more than 2^32 elements into the cache: written, and copied."""
+    from verify_dspark_markov_step_gb300 import paged_copy, qk_rope_append
+    N, H, P, D = 40000, 8, 256, 64  # 5.2e9 values
+    k = torch.zeros(N, H, P, D, device="cuda", dtype=torch.float8_e4m3fn)
+    v = torch.zeros(N, H, P, D, device="cuda", dtype=torch.float8_e4m3fn)
+    q, kk, vv = (torch.ones(2, h, D, device="cuda", dtype=torch.bfloat16) for h in (3, H, H))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    slots = torch.tensor([(N - 1) * P + 255, 35000 * P + 3], device="cuda")
+    qk_rope_append(q, kk, vv, k, v, torch.zeros(2, dtype=torch.int64, device="cuda"), slots, status=status)
+    paged_copy([(k, v)], torch.tensor([[N - 1, 17], [35000, N - 2]], dtype=torch.int32, device="cuda"),
+               torch.tensor([2], dtype=torch.int32, device="cuda"), status=status)
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    for c in (k, v):
+        for block, at in ((N - 1, 255), (35000, 3), (17, 255), (N - 2, 3)):
+            x = c[block].float()
+            assert (x[:, at] == 1).all() and x.sum().item() == H * D
+        assert c[0].float().sum().item() == 0 and c[N - 3].float().sum().item() == 0

@@ -495,6 +495,8 @@ _PAGED_DTYPES = {torch.bfloat16: DSPARK_BF16, torch.float16: DSPARK_F16,
                  torch.float8_e4m3fn: DSPARK_E4M3}
 
 
+_ROW_DTYPES = {torch.bfloat16: DSPARK_BF16, torch.float16: DSPARK_F16}
+
 MAX_PAGED_BATCH = 1024  # DSPARK_MAX_PAGED_BATCH
 
 # The calls below are made once a layer and step, some for a few microseconds of
@@ -534,6 +536,13 @@ def _raw_stream(stream, t):
 def _rows(t, name):
     """[T, H, D] rows whose tokens may be further apart than H * D (a view into
     a fused projection): (address, dtype, elements between tokens)."""
+    try:
+        T, H, D = t.shape
+        st, sh, sd = t.stride()
+        if t.is_cuda and (sd == 1 or D < 2) and (sh == D or H < 2):
+            return t.data_ptr(), _ROW_DTYPES[t.dtype], H * D if T < 2 else st
+    except (AttributeError, ValueError, KeyError):
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     dt = t.dtype
@@ -541,11 +550,7 @@ def _rows(t, name):
         raise TypeError(f"{name} must be bfloat16 or float16, got {dt}")
     if t.dim() != 3:
         raise ValueError(f"{name} must be [T, heads, head_dim]")
-    T, H, D = t.shape
-    st, sh, sd = t.stride()
-    if (sd != 1 and D > 1) or (sh != D and H > 1):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), _PAGED_DTYPES[dt], H * D if T < 2 else st
+    raise ValueError(f"{name}: the heads of a token must be contiguous")
 
 
 def _paged_kv(k_cache, v_cache, k_scale, v_scale):
@@ -630,12 +635,11 @@ def paged_fork(src, dst, cached_lens, block_table, held_blocks, free_blocks, poo
     n = src.shape[0]
     lens, table, held, free, pool_p, shares_p, S, M, N = _pages_of(
         cached_lens, block_table, held_blocks, free_blocks, pool, shares)
-    _here(block_table, "block_table")
     code = (_lib or lib()).dspark_paged_fork(
         _of(src, "src", i32, (n,)), _of(dst, "dst", i32, (n,)), lens, table, held, free, pool_p,
         shares_p, _of(copies, "copies", i32, (copies.shape[0], 2)), _of(count, "count", i32, (1,)),
         n, S, M, N, copies.shape[0], page_size, _maybe(status, "status", i32),
-        _raw_stream(stream, block_table))
+        _stream_here(stream, block_table, "block_table"))
     if code:
         _check(code, "dspark_paged_fork")
 
@@ -648,10 +652,9 @@ def paged_free(slots, cached_lens, block_table, held_blocks, free_blocks, pool, 
     n = slots.shape[0]
     lens, table, held, free, pool_p, shares_p, S, M, N = _pages_of(
         cached_lens, block_table, held_blocks, free_blocks, pool, shares)
-    _here(block_table, "block_table")
     code = (_lib or lib()).dspark_paged_free(
         _of(slots, "slots", i32, (n,)), lens, table, held, free, pool_p, shares_p, n, S, M, N,
-        _maybe(status, "status", i32), _raw_stream(stream, block_table))
+        _maybe(status, "status", i32), _stream_here(stream, block_table, "block_table"))
     if code:
         _check(code, "dspark_paged_free")
 
@@ -668,14 +671,14 @@ def paged_compact(block_table, held_blocks, free_blocks, pool, copies, count, sh
     i32 = torch.int32
     _, table, held, free, pool_p, shares_p, S, M, N = _pages_of(
         None, block_table, held_blocks, free_blocks, pool, shares)
-    _here(block_table, "block_table")
     if workspace_buf is None:
         with torch.cuda.stream(stream):  # memory of the stream that uses it
             workspace_buf = workspace(paged_compact_workspace_bytes(N), block_table.device)
     code = (_lib or lib()).dspark_paged_compact(
         table, held, free, pool_p, shares_p, _of(copies, "copies", i32, (copies.shape[0], 2)),
         _of(count, "count", i32, (1,)), S, M, N, copies.shape[0], workspace_buf.data_ptr(),
-        workspace_buf.nbytes, _maybe(status, "status", i32), _raw_stream(stream, block_table))
+        workspace_buf.nbytes, _maybe(status, "status", i32),
+        _stream_here(stream, block_table, "block_table"))
     if code:
         _check(code, "dspark_paged_compact")
 
@@ -698,11 +701,10 @@ def paged_copy(caches, copies, count, status=None, stream=None):
     if not isinstance(caches, PagedCaches):
         caches = PagedCaches(caches)
     i32 = torch.int32
-    _here(copies, "copies")
     code = (_lib or lib()).dspark_paged_copy(
         caches.array, len(caches.tensors), _of(copies, "copies", i32, (copies.shape[0], 2)),
         _of(count, "count", i32, (1,)), copies.shape[0], _maybe(status, "status", i32),
-        _raw_stream(stream, copies))
+        _stream_here(stream, copies, "copies"))
     if code:
         _check(code, "dspark_paged_copy")
 
@@ -726,11 +728,14 @@ def kv_append(k, v, k_cache, v_cache, slot_map, k_scale=None, v_scale=None, stat
         _check(code, "dspark_kv_append")
 
 
-def _here(t, name):
-    """Refuses tensors of another device than the current one: a launch goes to the
-    current device."""
-    if t.get_device() != torch._C._cuda_getDevice():
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, which is not the current device")
+def _stream_here(stream, t, name):
+    """_raw_stream of a tensor on the current device, to which a launch goes; of another
+    device it is refused."""
+    device = t.get_device()
+    if device != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on cuda:{device}, which is not the current device")
+    return (torch._C._cuda_getCurrentRawStream(device) if stream is None
+            else stream.cuda_stream)
 
 
 def _rotation(turns, head_dim, q_weight, k_weight, dtype):
@@ -773,11 +778,11 @@ def qk_rope(q, k, positions, turns=None, factor=1.0, interleaved=False, q_weight
         ko, kos = (kp, ks) if k_out is None else _rows_out(k_out, "k_out", k)
     elif k_out is not None:
         raise ValueError("k_out without k")
-    _here(q, "q")
     turns_p, R, qw, kw = _rotation(turns, D, q_weight, k_weight, q.dtype)
     code = (_lib or lib()).dspark_qk_rope(
         qp, qo, kp, ko, dt, qs, qos, ks, kos, _of(positions, "positions", torch.int64, (T,)),
-        turns_p, factor, R, bool(interleaved), qw, kw, eps, Hq, H, D, T, _raw_stream(stream, q))
+        turns_p, factor, R, bool(interleaved), qw, kw, eps, Hq, H, D, T,
+        _stream_here(stream, q, "q"))
     if code:
         _check(code, "dspark_qk_rope")
 
@@ -796,13 +801,12 @@ def qk_rope_append(q, k, v, k_cache, v_cache, positions, slot_map, turns=None, f
         raise ValueError(f"q, k and v must be [{T}, heads, {D}] of one dtype, k and v with "
                          f"{H} heads")
     qo, qos = (qp, qs) if q_out is None else _rows_out(q_out, "q_out", q)
-    _here(q, "q")
     turns_p, R, qw, kw = _rotation(turns, D, q_weight, k_weight, q.dtype)
     i64 = torch.int64
     code = (_lib or lib()).dspark_qk_rope_append(
         qp, qo, kp, vp, dt, qs, qos, ks, vs, cache, _of(positions, "positions", i64, (T,)),
         _of(slot_map, "slot_map", i64, (T,)), turns_p, factor, R, bool(interleaved), qw, kw, eps,
-        Hq, T, _maybe(status, "status", torch.int32), _raw_stream(stream, q))
+        Hq, T, _maybe(status, "status", torch.int32), _stream_here(stream, q, "q"))
     if code:
         _check(code, "dspark_qk_rope_append")
 

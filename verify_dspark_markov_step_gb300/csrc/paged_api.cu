@@ -55,6 +55,11 @@ dspark_status check_cache(const dspark_paged_kv* c, int dtype) {
   return DSPARK_OK;
 }
 
+// Rows written where they are read from lie as they do there.
+bool in_place_ok(const void* in, const void* out, int64_t in_stride, int64_t out_stride, int T) {
+  return in != out || in_stride == out_stride || T < 2;
+}
+
 // The checks both rotating calls make of the rotation and the norms.
 dspark_status check_rotation(const uint64_t* turns, float factor, int rotary_dim, int interleaved,
                              const void* q_weight, const void* k_weight, float eps, int head_dim) {
@@ -346,6 +351,9 @@ dspark_status dspark_qk_rope(const void* q, void* q_out, const void* k, void* k_
   if (bad != DSPARK_OK || T == 0) return bad;
   const bool keys = kv_heads > 0;
   if (!q || !q_out || !positions || (keys && (!k || !k_out))) return DSPARK_ERR_INVALID_ARG;
+  if (!in_place_ok(q, q_out, q_stride, q_out_stride, T) ||
+      (keys && !in_place_ok(k, k_out, k_stride, k_out_stride, T)))
+    return DSPARK_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(q_out) || !stride_ok(q_stride, 2) || !stride_ok(q_out_stride, 2))
     return DSPARK_ERR_ALIGNMENT;
   if (keys && (!aligned16(k) || !aligned16(k_out) || !stride_ok(k_stride, 2) ||
@@ -385,6 +393,7 @@ dspark_status dspark_qk_rope_append(const void* q, void* q_out, const void* k, c
                          cache->head_dim);
   if (bad != DSPARK_OK || T == 0) return bad;
   if (!q || !q_out || !k || !v || !positions || !slot_map) return DSPARK_ERR_INVALID_ARG;
+  if (!in_place_ok(q, q_out, q_stride, q_out_stride, T)) return DSPARK_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(v) ||
       !stride_ok(q_stride, 2) || !stride_ok(q_out_stride, 2) || !stride_ok(k_stride, 2) ||
       !stride_ok(v_stride, 2))

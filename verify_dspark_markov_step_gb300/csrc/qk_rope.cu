@@ -429,12 +429,12 @@ cudaError_t launch(const QkRopeParams& p, cudaStream_t stream) {
   constexpr int kWarps = 152 * 24, kPerCta = kThreads / 32;
   unsigned ctas = 0;
   const int total = (p.Hq + (kForm == kRows ? 1 : 2) * p.H + abreast - 1) / abreast;
-  const int most = (static_cast<int64_t>(total) * p.T + kWarps - 1) / kWarps;
+  const int64_t most = (static_cast<int64_t>(total) * p.T + kWarps - 1) / kWarps;
   for (int what = 0; what < 3; ++what) {
     auto& of = split.of[what];
     const int heads = what == 0 ? p.Hq : what == 1 || kForm != kRows ? p.H : 0;
     const int rounds = (heads + abreast - 1) / abreast;
-    of.per = rounds < most ? rounds : most;
+    of.per = rounds < most ? rounds : static_cast<int>(most);
     if (of.per < 1) of.per = 1;
     of.parts = (rounds + of.per - 1) / of.per;
     of.per = of.parts ? (rounds + of.parts - 1) / of.parts : 1;
