@@ -494,8 +494,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_compact_kernel(PagedCompact
 
 // ---- copies ------------------------------------------------------------------------
 constexpr int kCopyThreads = 256, kCopyEach = 8;  // 16-byte pieces a thread holds
+constexpr int kChunk = kCopyThreads * kCopyEach;
 
-// blockIdx.y: keys or values of a layer; blockIdx.x takes chunks of the copies in turn.
+// blockIdx.y: keys or values of a layer; blockIdx.x takes chunks in turn, of a large
+// block or (kMany) of several small ones: then every piece has a copy of its own to look
+// up (blocks of 2 KB 1062 us -> 238, of 8 KB 804 -> 436, of 12 KB 585 -> 456), which
+// would cost a large block 3%.
+template <bool kMany>
 __global__ void __launch_bounds__(kCopyThreads) paged_copy_kernel(PagedCopyParams P) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -506,38 +511,63 @@ __global__ void __launch_bounds__(kCopyThreads) paged_copy_kernel(PagedCopyParam
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) report(P.status, DSPARK_ERR_BOUNDS);
     n = n < 0 ? 0 : P.C;
   }
-  constexpr int kChunk = kCopyThreads * kCopyEach;
-  const int chunks = (P.pieces + kChunk - 1) / kChunk;
+  const int chunks = (P.pieces + kChunk - 1) / kChunk;  // of a block
+  const int group = kMany ? kChunk / P.pieces : 1;      // blocks of a chunk
   const int step_n = gridDim.x / chunks, step_c = gridDim.x - step_n * chunks;
   int i = blockIdx.x / chunks, c = blockIdx.x - i * chunks;
-  while (i < n) {
-    const int2 move = P.copies[i];
-    if (move.x >= 0 && move.x < P.num_blocks && move.y >= 0 && move.y < P.num_blocks) {
-      const uint8_t* from = base + move.x * P.block_bytes[which];
-      uint8_t* to = base + move.y * P.block_bytes[which];
-      uint4 x[kCopyEach];
+  for (; static_cast<int64_t>(i) * group < n; i += step_n, c += step_c) {
+    if (c >= chunks) {
+      c -= chunks;
+      if (static_cast<int64_t>(++i) * group >= n) break;
+    }
+    auto there = [&](int2 m) {
+      return m.x >= 0 && m.x < P.num_blocks && m.y >= 0 && m.y < P.num_blocks;
+    };
+    auto place = [&](int u) -> int64_t {  // of a block's piece
+      const int row = u >> P.row_shift;
+      return (row >> P.page_shift) * P.head_bytes[which] +
+             (row & ((1 << P.page_shift) - 1)) * P.token_bytes[which] +
+             ((u & ((1 << P.row_shift) - 1)) << 4);
+    };
+    uint4 x[kCopyEach];
+    if constexpr (kMany) {
+      uint8_t* to[kCopyEach];
+#pragma unroll
+      for (int k = 0; k < kCopyEach; ++k) {
+        const int all = k * kCopyThreads + threadIdx.x, b = all / P.pieces, u = all - b * P.pieces;
+        to[k] = nullptr;
+        if (b >= group || n - i * group <= b) continue;
+        const int2 m = P.copies[i * group + b];
+        if (there(m)) {
+          const int64_t at = place(u);
+          x[k] = *reinterpret_cast<const uint4*>(base + m.x * P.block_bytes[which] + at);
+          to[k] = base + m.y * P.block_bytes[which] + at;
+        } else if (u == 0) {
+          report(P.status, DSPARK_ERR_BOUNDS);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kCopyEach; ++k)
+        if (to[k]) *reinterpret_cast<uint4*>(to[k]) = x[k];
+    } else {
+      const int2 m = P.copies[i];
+      if (!there(m)) {
+        if (threadIdx.x == 0) report(P.status, DSPARK_ERR_BOUNDS);
+        continue;
+      }
+      const uint8_t* from = base + m.x * P.block_bytes[which];
+      uint8_t* to = base + m.y * P.block_bytes[which];
       int64_t at[kCopyEach];
 #pragma unroll
       for (int k = 0; k < kCopyEach; ++k) {
         const int u = c * kChunk + k * kCopyThreads + threadIdx.x;
-        const int row = u >> P.row_shift;
-        at[k] = (row >> P.page_shift) * P.head_bytes[which] +
-                (row & ((1 << P.page_shift) - 1)) * P.token_bytes[which] +
-                ((u & ((1 << P.row_shift) - 1)) << 4);
+        at[k] = place(u);
         if (u < P.pieces) x[k] = *reinterpret_cast<const uint4*>(from + at[k]);
       }
 #pragma unroll
       for (int k = 0; k < kCopyEach; ++k)
         if (c * kChunk + k * kCopyThreads + threadIdx.x < P.pieces)
           *reinterpret_cast<uint4*>(to + at[k]) = x[k];
-    } else if (threadIdx.x == 0) {
-      report(P.status, DSPARK_ERR_BOUNDS);
-    }
-    i += step_n;
-    c += step_c;
-    if (c >= chunks) {
-      c -= chunks;
-      ++i;
     }
   }
 }
@@ -589,7 +619,8 @@ cudaError_t launch_paged_copy(const PagedCopyParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_copy_kernel, p);
+  return p.pieces <= kChunk / 2 ? cudaLaunchKernelEx(&cfg, paged_copy_kernel<true>, p)
+                                : cudaLaunchKernelEx(&cfg, paged_copy_kernel<false>, p);
 }
 
 }  // namespace dspark
