@@ -39,6 +39,9 @@ def _positions(T, far, rng, gone=()):
     (37, 64, 8, 128, 64, "qk"), (300, 28, 4, 128, 128, ""), (19, 5, 2, 96, 48, "qk"), (3, 4, 2, 96, 96, ""),
     (11, 6, 3, 192, 64, "qk"), (9, 2, 1, 256, 256, "qk"), (7, 9, 2, 256, 16, ""), (13, 3, 5, 16, 16, "qk"),
     (4, 3, 2, 32, 16, "q"), (6, 10, 1, 48, 32, "qk"), (4100, 3, 1, 64, 64, "qk"), (21, 4, 4, 128, 0, "qk"),
+    # several tokens a warp and a round
+    (8192, 5, 1, 64, 64, "qk"), (8215, 1, 0, 128, 32, "q"), (8193, 9, 2, 96, 48, "k"), (8200, 2, 3, 256, 64, ""),
+    (9001, 1, 1, 16, 16, "qk"), (8211, 17, 4, 128, 128, "qk"),
 ])
 def test_rows(T, Hq, H, D, R, norm, interleaved, dtype):
     from verify_dspark_markov_step_gb300 import qk_rope
@@ -47,7 +50,7 @@ def test_rows(T, Hq, H, D, R, norm, interleaved, dtype):
     g = torch.Generator("cuda").manual_seed(T + D)
     q, k = _rows(T, (Hq, H), D, dt, g, 3.0)
     qw, kw = ((1 + 0.3 * torch.randn(D, device="cuda", generator=g)).to(dt) if c in norm else None for c in "qk")
-    positions = _positions(T, 200000, rng, gone=(T // 2,) if T > 2 else ())
+    positions = _positions(T, 200000, rng, gone=(T // 2, T - 1, T - 2) if T > 99 else (T // 2,) if T > 2 else ())
     rot = Rotary(R, 1e6, interleaved=interleaved) if R else None
     args = rot.args() if rot else {"interleaved": interleaved}
     q_out = torch.full_like(q.contiguous(), 7.0)
@@ -132,7 +135,7 @@ def _cache(layout, N, H, P, D, dt, g):
                                                 ("fp16", "e4m3", True), ("fp16", "e4m3", False), ("bf16", "bf16", True)])
 @pytest.mark.parametrize("T,Hq,H,D,R,P,norm,interleaved", [
     (1, 32, 8, 128, 128, 16, True, False), (45, 5, 1, 64, 32, 32, True, True), (130, 16, 8, 128, 64, 64, False, False),
-    (700, 4, 2, 64, 64, 256, True, False)])
+    (700, 4, 2, 64, 64, 256, True, False), (8197, 3, 1, 128, 64, 32, True, False), (8321, 9, 3, 64, 48, 64, False, True)])
 def test_append(T, Hq, H, D, R, P, norm, interleaved, dtype, cache, scaled, layout):
     from verify_dspark_markov_step_gb300 import qk_rope_append
     dt = DT[dtype]
@@ -147,10 +150,12 @@ def test_append(T, Hq, H, D, R, P, norm, interleaved, dtype, cache, scaled, layo
     if scaled:
         ks, vs = (0.01 + 0.01 * torch.rand(H, device="cuda", generator=g) for _ in range(2))
     w = [(1 + 0.3 * torch.randn(D, device="cuda", generator=g)).to(dt) if norm else None for _ in range(2)]
-    positions = _positions(T, 30000, rng, gone=(3,) if T > 9 else ())
+    positions = _positions(T, 30000, rng, gone=(3, T // 3, T - 1) if T > 99 else (3,) if T > 9 else ())
     slots = torch.randperm(N * P, generator=torch.Generator().manual_seed(T))[:T]
     if T > 9:
         slots[5] = -1
+    if T > 99:
+        slots[T // 2:T // 2 + 9] = -1
     rot = Rotary(R, 1e5, interleaved=interleaved)
     q_out = torch.zeros(T, Hq, D, device="cuda", dtype=dt)
     status = torch.zeros(1, dtype=torch.int32, device="cuda")

@@ -14,20 +14,19 @@
 // Layout. D / 16 lanes (up to a power of two) share a head's row, 16 values each: two
 // 16-byte pieces, each of which neighbouring lanes have side by side, with both halves
 // of eight pairs, so a pair never leaves its lane and the norm's sum is all that lanes
-// exchange. A warp takes a few heads at a time of one token and one kind of row; the
-// eight sines and cosines of a lane (each worked out once a warp, and folded with the
-// weights) serve all of its rounds. Rows come through a ring in shared memory, three
-// rounds ahead (cp.async; every lane reads what it has loaded itself, so nothing is
-// waited for but its own copies), and leave by wide stores; arithmetic is in packed
-// pairs.
+// exchange. A warp takes a few heads at a time of one kind of row (queries, keys,
+// values); a token's sines and cosines are shared out over the warp, passed on in shared
+// memory and folded with the weights, and serve all of its rounds. Rows come through a
+// ring in shared memory, three rounds ahead (cp.async; every lane reads what it has
+// loaded itself, so nothing is waited for but its own copies), and leave by wide stores;
+// arithmetic is in packed pairs.
 //
 // Bound and measured. Prompts: memory; 16384 tokens, 32/8 heads of 128 in fp16, rows to
-// rows: 50.6 us, 6.6 TB/s (98% of a copy; with rows one round ahead in registers 68);
-// 64/8 heads with norms into an e4m3 cache 103 us, 6.2 TB/s (91%), instruction issue
-// (62% of the slots) beside it: six CTAs of 128 threads an SM (80 registers, a few
-// spilled in the norms' kernels; five, which spill nothing, 105.5; three of 256 104;
-// kinds of rows mixed in a warp 115). A decode step: latency; 256 tokens 3.5 to 4.6 us,
-// one 2.6.
+// rows: 51.5 us, 6.5 TB/s (96% of a copy; with rows one round ahead in registers 68);
+// 64/8 heads with norms into a bf16 cache 103 us, 6.5 TB/s, into an e4m3 cache 104 us,
+// 6.1 TB/s, instruction issue beside it (with kinds of rows mixed in a warp 115). With few
+// heads the angles, once a token whatever its heads, and the start of a warp: 8/1 heads
+// 26 us where the bytes take 12. A decode step: latency; 256 tokens 3.7 to 4.8 us, one 2.5.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -40,6 +39,12 @@ namespace dspark {
 namespace {
 
 constexpr int kThreads = 128;
+// From so many tokens on a warp takes the rounds of several, and a round has place for
+// several tokens' heads, which spares starts (16384 tokens, single and several: 16/2 heads
+// of 128 43.7 and 38.8 us, 2/2 33.9 and 17.0, one of 64 30.6 and 9.7, 64/8 of 128 101.5 and
+// 99.5); with fewer they only make warps longer (8192 tokens, 16/2: 23.3 both; 4000: 12.9
+// and 16.3; 1500 of 64/8 11.7 and 15.2).
+constexpr int kManyTokens = 8192;
 constexpr int kStages = 4;  // rounds of rows on their way to a lane, and the one it works on
 
 // What becomes of keys and values: rows, the cache's pages as they are, in 8
@@ -153,15 +158,21 @@ __device__ __forceinline__ void copy_async(uint4* to, const void* from) {
                : "memory");
 }
 
-// How a launch's warps share the rows: `width` lanes a head (a power of two), 32 /
-// width heads a round; a kind of row (queries, keys, values) has `parts` warps a
-// token, `per` rounds each, and the CTAs from `first` on.
+// How a launch's warps share the rows of a kind (queries, keys, values): 32 / width
+// heads a round, `width` lanes each (a power of two). A round is of one token, or of
+// several where their heads (up to a power of two: `share`) leave place; a warp takes a
+// part of a token's rounds, or all of one or several tokens'.
+struct Kind {
+  int share;       // heads of a round that are of one token
+  int rounds;      // of a token (of a round's tokens)
+  int parts, per;  // warps that share a token's rounds, rounds of each
+  int tokens;      // consecutive tokens (rounds' tokens) a warp takes
+  int groups;      // tokens (rounds' tokens) in all
+  unsigned first;  // CTA
+};
 struct Split {
   int width;
-  struct {
-    int parts, per;
-    unsigned first;
-  } of[3];
+  Kind of[3];
 };
 
 // Where a lane's rows lie: the first values of its two pieces, of which neighbouring
@@ -196,37 +207,37 @@ struct Coefficients {
   unsigned long long ca[4], nsa[4], cb[4], sb[4];
 };
 
+// `table` [32 / share][8 width], of this warp; `position` is the lane's token's, `first`
+// the turns of the first two pairs that the lane works out.
 template <bool kF16, bool kSplit, bool kNorm>
 __device__ __forceinline__ void coefficients(const QkRopeParams& P, const Lane<kSplit>& L,
-                                             int width, int64_t position, const void* weight,
-                                             Coefficients& k) {
-  // the round's heads have the same angles: the lanes of each work out a share of the
-  // eight (two heads a round at least)
-  const int abreast = 32 / width, lg = abreast == 2 ? 2 : abreast == 4 ? 1 : 0, each = 1 << lg;
-  float mc[4], ms[4];
+                                             int width, int share, int64_t position,
+                                             const uint64_t (&first)[2], const void* weight,
+                                             float2* table, Coefficients& k) {
+  // the lanes of a token's heads share the work: all pairs' angles
+  const int lanes = share * width, q = (threadIdx.x & 31) & (lanes - 1), pairs = 8 * width;
+  table += (L.g / share) * pairs;
+  __syncwarp();  // (the last token's have been read)
+#pragma unroll 1
+  for (int f0 = q; f0 < pairs; f0 += 2 * lanes) {  // (two at a time)
+    float c[2], s[2];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    mc[j] = 1.f;
-    ms[j] = 0.f;
-    const int i = (L.g << lg) + j;
-    // the i-th pair of this lane: of its halves, or four of each piece
-    const int f = kSplit ? 8 * L.l + i : (i < 4 ? L.c0 / 2 + i : L.c1 / 2 + i - 4);
-    if (j < each && i < 8 && 2 * f < P.rotary && L.mine) {
-      const uint64_t at = static_cast<uint64_t>(position) * P.turns[f];
-      cos_sin(static_cast<uint32_t>(at >> 32), mc[j], ms[j]);
-      mc[j] *= P.factor;
-      ms[j] *= P.factor;
+    for (int u = 0; u < 2; ++u) {
+      const int f = f0 + u * lanes;
+      const bool turns = 2 * f < P.rotary;
+      const uint64_t a_turn = f0 == q ? first[u] : turns ? P.turns[f] : 0;
+      const uint64_t at = static_cast<uint64_t>(position) * a_turn;
+      cos_sin(static_cast<uint32_t>(at >> 32), c[u], s[u]);
+      if (turns) {
+        c[u] *= P.factor;
+        s[u] *= P.factor;
+      }
     }
-  }
-  float cs[8], sn[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int from = (i >> lg) * width + L.l, j = i & (each - 1);
-    const float c = j == 0 ? mc[0] : j == 1 ? mc[1] : j == 2 ? mc[2] : mc[3];
-    const float s = j == 0 ? ms[0] : j == 1 ? ms[1] : j == 2 ? ms[2] : ms[3];
-    cs[i] = __shfl_sync(0xFFFFFFFFu, c, from);
-    sn[i] = __shfl_sync(0xFFFFFFFFu, s, from);
+    for (int u = 0; u < 2; ++u)
+      if (f0 + u * lanes < pairs) table[f0 + u * lanes] = make_float2(c[u], s[u]);
   }
+  __syncwarp();
   float wx[8], wy[8];  // of the pairs' first and second values
 #pragma unroll
   for (int i = 0; i < 8; ++i) wx[i] = wy[i] = 1.f;
@@ -237,9 +248,11 @@ __device__ __forceinline__ void coefficients(const QkRopeParams& P, const Lane<k
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const unsigned long long c = f2_pack(cs[2 * i], cs[2 * i + 1]);
-    const unsigned long long s = f2_pack(sn[2 * i], sn[2 * i + 1]);
-    const unsigned long long ns = f2_pack(-sn[2 * i], -sn[2 * i + 1]);
+    // pairs 2 i and 2 i + 1 of this lane: of its halves, or four of each piece
+    const int f = kSplit ? 8 * L.l + 2 * i : (i < 2 ? L.c0 / 2 + 2 * i : L.c1 / 2 + 2 * i - 4);
+    const float4 cs = *reinterpret_cast<const float4*>(table + min(f, pairs - 2));
+    const unsigned long long c = f2_pack(cs.x, cs.z), s = f2_pack(cs.y, cs.w);
+    const unsigned long long ns = f2_pack(-cs.y, -cs.w);
     const unsigned long long x = f2_pack(wx[2 * i], wx[2 * i + 1]);
     const unsigned long long y = f2_pack(wy[2 * i], wy[2 * i + 1]);
     k.ca[i] = kNorm ? f2_mul(c, x) : c;
@@ -294,152 +307,202 @@ __device__ __forceinline__ void turn(const QkRopeParams& P, const Lane<kSplit>& 
   }
 }
 
-// One warp's rounds of one kind of row.
-template <int kWhat, Form kForm, bool kF16, bool kSplit, bool kNorm>
-__device__ __forceinline__ void rounds(const QkRopeParams& P, int width, int parts, int per,
-                                       unsigned block, uint4 (&ring)[kStages][2][kThreads]) {
+// One warp's rounds of one kind of row; of one token unless kMulti.
+template <int kWhat, Form kForm, bool kF16, bool kSplit, bool kNorm, bool kMulti>
+__device__ __forceinline__ void rounds(const QkRopeParams& P, int width, const Kind& of,
+                                       uint4 (&ring)[kStages][2][kThreads], float2* table) {
   constexpr bool kTurns = kWhat < 2, kPages = kForm != kRows && kWhat > 0;
-  const int64_t warp = static_cast<int64_t>(block) * (kThreads / 32) + (threadIdx.x >> 5);
-  const int t = static_cast<int>(warp / parts);
-  if (t >= P.T) return;
-  const int part = static_cast<int>(warp - static_cast<int64_t>(t) * parts);
+  constexpr int kBytes = kPages && kForm == kTo8 ? 1 : 2;
+  const int64_t warp = static_cast<int64_t>(blockIdx.x - of.first) * (kThreads / 32) +
+                       (threadIdx.x >> 5);
+  const int64_t group = warp / of.parts * of.tokens;
+  if (group >= of.groups) return;
+  int r = static_cast<int>(warp % of.parts) * of.per;
+  const int n = of.parts > 1 ? min(of.per, of.rounds - r)
+                             : static_cast<int>(min(static_cast<int64_t>(of.tokens),
+                                                    of.groups - group)) * of.rounds;
   const Lane<kSplit> L(P, width);
   const int abreast = 32 / width, heads = kWhat == 0 ? P.Hq : P.H;
-  const int first = part * per * abreast;  // head
-  const int n = min(per, (heads - first + abreast - 1) / abreast);
-  int h = first + L.g;
+  const int tokens = abreast / of.share;            // of a round
+  int t = static_cast<int>(group) * tokens + L.g / of.share;  // this lane's token
+  const int g = L.g & (of.share - 1);               // its head of a round
 
   // Rows into this lane's own places of the ring, so that nobody else waits.
-  const uint16_t* src = static_cast<const uint16_t*>(P.src[kWhat]) +
-                        t * P.src_stride[kWhat] + static_cast<int64_t>(h) * P.D + L.c0;
   const int across = L.c1 - L.c0, step = abreast * P.D;
-  int ahead = L.mine ? h : heads;  // head of the next row to load
-  auto load = [&](int stage) {
-    if (ahead < heads && ahead < first + n * abreast) {
-      copy_async(&ring[stage][0][threadIdx.x], src);
-      copy_async(&ring[stage][1][threadIdx.x], src + across);
+  int load_t = t, load_r = r, left = n;
+  auto row_of = [&](int token, int round) {
+    return static_cast<const uint16_t*>(P.src[kWhat]) + token * P.src_stride[kWhat] +
+           (static_cast<int64_t>(round) * step + g * P.D + L.c0);
+  };
+  const uint16_t* src = row_of(load_t, load_r);
+  int64_t position = t < P.T ? P.positions[t] : -1, slot = -1;
+  if (kPages && t < P.T) slot = P.slot_map[t];
+  // what the first coefficients need, on its way beside the position
+  const void* weight = kTurns ? P.weight[kTurns ? kWhat : 0] : nullptr;
+  uint64_t turns[2] = {0, 0};
+  if (kTurns) {
+    const int lanes = of.share * width, q = (threadIdx.x & 31) & (lanes - 1);
+    if (2 * q < P.rotary) turns[0] = P.turns[q];
+    if (2 * (q + lanes) < P.rotary) turns[1] = P.turns[q + lanes];
+  }
+  auto load = [&](unsigned stage) {
+    if (left > 0) {
+      if (L.mine && load_t < P.T && load_r * abreast + g < heads) {
+        copy_async(&ring[stage][0][threadIdx.x], src);
+        copy_async(&ring[stage][1][threadIdx.x], src + across);
+      }
+      --left;
+      src += step;
+      if (++load_r == of.rounds && kMulti) {
+        load_r = 0;
+        load_t += tokens;
+        src = row_of(load_t, 0);
+      }
     }
-    src += step;
-    ahead += abreast;
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) load(i);  // (not waiting for the position)
-  const int64_t position = P.positions[t];
-  bool skip = position < 0;
-  uint8_t* dst = nullptr;  // of this lane's first piece
-  int64_t next;            // bytes to the next round's
-  constexpr int kBytes = kPages && kForm == kTo8 ? 1 : 2;
-  if (kPages) {
-    const int64_t slot = P.slot_map[t];
-    if (slot >= P.num_slots && !skip && kWhat == 1 && part == 0 && (threadIdx.x & 31) == 0)
-      report(P.status, DSPARK_ERR_BOUNDS);
-    skip |= slot < 0 || slot >= P.num_slots;
-    if (!skip) {
-      const int64_t block_at = (slot >> P.page_shift) * P.block_stride[kWhat - 1];
+  Coefficients k;
+  uint8_t* dst = nullptr;  // of this lane's first piece of the round
+  const int64_t next = kPages ? abreast * P.head_stride[kWhat > 0 ? kWhat - 1 : 0] * kBytes
+                              : static_cast<int64_t>(step) * kBytes;
+  bool live = false;       // the token has a place for its rows
+  auto begin = [&]() {     // a token
+    live = L.mine && position >= 0;
+    const int64_t h = static_cast<int64_t>(r) * abreast + g;
+    if (kPages) {
+      if (slot >= P.num_slots) {
+        if (kWhat == 1 && live) report(P.status, DSPARK_ERR_BOUNDS);
+        slot = -1;
+      }
+      live &= slot >= 0;
       const int off = static_cast<int>(slot) & ((1 << P.page_shift) - 1);
       dst = static_cast<uint8_t*>(P.dst[kWhat]) +
-            (block_at + off * P.dst_stride[kWhat] + h * P.head_stride[kWhat - 1] + L.c0) * kBytes;
+            ((slot >> P.page_shift) * P.block_stride[kWhat > 0 ? kWhat - 1 : 0] +
+             off * P.dst_stride[kWhat] + h * P.head_stride[kWhat > 0 ? kWhat - 1 : 0] + L.c0) *
+                kBytes;
+    } else {
+      dst = static_cast<uint8_t*>(P.dst[kWhat]) +
+            (t * P.dst_stride[kWhat] + h * P.D + L.c0) * kBytes;
     }
-    next = abreast * P.head_stride[kWhat - 1] * kBytes;
-  } else {
-    dst = static_cast<uint8_t*>(P.dst[kWhat]) +
-          (t * P.dst_stride[kWhat] + static_cast<int64_t>(h) * P.D + L.c0) * kBytes;
-    next = static_cast<int64_t>(step) * kBytes;
-  }
-  if (skip) {
+    if (kTurns)
+      coefficients<kF16, kSplit, kNorm>(P, L, width, of.share, position, turns, weight, table, k);
+  };
+  begin();
+  if (!kMulti && __all_sync(0xFFFFFFFFu, !live)) {  // no place for any
     asm volatile("cp.async.wait_all;" ::: "memory");
     return;
   }
-  Coefficients k;
-  const void* weight = kTurns ? P.weight[kTurns ? kWhat : 0] : nullptr;
-  if (kTurns) coefficients<kF16, kSplit, kNorm>(P, L, width, position, weight, k);
-  for (int r0 = 0; r0 < n; r0 += kStages) {  // (uniform in a warp, whose lanes exchange sums)
-#pragma unroll
-    for (int s = 0; s < kStages; ++s) {
-      if (r0 + s >= n) break;
-      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-      uint4 a = ring[s][0][threadIdx.x], b = ring[s][1][threadIdx.x];
-      load((s + kStages - 1) % kStages);  // into the place that the round before has read
-      float scale = 1.f;
-      const bool live = L.mine && h < heads;
-      if (kPages && kForm != kCopy && live && P.scale[kWhat - 1]) scale = P.scale[kWhat - 1][h];
-      float x[8], y[8];
-      if (kTurns || (kPages && kForm != kCopy)) {
-        if (!L.mine) a = b = make_uint4(0u, 0u, 0u, 0u);
-        take<kF16, kSplit>(a, b, x, y);
+#pragma unroll(kMulti ? 1 : kStages)
+  for (int i = 0; i < n; ++i) {  // (uniform in a warp, whose lanes exchange sums)
+    if (kMulti && r == 0) {
+      if (i > 0) begin();
+      // of the next token, if it is this warp's
+      t += tokens;
+      position = -1;
+      if (t < P.T && n - i > of.rounds) {
+        position = P.positions[t];
+        if (kPages) slot = P.slot_map[t];
       }
-      if (kTurns) turn<kSplit, kNorm>(P, L, width, weight != nullptr, k, x, y);
-      if (kPages && kForm == kTo8) {
-        const bool slow = !temp_div_t_ok(scale);
-        const float rcp = __frcp_rn(scale);
-        if (!kSplit) unweave(x, y);
-        if (live) {
-          *reinterpret_cast<uint2*>(dst) = to8(x, rcp, scale, slow);
-          *reinterpret_cast<uint2*>(dst + across) = to8(y, rcp, scale, slow);
-        }
-      } else {
-        if (kPages && kForm == kTo16) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            x[i] = __fdiv_rn(x[i], scale);
-            y[i] = __fdiv_rn(y[i], scale);
-          }
-        }
-        if (kTurns || (kPages && kForm == kTo16)) give<kF16, kSplit>(x, y, a, b);
-        if (live) {
-          *reinterpret_cast<uint4*>(dst) = a;
-          *reinterpret_cast<uint4*>(dst + 2 * across) = b;
-        }
-      }
-      dst += next;
-      h += abreast;
     }
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    const unsigned stage = static_cast<unsigned>(i) % kStages;
+    uint4 a = ring[stage][0][threadIdx.x], b = ring[stage][1][threadIdx.x];
+    load((stage + kStages - 1) % kStages);  // into the place that the round before has read
+    const int h = r * abreast + g;
+    const bool store = live && h < heads;
+    float scale = 1.f;
+    if (kPages && kForm != kCopy && store && P.scale[kWhat - 1]) scale = P.scale[kWhat - 1][h];
+    float x[8], y[8];
+    if (kTurns || (kPages && kForm != kCopy)) {
+      if (!L.mine) a = b = make_uint4(0u, 0u, 0u, 0u);
+      take<kF16, kSplit>(a, b, x, y);
+    }
+    if (kTurns) turn<kSplit, kNorm>(P, L, width, weight != nullptr, k, x, y);
+    if (kPages && kForm == kTo8) {
+      const bool slow = !temp_div_t_ok(scale);
+      const float rcp = __frcp_rn(scale);
+      if (!kSplit) unweave(x, y);
+      if (store) {
+        *reinterpret_cast<uint2*>(dst) = to8(x, rcp, scale, slow);
+        *reinterpret_cast<uint2*>(dst + across) = to8(y, rcp, scale, slow);
+      }
+    } else {
+      if (kPages && kForm == kTo16) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          x[e] = __fdiv_rn(x[e], scale);
+          y[e] = __fdiv_rn(y[e], scale);
+        }
+      }
+      if (kTurns || (kPages && kForm == kTo16)) give<kF16, kSplit>(x, y, a, b);
+      if (store) {
+        *reinterpret_cast<uint4*>(dst) = a;
+        *reinterpret_cast<uint4*>(dst + 2 * across) = b;
+      }
+    }
+    dst += next;
+    if (++r == of.rounds && kMulti) r = 0;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // kSplit: pairs are (i, i + rotary / 2), else (2 i, 2 i + 1). kNorm: queries or keys
-// have a norm. The CTAs' kinds of rows are apart, so that one's warps end together.
-template <Form kForm, bool kF16, bool kSplit, bool kNorm>
-__global__ void __launch_bounds__(kThreads, 6) qk_rope_kernel(QkRopeParams P, Split split) {
+// have a norm. kMulti: several tokens a warp. The CTAs' kinds of rows are apart, so that
+// one's warps end together.
+template <Form kForm, bool kF16, bool kSplit, bool kNorm, bool kMulti>
+__global__ void __launch_bounds__(kThreads, kMulti ? 5 : 6)
+qk_rope_kernel(const __grid_constant__ QkRopeParams P, const __grid_constant__ Split split) {
   __shared__ uint4 ring[kStages][2][kThreads];
+  __shared__ __align__(16) float2 angles[kThreads / 32][256];  // 8 for each lane
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const unsigned block = blockIdx.x;
-  if (block < split.of[1].first) {
-    rounds<0, kForm, kF16, kSplit, kNorm>(P, split.width, split.of[0].parts, split.of[0].per,
-                                           block, ring);
-  } else if (kForm == kRows || block < split.of[2].first) {
-    rounds<1, kForm, kF16, kSplit, kNorm>(P, split.width, split.of[1].parts, split.of[1].per,
-                                           block - split.of[1].first, ring);
-  } else if constexpr (kForm != kRows) {
-    rounds<2, kForm, kF16, kSplit, false>(P, split.width, split.of[2].parts, split.of[2].per,
-                                          block - split.of[2].first, ring);
-  }
+  float2* table = angles[threadIdx.x >> 5];
+  if (blockIdx.x < split.of[1].first)
+    rounds<0, kForm, kF16, kSplit, kNorm, kMulti>(P, split.width, split.of[0], ring, table);
+  else if (kForm == kRows || blockIdx.x < split.of[2].first)
+    rounds<1, kForm, kF16, kSplit, kNorm, kMulti>(P, split.width, split.of[1], ring, table);
+  else if constexpr (kForm != kRows)
+    rounds<2, kForm, kF16, kSplit, false, kMulti>(P, split.width, split.of[2], ring, table);
 }
 
-template <Form kForm, bool kF16, bool kSplit, bool kNorm>
+template <Form kForm, bool kF16, bool kSplit, bool kNorm, bool kMulti>
 cudaError_t launch(const QkRopeParams& p, cudaStream_t stream) {
   Split split;
   split.width = 1;
   while (16 * split.width < p.D) split.width *= 2;
   const int abreast = 32 / split.width;
-  // a token's rounds over as many warps as it takes to give every SM 24
-  constexpr int kWarps = 152 * 24, kPerCta = kThreads / 32;
-  unsigned ctas = 0;
-  const int total = (p.Hq + (kForm == kRows ? 1 : 2) * p.H + abreast - 1) / abreast;
-  const int64_t most = (static_cast<int64_t>(total) * p.T + kWarps - 1) / kWarps;
+  // Warps that are resident at a time (as many rounds a warp as there are for each of
+  // them), and the most rounds a warp takes of more than one token.
+  constexpr int kWarps = 152 * (kMulti ? 20 : 24), kMost = 6, kPerCta = kThreads / 32;
+  const int heads[3] = {p.Hq, p.H, kForm == kRows ? 0 : p.H};
+  int64_t total = 0;
   for (int what = 0; what < 3; ++what) {
-    auto& of = split.of[what];
-    const int heads = what == 0 ? p.Hq : what == 1 || kForm != kRows ? p.H : 0;
-    const int rounds = (heads + abreast - 1) / abreast;
-    of.per = rounds < most ? rounds : static_cast<int>(most);
-    if (of.per < 1) of.per = 1;
-    of.parts = (rounds + of.per - 1) / of.per;
-    of.per = of.parts ? (rounds + of.parts - 1) / of.parts : 1;
+    Kind& of = split.of[what];
+    of.share = kMulti ? 1 : abreast;
+    while (of.share < heads[what] && of.share < abreast) of.share *= 2;
+    of.rounds = (heads[what] + abreast - 1) / abreast;
+    const int tokens = abreast / of.share;
+    of.groups = of.rounds ? (p.T + tokens - 1) / tokens : 0;
+    total += static_cast<int64_t>(of.groups) * of.rounds;
+  }
+  const int64_t per = (total + kWarps - 1) / kWarps;
+  unsigned ctas = 0;
+  for (Kind& of : split.of) {
+    of.parts = of.tokens = 1;
+    of.per = of.rounds;
+    if (per < of.rounds) {
+      of.parts = (of.rounds + static_cast<int>(per) - 1) / static_cast<int>(per);
+      of.per = (of.rounds + of.parts - 1) / of.parts;
+      of.parts = (of.rounds + of.per - 1) / of.per;
+    } else if (kMulti && of.rounds > 0 && of.rounds < kMost) {
+      of.tokens = static_cast<int>(per < kMost ? per : kMost) / of.rounds;
+    }
+    const int64_t warps =
+        (static_cast<int64_t>(of.groups) + of.tokens - 1) / of.tokens * of.parts;
     of.first = ctas;
-    ctas += static_cast<unsigned>((static_cast<int64_t>(p.T) * of.parts + kPerCta - 1) / kPerCta);
+    ctas += static_cast<unsigned>((warps + kPerCta - 1) / kPerCta);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
@@ -451,22 +514,27 @@ cudaError_t launch(const QkRopeParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, qk_rope_kernel<kForm, kF16, kSplit, kNorm>, p, split);
+  return cudaLaunchKernelEx(&cfg, qk_rope_kernel<kForm, kF16, kSplit, kNorm, kMulti>, p, split);
 }
 
-template <Form kForm, bool kNorm>
+template <Form kForm, bool kNorm, bool kMulti>
 cudaError_t launch_norm(const QkRopeParams& p, cudaStream_t stream) {
   if (p.dtype == DSPARK_F16)
-    return p.interleaved ? launch<kForm, true, false, kNorm>(p, stream)
-                         : launch<kForm, true, true, kNorm>(p, stream);
-  return p.interleaved ? launch<kForm, false, false, kNorm>(p, stream)
-                       : launch<kForm, false, true, kNorm>(p, stream);
+    return p.interleaved ? launch<kForm, true, false, kNorm, kMulti>(p, stream)
+                         : launch<kForm, true, true, kNorm, kMulti>(p, stream);
+  return p.interleaved ? launch<kForm, false, false, kNorm, kMulti>(p, stream)
+                       : launch<kForm, false, true, kNorm, kMulti>(p, stream);
 }
 
 template <Form kForm>
 cudaError_t launch_form(const QkRopeParams& p, cudaStream_t stream) {
-  return p.weight[0] || p.weight[1] ? launch_norm<kForm, true>(p, stream)
-                                    : launch_norm<kForm, false>(p, stream);
+  const bool multi = p.T >= kManyTokens;
+  const bool norm = p.weight[0] || p.weight[1];
+  if (multi)
+    return norm ? launch_norm<kForm, true, true>(p, stream)
+                : launch_norm<kForm, false, true>(p, stream);
+  return norm ? launch_norm<kForm, true, false>(p, stream)
+              : launch_norm<kForm, false, false>(p, stream);
 }
 
 }  // namespace
