@@ -15,11 +15,11 @@
 // last request, wins and pushes the block.
 //
 // Copies are bound by memory: a thread has eight 16-byte pieces on their way (2.8 GB
-// read and written: 417 us, 6.7 TB/s, what the plain copy of a large tensor makes; with
-// four 440). The table calls are bound by latency, few of them by the eight SMs of the
-// cluster (128 forks of 44 thousand entries 17 us, their freeing 33; with four SMs 1.4
-// times as much, with one 4): a fork or free of a few requests takes 4 to 8 us, a
-// compaction of 30 thousand blocks 15.
+// read and written: 413 us, 6.8 TB/s, what the plain copy of a large tensor makes; with
+// four 440). The table calls are bound by latency, long ones by the eight SMs of the
+// cluster (cold caches: 128 forks of 44 thousand entries 14 us, freeing them 30; fork,
+// copy and free with a cluster of four 1.4 times as long, on one SM 3.4 times): a fork or
+// free of a few requests takes 4 to 8 us, a compaction of 29 thousand blocks 20.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -42,8 +42,7 @@ constexpr int kCluster = 8;
 // more than its threads gain.
 constexpr int kFewEntries = 4096;
 static_assert(kMaxN <= kThreads, "a slot per thread");
-// Entries a thread has under way at a time: each is a bisection, a load or two that
-// depend on it and perhaps an atomic.
+// Entries a thread has under way at a time: each is a load or two and perhaps an atomic.
 constexpr int kAbreast = 4;
 
 // The last b < n with start[b] <= e.
@@ -57,6 +56,39 @@ __device__ __forceinline__ int find(const int* start, int n, int e) {
       hi = mid - 1;
   }
   return lo;
+}
+
+// The entries of a warp, a run of all the call's: which slot each is of. Lanes' entries
+// go up, so the slot is found by bisection once and then looked for from the last one's
+// (a bisection an entry took half as long again: 128 slots of 344 blocks).
+struct Run {
+  const int* start;  // [n + 1] first entries of the slots, then their number
+  int n, w0, w1;
+  int slot0;         // of w0
+  __device__ __forceinline__ Run(const int* start_, int n_, int entries, int rank, int size)
+      : start(start_), n(n_) {
+    const int warp = threadIdx.x >> 5;
+    const int each = (entries + size - 1) / size, per = ((each + kWarps - 1) / kWarps + 31) & ~31;
+    w0 = min(rank * each + min(warp * per, each), entries);
+    w1 = min(rank * each + min((warp + 1) * per, each), entries);
+    slot0 = w0 < w1 ? find(start, n, w0) : 0;
+  }
+  __device__ __forceinline__ int slot(int from, int e) const {
+    while (start[from + 1] <= e) ++from;
+    return from;
+  }
+};
+
+// For each i < n whether `clash(i, j)` for some j < n, by the block's warps; into bad[].
+template <typename Clash>
+__device__ __forceinline__ void find_clashes(int n, int* bad, Clash clash) {
+  for (int i = threadIdx.x >> 5; i < n; i += kWarps) {
+    bool any = false;
+    for (int j = threadIdx.x & 31; j < n; j += 32) any |= clash(i, j);
+    any = __any_sync(0xFFFFFFFFu, any);
+    if ((threadIdx.x & 31) == 0) bad[i] = any;
+  }
+  __syncthreads();
 }
 
 // The sum over the cluster's CTAs of `mine`, and of those before this one.
@@ -86,7 +118,8 @@ __device__ __forceinline__ int pool_count(const int32_t* pool, int N, bool tell,
 struct ForkSmem {
   unsigned long long warp[33];
   int src[kMaxN], dst[kMaxN];
-  int start[kMaxN + 1];  // first entry of each fork
+  int bad[kMaxN];
+  int start[kMaxN + 1];  // first entry of each fork, their number
   int keep[kMaxN];       // shared blocks
   int take0[kMaxN];      // blocks taken by the forks before
 };
@@ -111,17 +144,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_fork_kernel(PagedForkParams
     sm.dst[tid] = dst;
   }
   __syncthreads();
+  // a dst that is named before, or is a src
+  find_clashes(P.n, sm.bad, [&](int i, int j) {
+    return sm.src[i] >= 0 && (sm.dst[j] == sm.src[i] || (j < i && sm.dst[j] == sm.dst[i]));
+  });
   bool ok = false;
   int len = 0, need = 0, keep = 0;
   if (src >= 0) {
-    bool bad = src >= P.S || dst >= P.S;
+    bool bad = src >= P.S || dst >= P.S || sm.bad[tid];
     if (!bad) {
       len = P.cached_lens[src];
       const int held = P.held_blocks[src];
       need = static_cast<int>((static_cast<int64_t>(len) + (1 << sh) - 1) >> sh);
       bad = len < 0 || held > M || need > held || P.held_blocks[dst] != 0;
-      for (int j = 0; j < P.n; ++j)
-        bad |= sm.dst[j] == src || (j < tid && sm.dst[j] == dst);
     }
     ok = !bad;
     if (bad && first) report(P.status, DSPARK_ERR_BOUNDS);
@@ -150,16 +185,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_fork_kernel(PagedForkParams
     sm.keep[tid] = keep;
     sm.take0[tid] = static_cast<int>(static_cast<unsigned int>(ends)) - take;
   }
+  if (tid == 0) sm.start[P.n] = entries;
   __syncthreads();
-  const int all_threads = size * kThreads;
-  for (int e0 = rank * kThreads + tid; e0 < entries; e0 += kAbreast * all_threads) {
+  const Run run(sm.start, P.n, entries, rank, size);
+  int i = run.slot0;
+  for (int e0 = run.w0 + (tid & 31); e0 < run.w1; e0 += 32 * kAbreast) {
     int id[kAbreast], fresh[kAbreast], at[kAbreast];  // at: the copy's place, < 0 if shared
     int64_t to[kAbreast];
 #pragma unroll
     for (int u = 0; u < kAbreast; ++u) {
-      const int e = e0 + u * all_threads;
-      if (e >= entries) break;
-      const int i = find(sm.start, P.n, e), j = e - sm.start[i], k = j - sm.keep[i];
+      const int e = e0 + 32 * u;
+      if (e >= run.w1) break;
+      i = run.slot(i, e);
+      const int j = e - sm.start[i], k = j - sm.keep[i];
       id[u] = P.block_table[static_cast<int64_t>(sm.src[i]) * M + j];
       to[u] = static_cast<int64_t>(sm.dst[i]) * M + j;
       at[u] = k < 0 ? -1 : sm.take0[i] + k;
@@ -167,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_fork_kernel(PagedForkParams
     }
 #pragma unroll
     for (int u = 0; u < kAbreast; ++u) {
-      if (e0 + u * all_threads >= entries) break;
+      if (e0 + 32 * u >= run.w1) break;
       const bool there = id[u] >= 0 && id[u] < N;
       if (!there) report(P.status, DSPARK_ERR_BOUNDS);
       if (at[u] < 0) {
@@ -194,6 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_fork_kernel(PagedForkParams
 struct FreeSmem {
   unsigned long long warp[33];
   int slot[kMaxN];
+  int bad[kMaxN];
   int start[kMaxN + 1];
   int sums[kWarps];
   int shared;
@@ -212,9 +251,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_free_kernel(PagedFreeParams
   int slot = -1, held = 0;
   if (tid < P.n) sm.slot[tid] = slot = P.slots[tid];
   __syncthreads();
+  find_clashes(P.n, sm.bad, [&](int i, int j) { return j < i && sm.slot[j] == sm.slot[i]; });
   if (slot >= 0) {
-    bool bad = slot >= P.S;
-    for (int j = 0; j < tid; ++j) bad |= sm.slot[j] == slot;
+    bool bad = slot >= P.S || sm.bad[tid];
     if (!bad) {
       held = P.held_blocks[slot];
       bad = held < 0 || held > M;
@@ -229,16 +268,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_free_kernel(PagedFreeParams
   const unsigned long long ends = block_scan(static_cast<unsigned int>(held), sm.warp, &total);
   if (tid < P.n) sm.start[tid] = static_cast<int>(ends) - held;
   const int entries = static_cast<int>(total);
+  if (tid == 0) sm.start[P.n] = entries;
   __syncthreads();
 
-  // the entries of this CTA, and of this warp
-  const int each = (entries + size - 1) / size, per = ((each + kWarps - 1) / kWarps + 31) & ~31;
-  const int w0 = min(rank * each + warp * per, entries);
-  const int w1 = min(min(rank * each + min((warp + 1) * per, each), entries), entries);
+  const Run run(sm.start, P.n, entries, rank, size);
+  const int w0 = run.w0, w1 = run.w1;
   // Block and slot (place in the call) of kAbreast entries; -1 past the end.
   int id[kAbreast], of[kAbreast];
   int32_t* at[kAbreast];
+  int i = run.slot0;
   auto entries_of = [&](int e0) {
+    if (e0 < w0 + 32) i = run.slot0;  // a new pass
 #pragma unroll
     for (int u = 0; u < kAbreast; ++u) {
       const int e = e0 + 32 * u;
@@ -246,8 +286,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_free_kernel(PagedFreeParams
       at[u] = nullptr;
       of[u] = 0;
       if (e >= w1) continue;
-      of[u] = find(sm.start, P.n, e);
-      at[u] = P.block_table + static_cast<int64_t>(sm.slot[of[u]]) * M + (e - sm.start[of[u]]);
+      of[u] = i = run.slot(i, e);
+      at[u] = P.block_table + static_cast<int64_t>(sm.slot[i]) * M + (e - sm.start[i]);
       id[u] = *at[u];
       if (id[u] < 0 || id[u] >= N) id[u] = -2;
     }
