@@ -19,7 +19,7 @@
 // four 440). The table calls are bound by latency, long ones by the eight SMs of the
 // cluster (cold caches: 128 forks of 44 thousand entries 14 us, freeing them 30; fork,
 // copy and free with a cluster of four 1.4 times as long, on one SM 3.4 times): a fork or
-// free of a few requests takes 4 to 8 us, a compaction of 29 thousand blocks 20.
+// free of a few requests takes 4 to 8 us, a compaction of 27 thousand blocks 20.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
