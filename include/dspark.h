@@ -419,12 +419,13 @@ dspark_status dspark_paged_tables(
  *
  * shares [N] int32 counts for each block the rows of the block table that hold it
  * beyond the first; all 0 before the first call. dspark_paged_fork makes shared
- * blocks; where a cache has them, every call on its tables gets `shares`. New tokens
- * never reach a shared block: a fork has a copy of a last block that is not full.
+ * blocks; where a cache has them, every call on its tables gets `shares`. A fork has a
+ * copy of a last block that is not full, so the tokens that follow reach no shared one.
  *
  * dspark_paged_tables_shared -- dspark_paged_tables for such a cache: a request that
- * would return a block which another row holds too (its cached_lens was lowered into
- * its shared blocks) is treated as padding, with DSPARK_ERR_BOUNDS. shares may be NULL.
+ * would return a block which another row holds too, or whose new tokens would come to
+ * lie in one (its cached_lens was lowered into its shared blocks), is treated as
+ * padding, with DSPARK_ERR_BOUNDS. shares may be NULL.
  *
  * dspark_paged_fork -- the tokens of slots src into slots dst.
  *   For every i in order with src[i], dst[i] >= 0: dst's cached_lens becomes L =

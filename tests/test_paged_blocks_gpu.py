@@ -174,6 +174,18 @@ def test_tables_leave_shared_blocks():
     x.status.zero_()
     x.compare()
     bo.check(x.t)
+    # nor do new tokens come to lie in one, whether blocks go back or not
+    for n, new in ((90, 1), (90, 60), (95, 1), (80, 16), (16, 64), (0, 64)):
+        x.cached[1] = x.t["cached"][1] = n
+        out, _ = plan(1, new)
+        assert x.status.item() == -5 and out[1].item() == 0 and (out[3] == -1).all()
+        x.status.zero_()
+        x.compare()
+    x.cached[1] = x.t["cached"][1] = 96
+    _, want = plan(1, 20)
+    taken(want)
+    x.compare()
+    bo.check(x.t)
 
 
 def test_corrupt_tables_stay_in_bounds():

@@ -78,9 +78,10 @@ __global__ void __launch_bounds__(1024) paged_tables_kernel(PagedTablesParams P)
         cached = static_cast<int64_t>(c) + acc + 1;
         need = (cached + fresh + (1 << sh) - 1) >> sh;
         ok = acc >= -1 && c >= 0 && fresh >= 0 && held >= 0 && held <= M && need <= M;
-        // a block that other rows hold too is not this call's to put on the stack
+        // a block that other rows hold too is not this call's to put on the stack, nor
+        // new tokens' to write into
         if (P.shares && ok)
-          for (int j = static_cast<int>(need); j < held; ++j) {
+          for (int j = static_cast<int>(fresh > 0 ? cached >> sh : need); j < held; ++j) {
             const int id = P.block_table[static_cast<int64_t>(slot) * M + j];
             if (id >= 0 && id < N && P.shares[id] > 0) ok = false;
           }

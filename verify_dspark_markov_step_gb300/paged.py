@@ -26,8 +26,9 @@ class PagedCache:
 
     The calls run on ``stream``, or on torch's current stream. A step's plan, appends and
     attentions share the tables and the plan's results, forks, frees and compactions the
-    tables and the list of copies: on several streams the caller orders them. Each stream has an attention workspace of its own, so attentions of one
-    plan may run on different streams side by side."""
+    tables and the list of copies: on several streams the caller orders them. Each stream
+    has an attention workspace of its own, so attentions of one plan may run on different
+    streams side by side."""
 
     def __init__(self, *, layers, slots, max_len, num_blocks, page_size, q_heads, kv_heads,
                  head_dim, dtype=torch.bfloat16, cache_dtype=None, k_scale=None, v_scale=None,

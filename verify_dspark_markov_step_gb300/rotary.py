@@ -44,7 +44,8 @@ def frequencies(rotary_dim, base=10000.0, scaling=None):
     how, f = scaling.get("type"), float(scaling.get("factor", 1.0))
     if not f > 0 or not math.isfinite(f):
         raise ValueError(f"scaling: factor must be positive, got {f}")
-    known = {"linear": (), "ntk": (), "by_parts": ("original_max_position", "low_turns", "high_turns"),
+    known = {"linear": (), "ntk": (),
+             "by_parts": ("original_max_position", "low_turns", "high_turns"),
              "yarn": ("original_max_position", "fast_turns", "slow_turns", "attention_factor")}
     if how not in known:
         raise ValueError(f"scaling: type must be one of {sorted(known)}, got {how!r}")
