@@ -23,10 +23,11 @@
 //
 // Bound and measured. Prompts: memory; 16384 tokens, 32/8 heads of 128 in fp16, rows to
 // rows: 51.5 us, 6.5 TB/s (96% of a copy; with rows one round ahead in registers 68);
-// 64/8 heads with norms into a bf16 cache 103 us, 6.5 TB/s, into an e4m3 cache 104 us,
-// 6.1 TB/s, instruction issue beside it (with kinds of rows mixed in a warp 115). With few
+// 64/8 heads with norms into a bf16 cache 102 us, 6.6 TB/s, into an e4m3 cache 103.5 us,
+// 6.2 TB/s, instruction issue beside it (with kinds of rows mixed in a warp 115). With few
 // heads the angles, once a token whatever its heads, and the start of a warp: 8/1 heads
-// 26 us where the bytes take 12. A decode step: latency; 256 tokens 3.7 to 4.8 us, one 2.5.
+// 26 us where the bytes take 12. A decode step: latency; 256 tokens 3.9 to 4.3 us, one 2.3.
+// (Five CTAs an SM; six spill registers: 256 tokens 5.2 us, 1500 13.7 for 12.5.)
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -41,8 +42,8 @@ namespace {
 constexpr int kThreads = 128;
 // From so many tokens on a warp takes the rounds of several, and a round has place for
 // several tokens' heads, which spares starts (16384 tokens, single and several: 16/2 heads
-// of 128 43.7 and 38.8 us, 2/2 33.9 and 17.0, one of 64 30.6 and 9.7, 64/8 of 128 101.5 and
-// 99.5); with fewer they only make warps longer (8192 tokens, 16/2: 23.3 both; 4000: 12.9
+// of 128 43.5 and 37.5 us, 2/2 33.9 and 16.6, one of 64 30.6 and 9.6, 64/8 of 128 104.0 and
+// 102.3); with fewer they only make warps longer (8192 tokens, 16/2: 23.3 both; 4000: 12.9
 // and 16.3; 1500 of 64/8 11.7 and 15.2).
 constexpr int kManyTokens = 8192;
 constexpr int kStages = 4;  // rounds of rows on their way to a lane, and the one it works on
@@ -288,16 +289,28 @@ __device__ __forceinline__ void turn(const QkRopeParams& P, const Lane<kSplit>& 
     const float norm = rsqrtf(fmaf(s0, P.inv_d, P.eps));
     n2 = f2_pack(norm, norm);
   }
+  // (values that are not rotated apart: a sine of 0 would make NaN of an infinite
+  // neighbour)
+  constexpr int kPart = kSplit ? 4 : 2;
+#pragma unroll
+  for (int i0 = 0; i0 < 4; i0 += kPart) {
+    if (i0 == 0 ? L.turn0 : L.turn1) {
+#pragma unroll
+      for (int i = i0; i < i0 + kPart; ++i) {
+        const unsigned long long u = f2_fma(p[i], k.ca[i], f2_mul(q[i], k.nsa[i]));
+        q[i] = f2_fma(q[i], k.cb[i], f2_mul(p[i], k.sb[i]));
+        p[i] = u;
+      }
+    } else if (kNorm) {
+#pragma unroll
+      for (int i = i0; i < i0 + kPart; ++i) {
+        p[i] = f2_mul(p[i], k.ca[i]);
+        q[i] = f2_mul(q[i], k.cb[i]);
+      }
+    }
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (kSplit || i < 2 ? L.turn0 : L.turn1) {
-      const unsigned long long u = f2_fma(p[i], k.ca[i], f2_mul(q[i], k.nsa[i]));
-      q[i] = f2_fma(q[i], k.cb[i], f2_mul(p[i], k.sb[i]));
-      p[i] = u;
-    } else if (kNorm) {  // (a sine of 0 would make NaN of an infinite neighbour)
-      p[i] = f2_mul(p[i], k.ca[i]);
-      q[i] = f2_mul(q[i], k.cb[i]);
-    }
     if (kNorm && normed) {
       p[i] = f2_mul(p[i], n2);
       q[i] = f2_mul(q[i], n2);
@@ -361,6 +374,11 @@ __device__ __forceinline__ void rounds(const QkRopeParams& P, int width, const K
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  if (kTurns && !L.mine) {  // lanes past the row add nothing to its norm
+#pragma unroll
+    for (int i = 0; i < kStages; ++i)
+      ring[i][0][threadIdx.x] = ring[i][1][threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
+  }
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) load(i);  // (not waiting for the position)
   Coefficients k;
@@ -415,10 +433,7 @@ __device__ __forceinline__ void rounds(const QkRopeParams& P, int width, const K
     float scale = 1.f;
     if (kPages && kForm != kCopy && store && P.scale[kWhat - 1]) scale = P.scale[kWhat - 1][h];
     float x[8], y[8];
-    if (kTurns || (kPages && kForm != kCopy)) {
-      if (!L.mine) a = b = make_uint4(0u, 0u, 0u, 0u);
-      take<kF16, kSplit>(a, b, x, y);
-    }
+    if (kTurns || (kPages && kForm != kCopy)) take<kF16, kSplit>(a, b, x, y);
     if (kTurns) turn<kSplit, kNorm>(P, L, width, weight != nullptr, k, x, y);
     if (kPages && kForm == kTo8) {
       const bool slow = !temp_div_t_ok(scale);
@@ -452,7 +467,7 @@ __device__ __forceinline__ void rounds(const QkRopeParams& P, int width, const K
 // have a norm. kMulti: several tokens a warp. The CTAs' kinds of rows are apart, so that
 // one's warps end together.
 template <Form kForm, bool kF16, bool kSplit, bool kNorm, bool kMulti>
-__global__ void __launch_bounds__(kThreads, kMulti ? 5 : 6)
+__global__ void __launch_bounds__(kThreads, 5)
 qk_rope_kernel(const __grid_constant__ QkRopeParams P, const __grid_constant__ Split split) {
   __shared__ uint4 ring[kStages][2][kThreads];
   __shared__ __align__(16) float2 angles[kThreads / 32][256];  // 8 for each lane
@@ -475,7 +490,7 @@ cudaError_t launch(const QkRopeParams& p, cudaStream_t stream) {
   const int abreast = 32 / split.width;
   // Warps that are resident at a time (as many rounds a warp as there are for each of
   // them), and the most rounds a warp takes of more than one token.
-  constexpr int kWarps = 152 * (kMulti ? 20 : 24), kMost = 6, kPerCta = kThreads / 32;
+  constexpr int kWarps = 152 * 20, kMost = 6, kPerCta = kThreads / 32;
   const int heads[3] = {p.Hq, p.H, kForm == kRows ? 0 : p.H};
   int64_t total = 0;
   for (int what = 0; what < 3; ++what) {
