@@ -122,6 +122,43 @@ def test_a_fork_that_does_not_fit_is_not_served():
     assert out[0] == out[1] and len(out[0]) >= 3 and out[2] == []
 
 
+def test_a_sample_whose_slot_is_taken_is_not_served():
+    require_gpu()
+    from verify_dspark_markov_step_gb300.paged import speculative_loop
+    from verify_dspark_markov_step_gb300.step import DecodeStep
+    target = made(False, "cuda")
+    w = wl.custom(3, 2, 300, 64, w_std=0.0, temperature=0.0, S=4, rsi=[0, 1, 2])
+    step = DecodeStep(w)
+    cache = _cache(False, True, slots=4, blocks=40)
+    prompt = torch.randint(300, (70,), generator=torch.Generator().manual_seed(1)).tolist()
+    cache.plan(_ints(1), _ints(70), 70)  # slot 1 holds something of another's
+    cache.cached_lens[1] = 70
+
+    def draft_logits(anchor):
+        return torch.zeros(3, 2, 300, device="cuda")
+    out = speculative_loop(step, target, cache, [prompt, [], []], 2, draft_logits, parents=[0, 0, 0])
+    torch.cuda.synchronize()
+    assert cache.status_code() == -5
+    assert out[1] == [] and out[2] == out[0] and len(out[0]) >= 3
+    assert int(cache.cached_lens[1]) == 70 and int(cache.held_blocks[1]) == 5
+
+
+def test_caches_that_were_replaced_are_the_ones_copied():
+    require_gpu()
+    cache = _cache(False, False, slots=3, blocks=12)
+    cache.plan(_ints(0), _ints(20), 20)
+    cache.cached_lens[0] = 20
+    cache.fork(_ints(0), _ints(1))
+    cache.k[1] = torch.randn_like(cache.k[1])
+    cache.k.append(torch.randn_like(cache.k[0])), cache.v.append(torch.randn_like(cache.v[0]))
+    cache.fork(_ints(0), _ints(2))
+    torch.cuda.synchronize()
+    a, b = cache.block_table[0, :2].long(), cache.block_table[2, :2].long()
+    assert cache.status_code() == 0
+    for c in cache.k + cache.v:
+        assert torch.equal(c[a], c[b])
+
+
 def test_the_command_runs_with_samples_rotation_and_sinks():
     require_gpu()
     from verify_dspark_markov_step_gb300 import paged

@@ -155,8 +155,8 @@ class PagedCache:
 
     def _copy(self, stream):
         kept = self._caches
-        if kept is None or any(a is not k or b is not v
-                               for (a, b), k, v in zip(kept.tensors, self.k, self.v)):
+        if kept is None or len(kept.tensors) != len(self.k) or any(
+                a is not k or b is not v for (a, b), k, v in zip(kept.tensors, self.k, self.v)):
             kept = self._caches = _lib.PagedCaches(zip(self.k, self.v))
         _lib.paged_copy(kept, self.copies, self.copied, status=self.status, stream=stream)
 
@@ -259,9 +259,11 @@ def speculative_loop(step, target: ToyTarget, cache: PagedCache, prompts, steps,
     samples = [b for b in range(B) if parents[b] != b]
     if samples:  # a fork that was refused (the status says so) is a request that is not served
         of, own = (torch.tensor(x, device=dev) for x in (parents, samples))
+        slot = step.rsi.clamp(min=0).long()
+        empty = (step.rsi >= 0) & (cache.held_blocks[slot] == 0)
         cache.fork(torch.where(served, step.rsi, -1)[of[own]], step.rsi[own])
-        held = (step.rsi >= 0) & (cache.held_blocks[step.rsi.clamp(min=0).long()] > 0)
-        served = served.index_copy(0, own, (served[of] & held)[own])
+        forked = served[of] & empty & (cache.held_blocks[slot] > 0)
+        served = served.index_copy(0, own, forked[own])
         last = last[of]
     rsi = torch.where(served, step.rsi, -1)
     anchor = torch.where(served, logits[last].argmax(1), 0)
