@@ -538,7 +538,7 @@ constexpr int kChunk = kCopyThreads * kCopyEach;
 
 // blockIdx.y: keys or values of a layer; blockIdx.x takes chunks in turn, of a large
 // block or (kMany) of several small ones: then every piece has a copy of its own to look
-// up (blocks of 2 KB 1062 us -> 238, of 8 KB 804 -> 436, of 12 KB 585 -> 456), which
+// up (blocks of 2 KB 1062 us -> 237, of 8 KB 804 -> 426, of 12 KB 585 -> 431), which
 // would cost a large block 3%.
 template <bool kMany>
 __global__ void __launch_bounds__(kCopyThreads) paged_copy_kernel(PagedCopyParams P) {
