@@ -20,7 +20,11 @@
 // scans, a dependent round for the tokens (32 requests x 8 tokens: 4.5 us back to
 // back, 8.5 with cold caches). For long prompts a thread places eight tokens, each
 // by a bisection and a dependent load (256 requests, room for 262 thousand tokens,
-// 4.2 MB of positions and slots: 9.6 us, 11.7 cold; the bytes alone are 0.6).
+// 4.2 MB of positions and slots: 9.6 us, 11.7 cold; the bytes alone are 0.6). Where
+// blocks are shared, a request's thread looks at two blocks, and warps at those of a length
+// that was lowered, two more dependent rounds of loads each: 32 requests x 8 tokens 4.1 us
+// for 3.6 without, 1024 x 8 9.1 for 7.5; one row lowered by 65536 blocks 24 us (a block after
+// the other 4575; every row by warps alone, 1024 x 8 38.8).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -36,6 +40,9 @@ namespace {
 // sums for little work, more would leave SMs idle in mid-sized steps.
 constexpr int kTokensPerCta = 2048;
 constexpr int kMaxB = DSPARK_MAX_PAGED_BATCH;
+// Where blocks are shared: those of a request that its thread looks at, and of a longer
+// one that a warp looks at in one go.
+constexpr int kFew = 2, kLook = 256;
 
 struct TablesSmem {
   unsigned long long warp[33];
@@ -47,8 +54,14 @@ struct TablesSmem {
   int take0[kMaxB];       // blocks taken by the requests before
   int after[kMaxB];       // blocks returned by the requests after
   int last;
+  int n_long;
 };
 
+__device__ __forceinline__ bool is_shared(const PagedTablesParams& P, int id) {
+  return id >= 0 && id < P.N && P.shares[id] > 0;
+}
+
+template <bool kShared>
 __global__ void __launch_bounds__(1024) paged_tables_kernel(PagedTablesParams P) {
   __shared__ TablesSmem sm;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -78,17 +91,53 @@ __global__ void __launch_bounds__(1024) paged_tables_kernel(PagedTablesParams P)
         cached = static_cast<int64_t>(c) + acc + 1;
         need = (cached + fresh + (1 << sh) - 1) >> sh;
         ok = acc >= -1 && c >= 0 && fresh >= 0 && held >= 0 && held <= M && need <= M;
-        // a block that other rows hold too is not this call's to put on the stack, nor
-        // new tokens' to write into
-        if (P.shares && ok)
-          for (int j = static_cast<int>(fresh > 0 ? cached >> sh : need); j < held; ++j) {
-            const int id = P.block_table[static_cast<int64_t>(slot) * M + j];
-            if (id >= 0 && id < N && P.shares[id] > 0) ok = false;
-          }
       }
-      if (!ok && first) report(P.status, DSPARK_ERR_BOUNDS);
     }
   }
+  if constexpr (kShared) {
+    // A block that other rows hold too is not this call's to put on the stack, nor new
+    // tokens' to write into. A step's are one or two; a length that was lowered leaves as
+    // many as the row holds, which the warps share out.
+    if (tid == 0) sm.n_long = 0;
+    __syncthreads();
+    bool listed = false;
+    if (ok) {
+      const int j0 = static_cast<int>(fresh > 0 ? cached >> sh : need);
+      const int32_t* row = P.block_table + static_cast<int64_t>(slot) * M;
+#pragma unroll
+      for (int u = 0; u < kFew; ++u)
+        if (j0 + u < held && is_shared(P, row[j0 + u])) ok = false;
+      listed = ok && j0 + kFew < held;
+      if (listed) {
+        const int i = atomicAdd(&sm.n_long, 1);
+        sm.take0[i] = tid;
+        sm.slot[tid] = slot;
+        sm.held[tid] = held;
+        sm.need[tid] = j0 + kFew;
+        sm.after[tid] = 0;  // one was found
+      }
+    }
+    __syncthreads();
+    const int n_long = sm.n_long, parts = n_long < nw ? nw / max(n_long, 1) : 1;
+    for (int w = warp; w < n_long * parts; w += nw) {
+      const int b = sm.take0[w / parts], end = sm.held[b];
+      const int32_t* row = P.block_table + static_cast<int64_t>(sm.slot[b]) * M;
+      bool found = false;
+      for (int j = sm.need[b] + w % parts * kLook; j < end && !found; j += parts * kLook) {
+        int id[kLook / 32];  // (all on their way before the first count is)
+#pragma unroll
+        for (int u = 0; u < kLook / 32; ++u)
+          id[u] = j + 32 * u + lane < end ? row[j + 32 * u + lane] : -1;
+#pragma unroll
+        for (int u = 0; u < kLook / 32; ++u) found |= is_shared(P, id[u]);
+        found = __any_sync(0xFFFFFFFFu, found);
+      }
+      if (found && lane == 0) sm.after[b] = 1;
+    }
+    __syncthreads();
+    if (listed && sm.after[tid]) ok = false;
+  }
+  if (tid < B && slot >= 0 && !ok && first) report(P.status, DSPARK_ERR_BOUNDS);
   unsigned long long total;
   const unsigned long long tcum = block_scan(ok ? fresh : 0, sm.warp, &total);
   if (ok && fresh != 0 && tcum > static_cast<unsigned long long>(T)) {
@@ -228,7 +277,8 @@ cudaError_t launch_paged_tables(const PagedTablesParams& p, cudaStream_t stream)
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_tables_kernel, p);
+  return cudaLaunchKernelEx(&cfg, p.shares ? paged_tables_kernel<true> : paged_tables_kernel<false>,
+                            p);
 }
 
 }  // namespace dspark
