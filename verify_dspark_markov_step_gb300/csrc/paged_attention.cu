@@ -1751,13 +1751,16 @@ cudaError_t launch_paged_attention(PagedAttentionParams p, cudaStream_t stream) 
   const dspark_paged_kv& kv = p.kv;
   // the most key tiles a unit can have
   int64_t keys = static_cast<int64_t>(p.M) << p.page_shift;
+  const int64_t table_tiles = (keys + kKeys - 1) / kKeys;
   if (p.window > 0) {
     // (without a causal mask a unit sees from its first token's window to the end)
     const int64_t tokens = p.causal ? 2 * (kRows / (p.Hq / kv.kv_heads)) : p.T;
     keys = min(keys, p.window + tokens);
   }
-  p.whole = (keys + kKeys - 1) / kKeys + (p.window > 0 ? 1 : 0) + (p.sinks + kKeys - 1) / kKeys <=
-            (3 * p.B * kv.kv_heads >= sms ? kWholeTiles : kWholeTilesFewUnits);
+  int64_t tiles = (keys + kKeys - 1) / kKeys + (p.window > 0 ? 1 : 0);
+  if (p.sinks > 0)  // (which may be more than the table's tokens)
+    tiles = min(tiles + (p.sinks + kKeys - 1) / kKeys, table_tiles);
+  p.whole = tiles <= (3 * p.B * kv.kv_heads >= sms ? kWholeTiles : kWholeTilesFewUnits);
   if (!make_map(&mk, kv.k, kv, kv.k_block_stride, kv.k_head_stride, kv.k_token_stride) ||
       !make_map(&mv, kv.v, kv, kv.v_block_stride, kv.v_head_stride, kv.v_token_stride))
     return cudaErrorInvalidValue;
