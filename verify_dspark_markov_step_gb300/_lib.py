@@ -685,24 +685,38 @@ def paged_compact(block_table, held_blocks, free_blocks, pool, copies, count, sh
 
 class PagedCaches:
     """The caches of some layers as paged_copy takes them: pairs (k_cache, v_cache) of one
-    shape, dtype and strides."""
+    shape, dtype and strides. Memory or layout that changes under the tensors (.data, set_) is
+    noticed by the next copy."""
 
     def __init__(self, caches):
         self.tensors = [(k, v) for k, v in caches]  # (kept alive)
-        self.array = (PagedKv * len(self.tensors))()
+        self._seen = None
+        self.look()
+
+    def look(self):
+        """Writes the array again unless the tensors are as it has them."""
+        now = [(t.data_ptr(), t.stride(), t.shape, t.dtype) for kv in self.tensors for t in kv]
+        if now == self._seen:
+            return
+        self._seen = None
+        array = (PagedKv * len(self.tensors))()
         for i, (k, v) in enumerate(self.tensors):
-            _pack_kv(self.array, i * ctypes.sizeof(PagedKv), k, v, None, None)
+            _pack_kv(array, i * ctypes.sizeof(PagedKv), k, v, None, None)
+        self.array, self._seen = array, now
 
 
 def paged_copy(caches, copies, count, status=None, stream=None):
     """dspark_paged_copy on torch tensors (see include/dspark.h): blocks copied in all
     caches, a list of pairs (k_cache, v_cache) or a PagedCaches of them, by the pairs
     (from, to) that paged_fork and paged_compact leave in copies [C, 2] and count [1]."""
-    if not isinstance(caches, PagedCaches):
+    if isinstance(caches, PagedCaches):
+        caches.look()
+    else:
         caches = PagedCaches(caches)
     i32 = torch.int32
+    copies_p = _of(copies, "copies", i32, (copies.shape[0], 2))
     code = (_lib or lib()).dspark_paged_copy(
-        caches.array, len(caches.tensors), _of(copies, "copies", i32, (copies.shape[0], 2)),
+        caches.array, len(caches.tensors), copies_p,
         _of(count, "count", i32, (1,)), copies.shape[0], _maybe(status, "status", i32),
         _stream_here(stream, copies, "copies"))
     if code:
