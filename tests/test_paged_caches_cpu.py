@@ -1,4 +1,5 @@
 """A list of caches for the copies, without a GPU: tensors that say they are on one."""
+import pytest
 import torch
 
 from verify_dspark_markov_step_gb300 import _lib
@@ -11,6 +12,10 @@ class There(torch.Tensor):
 
     def get_device(self):
         return self.device_index
+
+
+class Elsewhere(There):
+    device_index = 1
 
 
 def _cache(kind=There, blocks=4):
@@ -42,3 +47,22 @@ def test_a_list_notices_what_changes_under_its_tensors():
     caches.look()
     got = caches.array[0]
     assert (got.k_block_stride, got.k_head_stride, got.k_token_stride) == strides[:3]
+
+
+def test_caches_of_two_devices_are_refused():
+    with pytest.raises(ValueError, match="one device"):
+        _lib.PagedCaches([(_cache(), _cache()), (_cache(), _cache(Elsewhere))])
+    with pytest.raises(ValueError, match="one device"):
+        _lib.PagedCaches([(_cache(), _cache()), (_cache(Elsewhere), _cache(Elsewhere))])
+
+
+def test_copies_on_another_device_are_refused(monkeypatch):
+    monkeypatch.setattr(_lib, "_lib", object())  # (no call is made)
+    caches = [(_cache(), _cache())]
+    copies = torch.zeros(3, 2, dtype=torch.int32).as_subclass(Elsewhere)
+    count = torch.zeros(1, dtype=torch.int32).as_subclass(Elsewhere)
+    for c in (caches, _lib.PagedCaches(caches)):
+        with pytest.raises(ValueError, match="device"):
+            _lib.paged_copy(c, copies, count)
+    with pytest.raises(TypeError, match="CUDA"):
+        _lib.paged_copy(caches, torch.zeros(3, 2, dtype=torch.int32), count)

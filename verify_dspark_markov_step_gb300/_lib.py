@@ -685,8 +685,8 @@ def paged_compact(block_table, held_blocks, free_blocks, pool, copies, count, sh
 
 class PagedCaches:
     """The caches of some layers as paged_copy takes them: pairs (k_cache, v_cache) of one
-    shape, dtype and strides. Memory or layout that changes under the tensors (.data, set_) is
-    noticed by the next copy."""
+    shape, dtype and strides, on one device. Memory or layout that changes under the tensors
+    (.data, set_) is noticed by the next copy."""
 
     def __init__(self, caches):
         self.tensors = [(k, v) for k, v in caches]  # (kept alive)
@@ -702,7 +702,10 @@ class PagedCaches:
         array = (PagedKv * len(self.tensors))()
         for i, (k, v) in enumerate(self.tensors):
             _pack_kv(array, i * ctypes.sizeof(PagedKv), k, v, None, None)
-        self.array, self._seen = array, now
+        devices = {t.get_device() for kv in self.tensors for t in kv}
+        if len(devices) > 1:
+            raise ValueError("the caches must be on one device")
+        self.array, self.device, self._seen = array, next(iter(devices), None), now
 
 
 def paged_copy(caches, copies, count, status=None, stream=None):
@@ -715,6 +718,8 @@ def paged_copy(caches, copies, count, status=None, stream=None):
         caches = PagedCaches(caches)
     i32 = torch.int32
     copies_p = _of(copies, "copies", i32, (copies.shape[0], 2))
+    if caches.tensors and caches.device != copies.get_device():
+        raise ValueError("copies must be on the caches' device")
     code = (_lib or lib()).dspark_paged_copy(
         caches.array, len(caches.tensors), copies_p,
         _of(count, "count", i32, (1,)), copies.shape[0], _maybe(status, "status", i32),
