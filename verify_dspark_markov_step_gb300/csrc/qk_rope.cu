@@ -5,8 +5,9 @@
 // Mathematics. A head's row x of D values: y = x w / sqrt(mean x^2 + eps), then the
 // pair (a, b) of frequency i becomes m (a cos t - b sin t, b cos t + a sin t), where
 // t = position * 2 pi * turns_i / 2^64. turns_i is a 64-bit integer, so position *
-// turns_i modulo 2^64 is the angle modulo a whole turn, exactly, at any position: no
-// table over the positions, and no loss where a 32-bit angle has lost its fraction.
+// turns_i modulo 2^64 is that angle modulo a whole turn, exactly: no table over the
+// positions, and no loss where a 32-bit angle has lost its fraction. (turns_i itself is
+// rounded: position * 2^-65 turns.)
 // The upper 32 bits give the nearest quarter turn and a rest of at most pi / 4, for
 // which the series of sine and cosine to the ninth and eighth power are exact to
 // 2^-25. All of this is fp32; a value is rounded once, to the type it is stored in.

@@ -2,8 +2,11 @@
 
 ``frequencies`` gives the radians a position of each pair of values, for the plain
 form and for the usual scalings of a trained model to longer contexts; ``Rotary``
-holds them on the device in the library's form, 64-bit fractions of a turn, with which
-the angle of any position is exact.
+holds them on the device in the library's form, 64-bit fractions of a turn. The product
+of a position and such a fraction is exact modulo a turn; what the angle is off by is the
+frequency's own rounding: position * 2^-65 turns from the fraction (2^-25 of a turn at
+position 2^40), and position times the rounding of the double that it is made from (a
+relative 2^-50 at most: 2^-10 radians at one radian a position and position 2^40).
 """
 from __future__ import annotations
 
