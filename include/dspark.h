@@ -550,7 +550,8 @@ dspark_status dspark_kv_append(const void* k, const void* v, dspark_dtype dtype,
  * Arguments
  *   q, q_out      [T, q_heads, head_dim] dtype, tokens q_stride / q_out_stride
  *                 elements apart (the heads of a token are contiguous). q_out is
- *                 q itself with the same stride (in place), or apart from it.
+ *                 q itself with the same stride (in place), or apart from it: other
+ *                 rows of the same stride, or other memory. Its rows do not overlap.
  *   k, k_out      [T, kv_heads, head_dim], the same; kv_heads = 0: no keys
  *   dtype         DSPARK_BF16 or DSPARK_F16
  *   positions     [T] int64

@@ -77,3 +77,21 @@ def test_queries_beside_the_pages(T, Hq, H, D, P, cache, scaled):
     assert all(torch.equal(a, b) for a, b in zip(*made))
     before[:, D:D + Hq * D] = q_out.flatten(1)
     assert torch.equal(x, before)
+
+
+def test_rows_interleaved_with_those_that_are_read():
+    """Rows of a wider buffer into others of it: apart, though the memory ranges meet."""
+    from verify_dspark_markov_step_gb300 import _lib, qk_rope
+    g = torch.Generator("cuda").manual_seed(3)
+    x = torch.randn(50, 6, 64, device="cuda", generator=g).half()
+    before, pos, rot = x.clone(), torch.arange(50, device="cuda"), Rotary(64)
+    want = x[:, :3].contiguous()
+    qk_rope(want, None, pos, **rot.args())
+    qk_rope(x[:, :3], None, pos, q_out=x[:, 3:], **rot.args())
+    torch.cuda.synchronize()
+    assert torch.equal(x[:, 3:], want) and torch.equal(x[:, :3], before[:, :3])
+    for q, out in ((x[:, :3], x[:, 2:5]), (x[:, 1:4], x[:, :3]), (x[:25, :3], x.view(25, 12, 64)[:, 5:8]),
+                   (x[:, :3], x.as_strided((50, 3, 64), (128, 64, 1)))):
+        with pytest.raises(_lib.DsparkError):
+            qk_rope(q, None, pos[:q.shape[0]], q_out=out, **rot.args())
+    assert torch.equal(x[:, :3], before[:, :3])

@@ -55,9 +55,22 @@ dspark_status check_cache(const dspark_paged_kv* c, int dtype) {
   return DSPARK_OK;
 }
 
-// Rows written where they are read from lie as they do there.
-bool in_place_ok(const void* in, const void* out, int64_t in_stride, int64_t out_stride, int T) {
-  return in != out || in_stride == out_stride || T < 2;
+// Whether T rows of `row` 16-bit values may be written: they do not overlap, and lie where
+// they are read from (as there) or apart from it. Rows of the same stride may be
+// interleaved with those that are read; of another stride, the ranges do not meet.
+bool rows_out_ok(const void* in, const void* out, int64_t in_stride, int64_t out_stride,
+                 int64_t row, int T) {
+  if (T > 1 && out_stride < row) return false;
+  if (in == out) return in_stride == out_stride || T < 2;
+  const __int128 a = reinterpret_cast<intptr_t>(in), b = reinterpret_cast<intptr_t>(out);
+  const __int128 a_end = a + (static_cast<__int128>(T - 1) * in_stride + row) * 2;
+  const __int128 b_end = b + (static_cast<__int128>(T - 1) * out_stride + row) * 2;
+  if (a_end <= b || b_end <= a) return true;
+  if (in_stride != out_stride || T < 2) return false;
+  const int64_t step = in_stride * 2;
+  int64_t off = static_cast<int64_t>((b - a) % step);
+  if (off < 0) off += step;
+  return off >= 2 * row && step - off >= 2 * row;
 }
 
 // The checks both rotating calls make of the rotation and the norms.
@@ -351,14 +364,14 @@ dspark_status dspark_qk_rope(const void* q, void* q_out, const void* k, void* k_
   if (bad != DSPARK_OK || T == 0) return bad;
   const bool keys = kv_heads > 0;
   if (!q || !q_out || !positions || (keys && (!k || !k_out))) return DSPARK_ERR_INVALID_ARG;
-  if (!in_place_ok(q, q_out, q_stride, q_out_stride, T) ||
-      (keys && !in_place_ok(k, k_out, k_stride, k_out_stride, T)))
-    return DSPARK_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(q_out) || !stride_ok(q_stride, 2) || !stride_ok(q_out_stride, 2))
     return DSPARK_ERR_ALIGNMENT;
   if (keys && (!aligned16(k) || !aligned16(k_out) || !stride_ok(k_stride, 2) ||
                !stride_ok(k_out_stride, 2)))
     return DSPARK_ERR_ALIGNMENT;
+  if (!rows_out_ok(q, q_out, q_stride, q_out_stride, int64_t(q_heads) * head_dim, T) ||
+      (keys && !rows_out_ok(k, k_out, k_stride, k_out_stride, int64_t(kv_heads) * head_dim, T)))
+    return DSPARK_ERR_INVALID_ARG;
   dspark::QkRopeParams p = rotation_params(positions, turns, factor, rotary_dim, interleaved,
                                            q_weight, keys ? k_weight : nullptr, eps, head_dim);
   p.src[0] = q;
@@ -393,11 +406,12 @@ dspark_status dspark_qk_rope_append(const void* q, void* q_out, const void* k, c
                          cache->head_dim);
   if (bad != DSPARK_OK || T == 0) return bad;
   if (!q || !q_out || !k || !v || !positions || !slot_map) return DSPARK_ERR_INVALID_ARG;
-  if (!in_place_ok(q, q_out, q_stride, q_out_stride, T)) return DSPARK_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(v) ||
       !stride_ok(q_stride, 2) || !stride_ok(q_out_stride, 2) || !stride_ok(k_stride, 2) ||
       !stride_ok(v_stride, 2))
     return DSPARK_ERR_ALIGNMENT;
+  if (!rows_out_ok(q, q_out, q_stride, q_out_stride, int64_t(q_heads) * cache->head_dim, T))
+    return DSPARK_ERR_INVALID_ARG;
   dspark::QkRopeParams p = rotation_params(positions, turns, factor, rotary_dim, interleaved,
                                            q_weight, k_weight, eps, cache->head_dim);
   p.src[0] = q;
