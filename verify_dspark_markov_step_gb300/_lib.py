@@ -249,6 +249,13 @@ def workspace(nbytes: int, device=None) -> torch.Tensor:
     return torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=device or "cuda")
 
 
+def _scratch(t):
+    """Address and size of a workspace, which has to be the GPU's memory."""
+    if not t.is_cuda:
+        raise TypeError("workspace_buf must be a CUDA tensor")
+    return t.data_ptr(), t.nbytes
+
+
 def markov_sample(base_logits, markov_w1, markov_w2, anchor_tokens, req_state_idx,
                   positions, temperature, seeds, out_tokens, cache=None,
                   cache_row_map=None, workspace_buf=None, status=None, stream=None,
@@ -289,8 +296,8 @@ def markov_sample(base_logits, markov_w1, markov_w2, anchor_tokens, req_state_id
         _ptr(base_logits), _logit_dtype(base_logits, "base_logits"), _ptr(markov_w1),
         _ptr(markov_w2), _ptr(anchor_tokens), _ptr(req_state_idx), _ptr(positions),
         _ptr(temperature), _ptr(seeds), _ptr(cache), cache_dt, _ptr(cache_row_map),
-        _ptr(out_tokens), _ptr(draft_stats), B, K, V, R, S, max(C, 1), _ptr(workspace_buf),
-        workspace_buf.numel() * workspace_buf.element_size(), _ptr(status), _stream(stream))
+        _ptr(out_tokens), _ptr(draft_stats), B, K, V, R, S, max(C, 1), *_scratch(workspace_buf),
+        _ptr(status), _stream(stream))
     _check(code, "dspark_markov_sample")
 
 
@@ -321,8 +328,8 @@ def markov_sample_wait_limit(base_logits, markov_w1, markov_w2, anchor_tokens, r
         _ptr(base_logits), _logit_dtype(base_logits, "base_logits"), _ptr(markov_w1),
         _ptr(markov_w2), _ptr(anchor_tokens), _ptr(req_state_idx), _ptr(positions),
         _ptr(temperature), _ptr(seeds), _ptr(cache), cache_dt, _ptr(cache_row_map),
-        _ptr(out_tokens), B, K, V, R, S, max(C, 1), _ptr(workspace_buf),
-        workspace_buf.numel() * workspace_buf.element_size(), _ptr(status), _stream(stream),
+        _ptr(out_tokens), B, K, V, R, S, max(C, 1), *_scratch(workspace_buf),
+        _ptr(status), _stream(stream),
         int(wait_limit_ns), int(barrier_extra))
     _check(code, "dspark_testing_markov_wait_limit")
 
@@ -416,8 +423,8 @@ def markov_sample_topk(base_logits, markov_w1, markov_w2, anchor_tokens, req_sta
         _ptr(base_logits), _logit_dtype(base_logits, "base_logits"), _ptr(markov_w1),
         _ptr(markov_w2), _ptr(anchor_tokens), _ptr(req_state_idx), _ptr(positions),
         _ptr(temperature), _ptr(seeds), _ptr(cache), cache_dt, _ptr(cache_row_map),
-        _ptr(out_tokens), int(topk), B, K, V, R, S, max(C, 1), _ptr(workspace_buf),
-        workspace_buf.numel() * workspace_buf.element_size(), _ptr(status), _stream(stream))
+        _ptr(out_tokens), int(topk), B, K, V, R, S, max(C, 1), *_scratch(workspace_buf),
+        _ptr(status), _stream(stream))
     _check(code, "dspark_markov_sample_topk")
 
 
@@ -462,8 +469,8 @@ def rejection_sample(draft_tokens, draft_cache, target_logits, req_state_idx, po
         _ptr(draft_tokens), _ptr(draft_cache), cache_dt, _ptr(cache_row_map), _ptr(draft_stats),
         _ptr(target_logits), _logit_dtype(target_logits, "target_logits"),
         _ptr(req_state_idx), _ptr(positions), _ptr(temperature), _ptr(top_p), _ptr(seeds),
-        _ptr(out_tokens), _ptr(num_accepted), B, K, V, S, max(C, 1), _ptr(workspace_buf),
-        workspace_buf.numel() * workspace_buf.element_size(), _ptr(status), _stream(stream))
+        _ptr(out_tokens), _ptr(num_accepted), B, K, V, S, max(C, 1), *_scratch(workspace_buf),
+        _ptr(status), _stream(stream))
     _check(code, "dspark_rejection_sample")
 
 
@@ -676,8 +683,8 @@ def paged_compact(block_table, held_blocks, free_blocks, pool, copies, count, sh
             workspace_buf = workspace(paged_compact_workspace_bytes(N), block_table.device)
     code = (_lib or lib()).dspark_paged_compact(
         table, held, free, pool_p, shares_p, _of(copies, "copies", i32, (copies.shape[0], 2)),
-        _of(count, "count", i32, (1,)), S, M, N, copies.shape[0], workspace_buf.data_ptr(),
-        workspace_buf.nbytes, _maybe(status, "status", i32),
+        _of(count, "count", i32, (1,)), S, M, N, copies.shape[0], *_scratch(workspace_buf),
+        _maybe(status, "status", i32),
         _stream_here(stream, block_table, "block_table"))
     if code:
         _check(code, "dspark_paged_compact")
@@ -862,7 +869,7 @@ def paged_attention(q, k_cache, v_cache, block_table, req_state_idx, query_start
         _of(query_start, "query_start", i32, (B + 1,)), _of(seq_lens, "seq_lens", i32, (B,)),
         _of(out, "out", q.dtype, q.shape), _maybe(lse, "lse", torch.float32, (T, Hq)),
         D ** -0.5 if scale is None else scale, bool(causal), window, sinks, Hq, B, S, M, T,
-        workspace_buf.data_ptr(), workspace_buf.nbytes, _maybe(status, "status", i32),
+        *_scratch(workspace_buf), _maybe(status, "status", i32),
         _raw_stream(stream, q))
     if code:
         _check(code, "dspark_paged_attention")
