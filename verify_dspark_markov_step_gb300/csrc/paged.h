@@ -10,6 +10,14 @@
 
 namespace dspark {
 
+// SMs of the current device.
+inline cudaError_t sm_count(int* sms) {
+  int dev = 0;
+  const cudaError_t err = cudaGetDevice(&dev);
+  return err != cudaSuccess ? err
+                            : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+}
+
 // Block tables and slot map of a step (paged_tables.cu).
 struct PagedTablesParams {
   const int32_t* rsi;

@@ -1742,10 +1742,8 @@ size_t paged_attention_workspace_bytes(int B, int Hq, int Hkv, int D) {
 }
 
 cudaError_t launch_paged_attention(PagedAttentionParams p, cudaStream_t stream) {
-  int dev = 0, sms = 0;
-  cudaError_t err = cudaGetDevice(&dev);
-  if (err == cudaSuccess)
-    err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  int sms = 0;
+  const cudaError_t err = sm_count(&sms);
   if (err != cudaSuccess) return err;
   CUtensorMap mq = {}, mk, mv;
   const dspark_paged_kv& kv = p.kv;

@@ -648,8 +648,13 @@ cudaError_t launch_paged_compact(const PagedCompactParams& p, cudaStream_t strea
 }
 
 cudaError_t launch_paged_copy(const PagedCopyParams& p, cudaStream_t stream) {
-  // eight CTAs an SM over all layers, keys and values
-  int ctas = (152 * 8 + 2 * p.caches - 1) / (2 * p.caches);
+  // Eight CTAs an SM over all layers, keys and values: four waves of the two that are
+  // resident at a time (86 registers a thread), since one wave of them, persistent, took
+  // 430 us for 413: the dies' halves are not equally fast, and chunks are dealt beforehand.
+  int sms = 0;
+  const cudaError_t err = sm_count(&sms);
+  if (err != cudaSuccess) return err;
+  const int ctas = (sms * 8 + 2 * p.caches - 1) / (2 * p.caches);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas, 2 * p.caches);
   cfg.blockDim = dim3(kCopyThreads);

@@ -40,7 +40,7 @@ namespace dspark {
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 128, kCtas = 5;  // of an SM
 // From so many tokens on a warp takes the rounds of several, and a round has place for
 // several tokens' heads, which spares starts (16384 tokens, single and several: 16/2 heads
 // of 128 43.5 and 37.5 us, 2/2 33.9 and 16.6, one of 64 30.6 and 9.6, 64/8 of 128 104.0 and
@@ -468,7 +468,7 @@ __device__ __forceinline__ void rounds(const QkRopeParams& P, int width, const K
 // have a norm. kMulti: several tokens a warp. The CTAs' kinds of rows are apart, so that
 // one's warps end together.
 template <Form kForm, bool kF16, bool kSplit, bool kNorm, bool kMulti>
-__global__ void __launch_bounds__(kThreads, 5)
+__global__ void __launch_bounds__(kThreads, kCtas)
 qk_rope_kernel(const __grid_constant__ QkRopeParams P, const __grid_constant__ Split split) {
   __shared__ uint4 ring[kStages][2][kThreads];
   __shared__ __align__(16) float2 angles[kThreads / 32][256];  // 8 for each lane
@@ -485,13 +485,17 @@ qk_rope_kernel(const __grid_constant__ QkRopeParams P, const __grid_constant__ S
 
 template <Form kForm, bool kF16, bool kSplit, bool kNorm, bool kMulti>
 cudaError_t launch(const QkRopeParams& p, cudaStream_t stream) {
+  int sms = 0;
+  const cudaError_t err = sm_count(&sms);
+  if (err != cudaSuccess) return err;
   Split split;
   split.width = 1;
   while (16 * split.width < p.D) split.width *= 2;
   const int abreast = 32 / split.width;
   // Warps that are resident at a time (as many rounds a warp as there are for each of
   // them), and the most rounds a warp takes of more than one token.
-  constexpr int kWarps = 152 * 20, kMost = 6, kPerCta = kThreads / 32;
+  constexpr int kMost = 6, kPerCta = kThreads / 32;
+  const int resident = sms * kCtas * kPerCta;
   const int heads[3] = {p.Hq, p.H, kForm == kRows ? 0 : p.H};
   int64_t total = 0;
   for (int what = 0; what < 3; ++what) {
@@ -503,7 +507,7 @@ cudaError_t launch(const QkRopeParams& p, cudaStream_t stream) {
     of.groups = of.rounds ? (p.T + tokens - 1) / tokens : 0;
     total += static_cast<int64_t>(of.groups) * of.rounds;
   }
-  const int64_t per = (total + kWarps - 1) / kWarps;
+  const int64_t per = (total + resident - 1) / resident;
   unsigned ctas = 0;
   for (Kind& of : split.of) {
     of.parts = of.tokens = 1;
