@@ -690,6 +690,17 @@ def paged_compact(block_table, held_blocks, free_blocks, pool, copies, count, sh
         _check(code, "dspark_paged_compact")
 
 
+def _caches_of(pairs):
+    """The dspark_paged_kv of each pair of caches, in an array, and their device."""
+    array = (PagedKv * len(pairs))()
+    for i, (k, v) in enumerate(pairs):
+        _pack_kv(array, i * ctypes.sizeof(PagedKv), k, v, None, None)
+    devices = {t.get_device() for kv in pairs for t in kv}
+    if len(devices) > 1:
+        raise ValueError("the caches must be on one device")
+    return array, next(iter(devices), None)
+
+
 class PagedCaches:
     """The caches of some layers as paged_copy takes them: pairs (k_cache, v_cache) of one
     shape, dtype and strides, on one device. Memory or layout that changes under the tensors
@@ -703,16 +714,10 @@ class PagedCaches:
     def look(self):
         """Writes the array again unless the tensors are as it has them."""
         now = [(t.data_ptr(), t.stride(), t.shape, t.dtype) for kv in self.tensors for t in kv]
-        if now == self._seen:
-            return
-        self._seen = None
-        array = (PagedKv * len(self.tensors))()
-        for i, (k, v) in enumerate(self.tensors):
-            _pack_kv(array, i * ctypes.sizeof(PagedKv), k, v, None, None)
-        devices = {t.get_device() for kv in self.tensors for t in kv}
-        if len(devices) > 1:
-            raise ValueError("the caches must be on one device")
-        self.array, self.device, self._seen = array, next(iter(devices), None), now
+        if now != self._seen:
+            self._seen = None
+            self.array, self.device = _caches_of(self.tensors)
+            self._seen = now
 
 
 def paged_copy(caches, copies, count, status=None, stream=None):
@@ -721,15 +726,17 @@ def paged_copy(caches, copies, count, status=None, stream=None):
     (from, to) that paged_fork and paged_compact leave in copies [C, 2] and count [1]."""
     if isinstance(caches, PagedCaches):
         caches.look()
+        array, device = caches.array, caches.device
     else:
-        caches = PagedCaches(caches)
+        caches = list(caches)
+        array, device = _caches_of(caches)
     i32 = torch.int32
     copies_p = _of(copies, "copies", i32, (copies.shape[0], 2))
-    if caches.tensors and caches.device != copies.get_device():
+    if len(array) and device != copies.get_device():
         raise ValueError("copies must be on the caches' device")
     code = (_lib or lib()).dspark_paged_copy(
-        caches.array, len(caches.tensors), copies_p,
-        _of(count, "count", i32, (1,)), copies.shape[0], _maybe(status, "status", i32),
+        array, len(array), copies_p, _of(count, "count", i32, (1,)), copies.shape[0],
+        _maybe(status, "status", i32),
         _stream_here(stream, copies, "copies"))
     if code:
         _check(code, "dspark_paged_copy")
