@@ -455,14 +455,15 @@ dspark_status dspark_paged_tables(
  *   copies[0 .. count[0]) are the pairs (old number, new number), and the table
  *   entries of all slots and shares follow. free_blocks[i] = N - 1 - i for i < N - U.
  *   The blocks' contents are moved by dspark_paged_copy, on the same stream before
- *   anything that reads them; slot maps made before are void. A table entry within held_blocks that is out of range or
- *   on the stack stays as it is, with DSPARK_ERR_BOUNDS.
+ *   anything that reads them; slot maps made before are void. A table entry within
+ *   held_blocks that is out of range or on the stack stays as it is, with
+ *   DSPARK_ERR_BOUNDS.
  *
  * dspark_paged_copy -- blocks copied in the caches of all layers.
  *   For i < count[0]: block copies[i][1] of each of the n_caches caches becomes a copy
- *   of block copies[i][0], keys and values. No block is both read and written, and of
- *   two copies into one either may win. A block out of range is skipped, a count past
- *   max_copies cut off, with DSPARK_ERR_BOUNDS.
+ *   of block copies[i][0], keys and values. No block is both read and written, and
+ *   two copies into one may leave some of each. A block out of range is skipped, a count
+ *   past max_copies cut off, with DSPARK_ERR_BOUNDS.
  *
  * Arguments (others as for dspark_paged_tables)
  *   src, dst, slots  [n] int32, n in [0, 1024]
@@ -524,7 +525,7 @@ dspark_status dspark_paged_copy(const dspark_paged_kv* caches, int n_caches,
  *   k, v          [T, kv_heads, head_dim] dtype, tokens k_stride / v_stride
  *                 elements apart (the heads of a token are contiguous)
  *   dtype         DSPARK_BF16 or DSPARK_F16, the cache's unless that is 8-bit
- *   slot_map      [T] int64; of two tokens with one slot either may win
+ *   slot_map      [T] int64; two tokens with one slot may leave some of each
  *   T in [0, 2^30).
  * Alignment: k, v, the caches and all strides (in bytes): 16.
  * ------------------------------------------------------------------------ */
@@ -577,7 +578,7 @@ dspark_status dspark_kv_append(const void* k, const void* v, dspark_dtype dtype,
  * scale and rounded once. A slot past the cache is skipped, with DSPARK_ERR_BOUNDS.
  *   v             [T, kv_heads, head_dim] dtype, tokens v_stride elements apart
  *   cache         head_dim 64 or 128 and kv_heads are its
- *   slot_map      [T] int64; of two tokens with one slot either may win
+ *   slot_map      [T] int64; two tokens with one slot may leave some of each
  * Alignment: the caches and their strides, too.
  * ------------------------------------------------------------------------ */
 dspark_status dspark_qk_rope(const void* q, void* q_out, const void* k,

@@ -7,7 +7,9 @@
 // the first), and whether a block comes free is only known once every row of the call
 // has given it up; and compaction renumbers all blocks. Both are a few phases over
 // the same data with a barrier between them: one launch of one cluster of CTAs (a
-// single CTA where there is little to do), whose barrier is the hardware's.
+// single CTA where there is little to do), whose barrier is the hardware's. A fork has
+// no such phases, only lengths and pool that are written once every CTA has read them;
+// it uses the same cluster, and so eight SMs.
 //
 // Which row puts a shared block on the stack must not depend on timing: after all
 // rows of the call have taken their share off the count, each of a block that came
@@ -538,8 +540,9 @@ constexpr int kChunk = kCopyThreads * kCopyEach;
 
 // blockIdx.y: keys or values of a layer; blockIdx.x takes chunks in turn, of a large
 // block or (kMany) of several small ones: then every piece has a copy of its own to look
-// up (blocks of 2 KB 1062 us -> 237, of 8 KB 804 -> 426, of 12 KB 585 -> 431), which
-// would cost a large block 3%.
+// up, which would cost a large block 3%. A chunk of one and of several, two layers: blocks
+// of 2 KB (0.98 GB read and written) 761 and 168 us, of 8 KB (1.97 GB) 583 and 300, of 12 KB
+// (2.95 GB) 632 and 453, of 16 KB (2.62 GB) 474 and 396; of 32 KB either 384.
 template <bool kMany>
 __global__ void __launch_bounds__(kCopyThreads) paged_copy_kernel(PagedCopyParams P) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -25,9 +25,12 @@
 // Bound and measured. Prompts: memory; 16384 tokens, 32/8 heads of 128 in fp16, rows to
 // rows: 51.5 us, 6.5 TB/s (96% of a copy; with rows one round ahead in registers 68);
 // 64/8 heads with norms into a bf16 cache 102 us, 6.6 TB/s, into an e4m3 cache 103.5 us,
-// 6.2 TB/s, instruction issue beside it (with kinds of rows mixed in a warp 115). With few
-// heads the angles, once a token whatever its heads, and the start of a warp: 8/1 heads
-// 26 us where the bytes take 12. A decode step: latency; 256 tokens 3.9 to 4.3 us, one 2.3.
+// 6.2 TB/s, instruction issue beside it (with kinds of rows mixed in a warp 115), into a
+// bf16 cache with scales 113 us, 5.9 TB/s (16 divisions a lane; its long-batch kernels spill
+// 4 to 16 bytes); in place 1 to 2% slower than into other rows. With few heads the angles,
+// twice a token whatever its heads (queries and keys are in different CTAs), and the start
+// of a warp: 8/1 heads 25 us where the bytes take 12. A decode step: latency; 256 tokens 3.9
+// to 4.3 us, one 2.3.
 // (Five CTAs an SM; six spill registers: 256 tokens 5.2 us, 1500 13.7 for 12.5.)
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -45,7 +48,11 @@ constexpr int kThreads = 128, kCtas = 5;  // of an SM
 // several tokens' heads, which spares starts (16384 tokens, single and several: 16/2 heads
 // of 128 43.5 and 37.5 us, 2/2 33.9 and 16.6, one of 64 30.6 and 9.6, 64/8 of 128 104.0 and
 // 102.3); with fewer they only make warps longer (8192 tokens, 16/2: 23.3 both; 4000: 12.9
-// and 16.3; 1500 of 64/8 11.7 and 15.2).
+// and 16.3; 1500 of 64/8 11.7 and 15.2). That holds for many heads. With few of them the
+// crossing lies lower, as 8191 (single) and 8192 (several) show: 1/1 heads of 64 16.7 and
+// 6.3 us, 2/2 of 128 17.8 and 12.0, 8/1 21.4 and 18.2, 16/2 24.8 and 22.6, 64/8 54.1 and
+// 52.6. What decides is how many of a round's lanes a token leaves free and the rounds in
+// all; the rule does not look at them.
 constexpr int kManyTokens = 8192;
 constexpr int kStages = 4;  // rounds of rows on their way to a lane, and the one it works on
 
