@@ -66,3 +66,39 @@ def test_copies_on_another_device_are_refused(monkeypatch):
             _lib.paged_copy(c, copies, count)
     with pytest.raises(TypeError, match="CUDA"):
         _lib.paged_copy(caches, torch.zeros(3, 2, dtype=torch.int32), count)
+
+
+def test_a_paged_cache_keeps_no_replaced_tensor(monkeypatch):
+    """Caches that are replaced, added or given up are the ones copied, and their memory goes."""
+    import types
+    import weakref
+
+    from verify_dspark_markov_step_gb300.paged import PagedCache
+    cache = PagedCache(layers=2, slots=3, max_len=64, num_blocks=4, page_size=16, q_heads=2, kv_heads=2, head_dim=64,
+                       dtype=torch.float16, device="cpu")
+    cache.k, cache.v = ([_cache() for _ in range(2)] for _ in range(2))
+    cache.copies, cache.copied = (t.as_subclass(There) for t in (cache.copies, cache.copied))
+    cache.status = cache.status.as_subclass(There)
+    seen = []
+
+    def copy(array, n, *a):
+        seen.append([(kv.k, kv.v) for kv in array[:n]])
+        return 0
+    monkeypatch.setattr(_lib, "_lib", types.SimpleNamespace(dspark_paged_copy=copy))
+    monkeypatch.setattr(_lib, "_stream_here", lambda *a: 0)
+    monkeypatch.setattr(_lib, "paged_fork", lambda *a, **kw: None)
+
+    def now():
+        return [(k.data_ptr(), v.data_ptr()) for k, v in zip(cache.k, cache.v)]
+    slots = torch.zeros(1, dtype=torch.int32)
+    cache.fork(slots, slots)
+    assert seen[-1] == now()
+    gone = weakref.ref(cache.k[1])
+    cache.k[1] = _cache()
+    assert gone() is None
+    cache.k.append(_cache()), cache.v.append(_cache())
+    cache.fork(slots, slots)
+    assert seen[-1] == now() and len(seen[-1]) == 3
+    gone = [weakref.ref(t) for t in cache.k]
+    cache.k, cache.v = [], []
+    assert not any(g() is not None for g in gone)

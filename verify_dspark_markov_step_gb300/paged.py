@@ -49,7 +49,7 @@ class PagedCache:
         self.status = ints((1,))
         self.shares = ints((num_blocks,)) if sharing else None
         self.copies, self.copied = ints((num_blocks, 2)), ints((1,))
-        self._caches = self._compacting = None
+        self._caches, self._compacting = _lib.PagedCaches(()), None
         self._dims = (q_heads, kv_heads, head_dim)
         self._made = {}  # buffers of plans, by the power of two that holds their tokens
         self._last = None, None
@@ -155,10 +155,11 @@ class PagedCache:
 
     def _copy(self, stream):
         kept = self._caches
-        if kept is None or len(kept.tensors) != len(self.k) or any(
-                a is not k or b is not v for (a, b), k, v in zip(kept.tensors, self.k, self.v)):
-            kept = self._caches = _lib.PagedCaches(zip(self.k, self.v))
-        _lib.paged_copy(kept, self.copies, self.copied, status=self.status, stream=stream)
+        kept.tensors = list(zip(self.k, self.v))
+        try:
+            _lib.paged_copy(kept, self.copies, self.copied, status=self.status, stream=stream)
+        finally:
+            kept.tensors = []  # (caches that are replaced are not kept alive)
 
     def status_code(self) -> int:
         return int(self.status.item())
